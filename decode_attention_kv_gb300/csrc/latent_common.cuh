@@ -1,0 +1,187 @@
+// latent_common.cuh -- what the latent-cache kernels share: the arguments of a
+// call, the sequence checks, and the division of ragged sequences over a grid.
+//
+// Division of kvd_attend_latent.  The host knows the sizes but not the
+// lengths, so every CTA derives its share on the device: the key tiles of all
+// sequences form one line, cut into W equal runs, and worker w takes the tiles
+// [w * tot / W, (w + 1) * tot / W), whichever sequences they belong to.  Only
+// the first and the last sequence of a run can be shared with other workers,
+// so a worker leaves at most two partial results (slots 2w and 2w + 1) and
+// every other sequence of its run goes straight to the output.  A grid of one
+// CTA per SM is then balanced to one tile, whatever the lengths are.
+#pragma once
+
+#include "kvd_device.cuh"
+
+namespace kvd {
+
+constexpr int kLatentSMs = 152;  // SMs of a GB300: the workers of one call
+
+struct LatentArgs {
+    const void* q_latent;   // [Q, T, H, R]
+    const void* q_rope;     // [Q, T, H, P]
+    const void* latent;     // [NB, BS, R]
+    const void* rope;       // [NB, BS, P]
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    const int32_t* seq_offset;
+    void* out;              // [Q, T, H, R]
+    float* lse_out;         // [Q, T, H] or null
+    int32_t* dev_status;
+    int Q, T, H, NB, BS, cols, R, P;
+    float qscale;           // scale * log2(e)
+    int rows;               // T * H query rows of a sequence
+    int groups, rpg;        // row groups of a sequence, rows per group
+    int workers;            // W at most (the grid's x extent)
+    int min_tiles;          // fewest tiles worth a worker of its own
+    int4* meta;             // [Q] first worker, last worker, first slot's parity
+    float* part_lse;        // [workers * groups * 2, rpg], log2 units
+    float* part_o;          // [workers * groups * 2, rpg, R], normalised
+};
+
+// A sequence's keys: count (0 if the sequence is refused), first table column.
+struct SeqInfo {
+    int n;
+    int col0;
+    uint32_t bad;
+};
+
+__device__ __forceinline__ SeqInfo latent_seq(const LatentArgs& a, int b) {
+    SeqInfo s{0, 0, 0u};
+    const int s0 = a.seq_lens[b], s1 = a.seq_lens[b + 1];
+    const int off = a.seq_offset ? a.seq_offset[b] : 0;
+    if ((b == 0 && s0 != 0) || s0 < 0 || s1 < s0) s.bad |= KVD_DEV_SEQLENS;
+    if (off < 0 || off % a.BS) s.bad |= KVD_DEV_SEQ_OFFSET;
+    if (s.bad) return s;
+    const int n = s1 - s0;
+    if ((long long)off / a.BS + ((long long)n + a.BS - 1) / a.BS > a.cols) {
+        s.bad |= KVD_DEV_TABLE_COLS;
+        return s;
+    }
+    s.n = n;
+    s.col0 = off / a.BS;
+    return s;
+}
+
+// Finds, with the whole block, the item of `target` in a line of items with
+// count(b) places each (b < Q): item, the places before it, and the total.
+// Every thread gets the result; item = Q if target is behind the line.
+// `scratch`: kFindWords ints of shared memory.
+constexpr int kFindWords = 40;
+struct Found {
+    int item;
+    int before;
+    int total;
+};
+
+template <int THREADS, typename Total, typename Count>
+__device__ __forceinline__ Found block_find(int Q, int* scratch, Total target_of, Count count) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (Q + THREADS - 1) / THREADS;
+    const int lo = min(tid * per, Q), hi = min(lo + per, Q);
+    int sum = 0;
+    for (int b = lo; b < hi; ++b) sum += count(b);
+    int inc = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    if (tid == 0) scratch[32] = Q;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        const int s = scratch[i];
+        if (i < warp) before += s;
+        total += s;
+    }
+    before += inc - sum;
+    const int target = target_of(total);
+    if (target >= before && target < before + sum) {
+        int b = lo, at = before;
+        while (b < hi) {
+            const int c = count(b);
+            if (target < at + c) break;
+            at += c;
+            ++b;
+        }
+        scratch[32] = b;
+        scratch[33] = at;
+    }
+    __syncthreads();
+    Found f{scratch[32], scratch[33], total};
+    __syncthreads();
+    return f;
+}
+
+// Worker w's run [t0, t1) of `tot` tiles over `W` workers, and its inverse.
+__device__ __forceinline__ int run_start(int w, int tot, int W) {
+    return (int)((long long)w * tot / W);
+}
+__device__ __forceinline__ int worker_of(int tile, int tot, int W) {
+    return (int)((((long long)tile + 1) * W - 1) / tot);
+}
+__device__ __forceinline__ int used_workers(const LatentArgs& a, int tot) {
+    return max(1, min(a.workers, (tot + a.min_tiles - 1) / a.min_tiles));
+}
+
+// Merges the partial rows of sequences that several workers share.
+cudaError_t launch_latent_combine(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream);
+cudaError_t launch_latent_simt(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream);
+
+struct ExpandedArgs {
+    const void* q;       // [Nq, H, Dn + P]
+    const void* kv;      // [Nk, H, Dn + Dv]
+    const void* k_rope;  // [Nk, P]
+    const int32_t* q_lens;
+    const int32_t* k_lens;
+    void* out;           // [Nq, H, Dv]
+    float* lse_out;      // [Nq, H] or null
+    int32_t* dev_status;
+    int Q, Nq, Nk, H, Dn, Dv, P;
+    float qscale;        // scale * log2(e)
+    int causal;
+};
+
+// Queries and keys of one sequence.  A bad pair of q_lens leaves no queries, a
+// bad pair of k_lens no keys.
+struct PackedSeq {
+    int q0, nq, k0, nk;
+    uint32_t bad;
+};
+
+__device__ __forceinline__ PackedSeq packed_seq(const ExpandedArgs& a, int b) {
+    PackedSeq s{0, 0, 0, 0, 0u};
+    const int q0 = a.q_lens[b], q1 = a.q_lens[b + 1], k0 = a.k_lens[b], k1 = a.k_lens[b + 1];
+    if ((b == 0 && q0 != 0) || q0 < 0 || q1 < q0 || q1 > a.Nq) {
+        s.bad = KVD_DEV_SEQLENS;
+    } else {
+        s.q0 = q0;
+        s.nq = q1 - q0;
+    }
+    if ((b == 0 && k0 != 0) || k0 < 0 || k1 < k0 || k1 > a.Nk) {
+        s.bad = KVD_DEV_SEQLENS;
+    } else {
+        s.k0 = k0;
+        s.nk = k1 - k0;
+    }
+    return s;
+}
+
+cudaError_t launch_expanded_simt(const ExpandedArgs& a, kvd_dtype dt, cudaStream_t stream);
+
+cudaError_t launch_append_latent(void* latent, void* rope, const void* latent_new,
+                                 const void* rope_new, const int32_t* block_tables,
+                                 const int32_t* seq_offset, const int32_t* new_lens,
+                                 const int32_t* pos, int Q, int N, int NB, int BS, int cols,
+                                 int latent_bytes, int rope_bytes, int32_t* dev_status,
+                                 cudaStream_t stream);
+cudaError_t launch_verify_drafts(const void* target, const void* draft, const int32_t* drafts,
+                                 const float* u_accept, const float* u_sample,
+                                 const int32_t* num_drafts, int32_t* tokens, int32_t* accepted,
+                                 int Q, int T, int V, kvd_dtype dt, int32_t* dev_status,
+                                 cudaStream_t stream);
+
+}  // namespace kvd

@@ -26,6 +26,9 @@ DEV_TABLE_COLS = 4
 DEV_SEQLENS = 8
 DEV_SEQ_OFFSET = 16
 DEV_TIMEOUT = 32
+DEV_POINTER = 64
+DEV_TOKEN_RANGE = 128
+DEV_PROBS = 256
 
 # Entry points of include/kvd.h with their argument types.
 _vp, _sz, _i, _f = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
@@ -83,6 +86,11 @@ SIGNATURES = {
     "kvd_gather_paged": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp] + [_i] * 10 + [_vp, _vp], _i),
     "kvd_combine": ([_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
     "kvd_combine_gathered": ([_vp, _vp, _vp, _i, _i, _i, _i, _vp], _i),
+    "kvd_append_latent": ([_vp] * 8 + [_i] * 8 + [_vp, _vp], _i),
+    "kvd_attend_latent_workspace_bytes": ([_i] * 8, _sz),
+    "kvd_attend_latent": ([_vp] * 9 + [_i] * 8 + [_f, _i, _vp, _sz, _vp, _vp], _i),
+    "kvd_attend_expanded": ([_vp] * 7 + [_i] * 7 + [_f, _i, _i, _vp, _vp], _i),
+    "kvd_verify_drafts": ([_vp] * 8 + [_i] * 4 + [_vp, _vp], _i),
     "kvd_status_string": ([_i], ctypes.c_char_p),
     "kvd_last_error": ([], ctypes.c_char_p),
     "kvd_version": ([], _i),
@@ -152,7 +160,7 @@ def status_tensor(device=None):
 # the KVD_DEV_* bits of kvd.h
 DEV_BITS = {1: "KVD_DEV_POS_RANGE", 2: "KVD_DEV_BLOCK_RANGE", 4: "KVD_DEV_TABLE_COLS",
             8: "KVD_DEV_SEQLENS", 16: "KVD_DEV_SEQ_OFFSET", 32: "KVD_DEV_TIMEOUT",
-            64: "KVD_DEV_POINTER"}
+            64: "KVD_DEV_POINTER", 128: "KVD_DEV_TOKEN_RANGE", 256: "KVD_DEV_PROBS"}
 
 
 class KvdDeviceError(RuntimeError):
@@ -1040,3 +1048,215 @@ def combine_gathered(parts, R, D, out=None, lse=None, out_dtype=torch.float32):
                                      _stream(parts.device))
     _check("kvd_combine_gathered", st)
     return out
+
+
+# ------------------------------------------------------------------ latent caches
+
+def _latent_tensors(fn, dev, *named):
+    """Every (name, tensor) is a contiguous CUDA tensor of device `dev`."""
+    for n, t in named:
+        if not (t.is_cuda and t.is_contiguous()):
+            raise ValueError(f"{fn}: {n} must be a contiguous CUDA tensor")
+        if t.device != dev:
+            raise ValueError(f"{fn}: {n} is on {t.device}, not on {dev}")
+
+
+def _latent_int32(fn, dev, name, t, shape):
+    _latent_tensors(fn, dev, (name, t))
+    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        raise ValueError(f"{fn}: {name} must be int32 {list(shape)}")
+
+
+def _latent_outputs(fn, dev, out, out_shape, dtype, lse, lse_shape):
+    if out is None:
+        out = torch.empty(out_shape, dtype=dtype, device=dev)
+    else:
+        _latent_tensors(fn, dev, ("out", out))
+        if tuple(out.shape) != out_shape or out.dtype != dtype:
+            raise ValueError(f"{fn}: out must be {dtype} {list(out_shape)}")
+    if lse is not None:
+        _latent_tensors(fn, dev, ("lse", lse))
+        if tuple(lse.shape) != lse_shape or lse.dtype != torch.float32:
+            raise ValueError(f"{fn}: lse must be fp32 {list(lse_shape)}")
+    return out
+
+
+def _latent_call(fn, dev, *args):
+    """One call of the C entry point on the tensors' device and its current stream."""
+    call = getattr(load(), fn)
+    if torch.cuda.current_device() == dev.index:
+        st = call(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = call(*args, _stream(dev))
+    _check(fn, st)
+
+
+def _latent_cache(fn, latent_cache, rope_cache, block_tables, seq_offset, Q):
+    dev = latent_cache.device
+    _latent_tensors(fn, dev, ("latent_cache", latent_cache), ("rope_cache", rope_cache))
+    if latent_cache.dim() != 4 or latent_cache.shape[2] != 1 or \
+            tuple(rope_cache.shape[:3]) != tuple(latent_cache.shape[:3]) or rope_cache.dim() != 4:
+        raise ValueError(f"{fn}: caches must be [NB, BS, 1, R] and [NB, BS, 1, P]")
+    if rope_cache.dtype != latent_cache.dtype:
+        raise TypeError(f"{fn}: the caches must share a dtype")
+    if block_tables.dim() != 2:
+        raise ValueError(f"{fn}: block_tables must be int32 [Q, cols]")
+    cols = block_tables.shape[1]
+    _latent_int32(fn, dev, "block_tables", block_tables, (Q, cols))
+    if seq_offset is not None:
+        _latent_int32(fn, dev, "seq_offset", seq_offset, (Q,))
+    NB, BS, _, R = latent_cache.shape
+    return dev, NB, BS, cols, R, rope_cache.shape[3]
+
+
+def append_latent(latent_cache, rope_cache, block_tables, seq_offset, latent_new, rope_new,
+                  new_lens, pos, dev_status=None):
+    """kvd_append_latent: row new_lens[q] + i of latent_new [N, R] and rope_new
+    [N, P] becomes token pos[q] + i of sequence q in the paged latent cache
+    (latent_cache [NB, BS, 1, R], rope_cache [NB, BS, 1, P]; block_tables
+    [Q, cols], seq_offset [Q] or None, new_lens [Q + 1] cumsum, pos [Q] int32)."""
+    fn = "append_latent"
+    Q = pos.shape[0] if pos.dim() == 1 else -1
+    dev, NB, BS, cols, R, P = _latent_cache(fn, latent_cache, rope_cache, block_tables, seq_offset,
+                                            Q)
+    _latent_tensors(fn, dev, ("latent_new", latent_new), ("rope_new", rope_new))
+    N = latent_new.shape[0]
+    if tuple(latent_new.shape) != (N, R) or tuple(rope_new.shape) != (N, P):
+        raise ValueError(f"{fn}: new rows must be [N, {R}] and [N, {P}]")
+    if not (latent_new.dtype == rope_new.dtype == latent_cache.dtype):
+        raise TypeError(f"{fn}: caches and new rows must share a dtype")
+    _latent_int32(fn, dev, "new_lens", new_lens, (Q + 1,))
+    _latent_int32(fn, dev, "pos", pos, (Q,))
+    _latent_call("kvd_append_latent", dev, _ptr(latent_cache), _ptr(rope_cache), _ptr(latent_new),
+                 _ptr(rope_new), _ptr(block_tables), _ptr(seq_offset), _ptr(new_lens), _ptr(pos),
+                 Q, N, NB, BS, cols, R, P, _dtype_code(latent_cache), _ptr(dev_status))
+
+
+def attend_latent_workspace_bytes(Q, T, H, BS, cols, R, P, dtype=torch.bfloat16):
+    return load().kvd_attend_latent_workspace_bytes(Q, T, H, BS, cols, R, P,
+                                                    BF16 if dtype == torch.bfloat16 else F32)
+
+
+def attend_latent(q_latent, q_rope, latent_cache, rope_cache, block_tables, seq_lens, scale,
+                  seq_offset=None, out=None, lse=None, workspace=None, dev_status=None):
+    """kvd_attend_latent: the newest T tokens of every sequence attend over its
+    rows of the paged latent cache, each to the tokens up to itself.
+
+    q_latent [Q, T, H, R], q_rope [Q, T, H, P]; latent_cache [NB, BS, 1, R],
+    rope_cache [NB, BS, 1, P]; block_tables [Q, cols], seq_lens [Q + 1] cumsum
+    (the T new tokens counted), seq_offset [Q] or None, int32.  ``scale`` is
+    that of the attention before the projections were absorbed.  Returns out
+    [Q, T, H, R]; fills ``lse`` [Q, T, H] fp32 if given.
+    """
+    fn = "attend_latent"
+    if q_latent.dim() != 4 or q_rope.dim() != 4:
+        raise ValueError(f"{fn}: queries must be [Q, T, H, R] and [Q, T, H, P]")
+    Q, T, H, _ = q_latent.shape
+    dev, NB, BS, cols, R, P = _latent_cache(fn, latent_cache, rope_cache, block_tables, seq_offset,
+                                            Q)
+    _latent_tensors(fn, dev, ("q_latent", q_latent), ("q_rope", q_rope))
+    if tuple(q_latent.shape) != (Q, T, H, R) or tuple(q_rope.shape) != (Q, T, H, P):
+        raise ValueError(f"{fn}: queries must be [Q, T, H, {R}] and [Q, T, H, {P}]")
+    if not (q_latent.dtype == q_rope.dtype == latent_cache.dtype):
+        raise TypeError(f"{fn}: queries and caches must share a dtype")
+    _latent_int32(fn, dev, "seq_lens", seq_lens, (Q + 1,))
+    dt = _dtype_code(q_latent)
+    out = _latent_outputs(fn, dev, out, (Q, T, H, R), q_latent.dtype, lse, (Q, T, H))
+    need = load().kvd_attend_latent_workspace_bytes(Q, T, H, BS, cols, R, P, dt)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace is not None:
+        _latent_tensors(fn, dev, ("workspace", workspace))
+    _latent_call("kvd_attend_latent", dev, _ptr(q_latent), _ptr(q_rope), _ptr(latent_cache),
+                 _ptr(rope_cache), _ptr(block_tables), _ptr(seq_lens), _ptr(seq_offset), _ptr(out),
+                 _ptr(lse), Q, T, H, NB, BS, cols, R, P, float(scale), dt, _ptr(workspace),
+                 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                 _ptr(dev_status))
+    return out
+
+
+def attend_expanded(q, kv, k_rope, q_lens, k_lens, scale=None, causal=True, out=None, lse=None,
+                    dev_status=None):
+    """kvd_attend_expanded: packed sequences over keys and values expanded from
+    latent rows, the rotary key part shared by all heads.
+
+    q [Nq, H, Dn + P], kv [Nk, H, Dn + Dv] (keys, then values), k_rope [Nk, P];
+    q_lens, k_lens [Q + 1] int32 cumsum.  The last query of a sequence sees all
+    its keys, each one before it one key fewer (``causal=False``: every query
+    sees them all).  ``scale`` defaults to 1/sqrt(Dn + P).  Returns out
+    [Nq, H, Dv]; fills ``lse`` [Nq, H] fp32 if given.
+    """
+    fn = "attend_expanded"
+    dev = q.device
+    _latent_tensors(fn, dev, ("q", q), ("kv", kv), ("k_rope", k_rope))
+    if q.dim() != 3 or kv.dim() != 3 or k_rope.dim() != 2 or k_rope.shape[0] != kv.shape[0] or \
+            kv.shape[1] != q.shape[1]:
+        raise ValueError(f"{fn}: q [Nq, H, Dn + P], kv [Nk, H, Dn + Dv], k_rope [Nk, P] required")
+    Nq, H, Dqk = q.shape
+    Nk, P = k_rope.shape
+    Dn = Dqk - P
+    Dv = kv.shape[2] - Dn
+    if Dn < 1 or Dv < 1:
+        raise ValueError(f"{fn}: rows of q {Dqk}, kv {kv.shape[2]} and k_rope {P} do not fit")
+    if not (q.dtype == kv.dtype == k_rope.dtype):
+        raise TypeError(f"{fn}: q, kv and k_rope must share a dtype")
+    Q = q_lens.shape[0] - 1 if q_lens.dim() == 1 else -1
+    _latent_int32(fn, dev, "q_lens", q_lens, (Q + 1,))
+    _latent_int32(fn, dev, "k_lens", k_lens, (Q + 1,))
+    if scale is None:
+        scale = 1.0 / math.sqrt(Dqk)
+    out = _latent_outputs(fn, dev, out, (Nq, H, Dv), q.dtype, lse, (Nq, H))
+    _latent_call("kvd_attend_expanded", dev, _ptr(q), _ptr(kv), _ptr(k_rope), _ptr(q_lens),
+                 _ptr(k_lens), _ptr(out), _ptr(lse), Q, Nq, Nk, H, Dn, Dv, P, float(scale),
+                 int(bool(causal)), _dtype_code(q), _ptr(dev_status))
+    return out
+
+
+# ------------------------------------------------------------------ drafted tokens
+
+def verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, num_drafts=None,
+                  tokens=None, accepted=None, dev_status=None):
+    """kvd_verify_drafts: drafted tokens accepted while u * q(x) < p(x), then one
+    more from max(p - q, 0) (or, behind the last draft, from p) by u_sample.
+
+    target_probs [Q, T + 1, V], draft_probs [Q, T, V] bf16 or fp32;
+    draft_tokens [Q, T] int32; u_accept [Q, T], u_sample [Q] fp32; num_drafts
+    [Q] int32 or None (T each).  The drafts' arguments may be None where T = 0.
+    Returns tokens [Q, T + 1] int32 (accepted drafts, the new token, then -1)
+    and accepted [Q] int32.
+    """
+    fn = "verify_drafts"
+    dev = target_probs.device
+    _latent_tensors(fn, dev, ("target_probs", target_probs))
+    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+        raise ValueError(f"{fn}: target_probs must be [Q, T + 1, V]")
+    Q, T, V = target_probs.shape
+    T -= 1
+    if T > 0:
+        _latent_tensors(fn, dev, ("draft_probs", draft_probs), ("u_accept", u_accept))
+        if tuple(draft_probs.shape) != (Q, T, V) or draft_probs.dtype != target_probs.dtype:
+            raise ValueError(f"{fn}: draft_probs must be {target_probs.dtype} {[Q, T, V]}")
+        _latent_int32(fn, dev, "draft_tokens", draft_tokens, (Q, T))
+        if tuple(u_accept.shape) != (Q, T) or u_accept.dtype != torch.float32:
+            raise ValueError(f"{fn}: u_accept must be fp32 {[Q, T]}")
+    else:
+        draft_probs = draft_tokens = u_accept = None
+    _latent_tensors(fn, dev, ("u_sample", u_sample))
+    if tuple(u_sample.shape) != (Q,) or u_sample.dtype != torch.float32:
+        raise ValueError(f"{fn}: u_sample must be fp32 {[Q]}")
+    if num_drafts is not None:
+        _latent_int32(fn, dev, "num_drafts", num_drafts, (Q,))
+    if tokens is None:
+        tokens = torch.empty((Q, T + 1), dtype=torch.int32, device=dev)
+    else:
+        _latent_int32(fn, dev, "tokens", tokens, (Q, T + 1))
+    if accepted is None:
+        accepted = torch.empty((Q,), dtype=torch.int32, device=dev)
+    else:
+        _latent_int32(fn, dev, "accepted", accepted, (Q,))
+    _latent_call("kvd_verify_drafts", dev, _ptr(target_probs), _ptr(draft_probs),
+                 _ptr(draft_tokens), _ptr(u_accept), _ptr(u_sample), _ptr(num_drafts),
+                 _ptr(tokens), _ptr(accepted), Q, T, V, _dtype_code(target_probs),
+                 _ptr(dev_status))
+    return tokens, accepted

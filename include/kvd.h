@@ -79,6 +79,8 @@ typedef enum { KVD_BF16 = 0, KVD_F32 = 1 } kvd_dtype;
 #define KVD_DEV_SEQ_OFFSET 16u   /* seq_offset negative or not a multiple of block_size */
 #define KVD_DEV_TIMEOUT 32u      /* a bounded in-kernel wait ran out */
 #define KVD_DEV_POINTER 64u      /* a pointer read from a device pointer array is null or misaligned */
+#define KVD_DEV_TOKEN_RANGE 128u /* drafted token outside [0, V) */
+#define KVD_DEV_PROBS 256u       /* no finite positive weight to sample a token from */
 
 /*
  * kvd_append -- [NPU] Part 2, update_kvcache_for: for every batch entry b
@@ -625,6 +627,135 @@ kvd_status kvd_combine(const float* part_o, const float* part_lse, void* out, fl
  */
 kvd_status kvd_combine_gathered(const float* parts, void* out, float* lse_out, int R, int S,
                                 int D, kvd_dtype out_dtype, kvd_stream_t stream);
+
+/*
+ * Latent caches.  One row a token, shared by all heads: R latent values, which
+ * are the keys and the values at once, and P rotary key values.  The paged
+ * cache is the one kvd_gather_paged reads with one head ([PyPTO] 3.1, 8.1):
+ *   latent_cache [NB, BS, 1, R], rope_cache [NB, BS, 1, P] of `dtype`.
+ * R in {128, 256, 384, 512}, P = 64.  The attention of such a cache has two
+ * forms.  With the up-projections multiplied into the queries and the outputs
+ * (absorbed), it runs over the rows themselves: kvd_attend_latent.  With the
+ * rows gathered and expanded into keys and values per head, it is ordinary
+ * attention whose rotary key part is shared: kvd_attend_expanded.
+ */
+
+/*
+ * kvd_append_latent -- kvd_append_paged for latent rows, any number of new
+ * tokens a sequence: row new_lens[q] + i of latent_new and rope_new is written
+ * to token pos[q] + i of sequence q, 0 <= i < new_lens[q + 1] - new_lens[q],
+ * i.e. to page block_tables[q, seq_offset[q] / BS + (pos[q] + i) / BS], slot
+ * (pos[q] + i) % BS.
+ *   latent_cache [NB, BS, 1, R], rope_cache [NB, BS, 1, P] of `dtype` (in/out)
+ *   latent_new [N, R], rope_new [N, P] of `dtype`, packed
+ *   new_lens [Q + 1] int32, cumsum starting at 0;  pos [Q] int32 (device)
+ *   block_tables [Q, cols] int32;  seq_offset [Q] int32 or NULL (zeros)
+ * A byte copy.  Rows at and behind new_lens[Q] are not read.  Device-detected
+ * errors skip the row (nothing written): new_lens not starting at 0,
+ * decreasing or past N (KVD_DEV_SEQLENS), pos[q] < 0 (KVD_DEV_POS_RANGE),
+ * seq_offset negative or not a multiple of BS (KVD_DEV_SEQ_OFFSET), table
+ * column past cols (KVD_DEV_TABLE_COLS), block id outside [0, NB)
+ * (KVD_DEV_BLOCK_RANGE).  Any R and P with rows of whole 16-byte vectors.
+ */
+kvd_status kvd_append_latent(void* latent_cache, void* rope_cache, const void* latent_new,
+                             const void* rope_new, const int32_t* block_tables,
+                             const int32_t* seq_offset, const int32_t* new_lens,
+                             const int32_t* pos, int Q, int N, int NB, int BS, int cols, int R,
+                             int P, kvd_dtype dtype, int32_t* dev_status, kvd_stream_t stream);
+
+/*
+ * kvd_attend_latent -- attention of the newest T tokens of every sequence over
+ * the paged latent cache, the absorbed form ([FlashMLA] "Математическая
+ * постановка": one KV row per token, the values its first R elements).  With
+ * n = seq_lens[q + 1] - seq_lens[q] tokens in the cache (the T new ones among
+ * them), query token t of sequence q and head h:
+ *   s_k = scale * (q_latent[q, t, h, :] . latent_k + q_rope[q, t, h, :] . rope_k)
+ *   out[q, t, h, :] = sum_k w_k latent_k / sum_k w_k,  w_k = exp(s_k - max)
+ *   lse[q, t, h] = log sum_k exp(s_k),  over the tokens 0 <= k <= n - T + t
+ * (token t of the newest T sees everything up to itself; T = 1: the whole
+ * sequence).  A query with no such token (n - T + t < 0) gives out = 0,
+ * lse = -inf.
+ *   q_latent [Q, T, H, R], q_rope [Q, T, H, P] of `dtype`
+ *   block_tables, seq_lens, seq_offset as for kvd_attend_paged
+ *   out [Q, T, H, R] of `dtype`;  lse_out [Q, T, H] float or NULL
+ * Slots of a page behind the sequence's end may hold anything (inf, NaN).
+ * The rows of the sequence itself must be finite: one that is not reaches all
+ * T queries of its sequence, also those that come before it.
+ * Device-detected errors as for kvd_attend_paged: KVD_DEV_SEQLENS, SEQ_OFFSET
+ * and TABLE_COLS make the sequence empty, KVD_DEV_BLOCK_RANGE drops the
+ * block's tokens.
+ * Workspace: at least kvd_attend_latent_workspace_bytes(...) bytes, 256-byte
+ * aligned; its contents do not matter before a call (no zero fill) and calls
+ * that may overlap on the GPU must not share one.
+ */
+size_t kvd_attend_latent_workspace_bytes(int Q, int T, int H, int BS, int cols, int R, int P,
+                                         kvd_dtype dtype);
+kvd_status kvd_attend_latent(const void* q_latent, const void* q_rope, const void* latent_cache,
+                             const void* rope_cache, const int32_t* block_tables,
+                             const int32_t* seq_lens, const int32_t* seq_offset, void* out,
+                             float* lse_out, int Q, int T, int H, int NB, int BS, int cols, int R,
+                             int P, float scale, kvd_dtype dtype, void* workspace,
+                             size_t workspace_bytes, int32_t* dev_status, kvd_stream_t stream);
+
+/*
+ * kvd_attend_expanded -- the expanded form, for prompts and chunks of them:
+ * packed sequences, per-head keys and values that were expanded from gathered
+ * latent rows (kv, as one projection leaves them: Dn key values, then Dv
+ * values), the rotary key part shared by all heads.  With nq queries and nk
+ * keys of sequence b, query i of head h sees the keys 0 <= j <= i + nk - nq
+ * (causal from the end: the last query sees every key):
+ *   s_j = scale * (q[i, h, :Dn] . kv[j, h, :Dn] + q[i, h, Dn:] . k_rope[j, :])
+ *   out[i, h, :] = sum_j w_j kv[j, h, Dn:] / sum_j w_j,  w_j = exp(s_j - max)
+ *   lse[i, h] = log sum_j exp(s_j)
+ * With causal = 0 every query of b sees all nk keys.  A query that sees no
+ * key gives out = 0, lse = -inf.
+ *   q [Nq, H, Dn + P], kv [Nk, H, Dn + Dv], k_rope [Nk, P] of `dtype`
+ *   q_lens, k_lens [Q + 1] int32, cumsum starting at 0 (device)
+ *   out [Nq, H, Dv] of `dtype`;  lse_out [Nq, H] float or NULL
+ * Rows of out and lse_out at and behind q_lens[Q] are left as they were; rows
+ * of kv and k_rope of other sequences and behind k_lens[Q] may hold anything.
+ * The keys and values of a sequence must be finite (one that is not may reach
+ * queries of its sequence that come before it).
+ * Device-detected errors: a bad pair of k_lens (not starting at 0, decreasing,
+ * past Nk) makes the sequence's keys empty, a bad pair of q_lens skips its
+ * queries; both set KVD_DEV_SEQLENS.
+ * Supported: Dn, Dv in {64, 128}, P = 64.  Needs no workspace.
+ */
+kvd_status kvd_attend_expanded(const void* q, const void* kv, const void* k_rope,
+                               const int32_t* q_lens, const int32_t* k_lens, void* out,
+                               float* lse_out, int Q, int Nq, int Nk, int H, int Dn, int Dv, int P,
+                               float scale, int causal, kvd_dtype dtype, int32_t* dev_status,
+                               kvd_stream_t stream);
+
+/*
+ * kvd_verify_drafts -- drafted tokens against the target's probabilities, from
+ * given random numbers.  Sequence q has m = num_drafts[q] drafts (T without
+ * num_drafts) x_i = draft_tokens[q, i], drawn from draft_probs[q, i, :].
+ *   draft i is accepted while  u_accept[q, i] * draft_probs[q, i, x_i] <
+ *   target_probs[q, i, x_i]  (in 64 bits) and all drafts before it are;
+ *   n = number of accepted drafts;
+ *   one more token comes from the weights w_v = max(target_probs[q, n, v] -
+ *   draft_probs[q, n, v], 0) if n < m (from target_probs[q, n, v] itself where
+ *   these are all zero), w_v = target_probs[q, m, v] if n = m: the smallest v
+ *   with w_0 + ... + w_v > u_sample[q] * (sum of w), the largest v with
+ *   w_v > 0 where rounding leaves none.
+ *   tokens[q, :] = x_0 .. x_{n-1}, that token, then -1;  accepted[q] = n.
+ *   target_probs [Q, T + 1, V], draft_probs [Q, T, V] of `dtype`; they need
+ *   not be normalised; NaN and negative weights count as zero
+ *   draft_tokens [Q, T] int32;  u_accept [Q, T], u_sample [Q] float in [0, 1)
+ *   num_drafts [Q] int32 or NULL;  tokens [Q, T + 1] int32;  accepted [Q] int32
+ * T = 0 (a token without drafts) takes NULL for the drafts' arrays.  The
+ * acceptance and the subtraction are exact to 64 bits and the sums are held in
+ * two fp32 words or 64 bits.  Device-detected errors: a drafted token outside
+ * [0, V) is rejected (KVD_DEV_TOKEN_RANGE); no weight above zero, or a sum
+ * that is not finite, gives the token -1 (KVD_DEV_PROBS); num_drafts[q]
+ * outside [0, T] gives tokens -1 and accepted 0 (KVD_DEV_POS_RANGE).
+ */
+kvd_status kvd_verify_drafts(const void* target_probs, const void* draft_probs,
+                             const int32_t* draft_tokens, const float* u_accept,
+                             const float* u_sample, const int32_t* num_drafts, int32_t* tokens,
+                             int32_t* accepted, int Q, int T, int V, kvd_dtype dtype,
+                             int32_t* dev_status, kvd_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
 const char* kvd_status_string(kvd_status status);
