@@ -52,10 +52,11 @@ kvd_status latent_plan(const char* fn, int Q, int T, int H, int BS, int cols, in
     if (Q > 65535) return fail(KVD_ERR_UNSUPPORTED, "%s: Q > 65535", fn);
     if ((long long)T * H > 65535) return fail(KVD_ERR_UNSUPPORTED, "%s: T*H > 65535", fn);
     if ((long long)cols * BS >= (1ll << 31)) return fail(KVD_ERR_UNSUPPORTED, "%s: cols*BS >= 2^31", fn);
-    const int rows = T * H, most = 16;
+    const bool mma = dt == KVD_BF16;
+    const int rows = T * H, most = mma ? 64 : 16, ctas = mma ? kLatentSMs : 2 * kLatentSMs;
     pl->groups = (rows + most - 1) / most;
     pl->rpg = (rows + pl->groups - 1) / pl->groups;
-    pl->workers = pl->groups < 2 * kLatentSMs ? 2 * kLatentSMs / pl->groups : 1;
+    pl->workers = pl->groups < ctas ? ctas / pl->groups : 1;
     pl->min_tiles = 2;
     const size_t slots = (size_t)pl->workers * pl->groups * 2;
     pl->off_lse = round256((size_t)(Q < 1 ? 1 : Q) * sizeof(int4));
@@ -158,7 +159,16 @@ kvd_status kvd_attend_latent(const void* q_latent, const void* q_rope, const voi
     a.meta = reinterpret_cast<int4*>(ws);
     a.part_lse = reinterpret_cast<float*>(ws + pl.off_lse);
     a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
-    cudaError_t e = launch_latent_simt(a, dtype, (cudaStream_t)stream);
+    cudaError_t e;
+    if (dtype == KVD_BF16) {
+        CUtensorMap lmap, rmap;
+        e = encode_rows(&lmap, latent_cache, R, (long long)NB * BS, latent_piece(BS));
+        if (e == cudaSuccess)
+            e = encode_rows(&rmap, rope_cache, P, (long long)NB * BS, latent_piece(BS));
+        if (e == cudaSuccess) e = launch_latent_mma(a, lmap, rmap, (cudaStream_t)stream);
+    } else {
+        e = launch_latent_simt(a, dtype, (cudaStream_t)stream);
+    }
     if (e == cudaSuccess) e = launch_latent_combine(a, dtype, (cudaStream_t)stream);
     return launched(fn, e);
 }

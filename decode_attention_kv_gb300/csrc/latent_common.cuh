@@ -129,6 +129,9 @@ __device__ __forceinline__ int used_workers(const LatentArgs& a, int tot) {
 
 // Merges the partial rows of sequences that several workers share.
 cudaError_t launch_latent_combine(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream);
+int latent_piece(int BS);
+cudaError_t launch_latent_mma(const LatentArgs& a, const CUtensorMap& lmap, const CUtensorMap& rmap,
+                              cudaStream_t stream);
 cudaError_t launch_latent_simt(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream);
 
 struct ExpandedArgs {
