@@ -50,6 +50,7 @@ kvd_status latent_plan(const char* fn, int Q, int T, int H, int BS, int cols, in
         return fail(KVD_ERR_UNSUPPORTED, "%s: R = %d (supported: 128, 256, 384, 512)", fn, R);
     if (P != 64) return fail(KVD_ERR_UNSUPPORTED, "%s: P = %d (supported: 64)", fn, P);
     if (Q > 65535) return fail(KVD_ERR_UNSUPPORTED, "%s: Q > 65535", fn);
+    if ((long long)Q * T * H >= (1ll << 31)) return fail(KVD_ERR_UNSUPPORTED, "%s: Q*T*H >= 2^31", fn);
     if ((long long)T * H > 65535) return fail(KVD_ERR_UNSUPPORTED, "%s: T*H > 65535", fn);
     if ((long long)cols * BS >= (1ll << 31)) return fail(KVD_ERR_UNSUPPORTED, "%s: cols*BS >= 2^31", fn);
     const bool mma = dt == KVD_BF16;
@@ -159,16 +160,8 @@ kvd_status kvd_attend_latent(const void* q_latent, const void* q_rope, const voi
     a.meta = reinterpret_cast<int4*>(ws);
     a.part_lse = reinterpret_cast<float*>(ws + pl.off_lse);
     a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
-    cudaError_t e;
-    if (dtype == KVD_BF16) {
-        CUtensorMap lmap, rmap;
-        e = encode_rows(&lmap, latent_cache, R, (long long)NB * BS, latent_piece(BS));
-        if (e == cudaSuccess)
-            e = encode_rows(&rmap, rope_cache, P, (long long)NB * BS, latent_piece(BS));
-        if (e == cudaSuccess) e = launch_latent_mma(a, lmap, rmap, (cudaStream_t)stream);
-    } else {
-        e = launch_latent_simt(a, dtype, (cudaStream_t)stream);
-    }
+    cudaError_t e = dtype == KVD_BF16 ? launch_latent_mma(a, (cudaStream_t)stream)
+                                      : launch_latent_simt(a, dtype, (cudaStream_t)stream);
     if (e == cudaSuccess) e = launch_latent_combine(a, dtype, (cudaStream_t)stream);
     return launched(fn, e);
 }

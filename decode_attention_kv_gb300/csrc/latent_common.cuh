@@ -63,11 +63,13 @@ __device__ __forceinline__ SeqInfo latent_seq(const LatentArgs& a, int b) {
     return s;
 }
 
-// Finds, with the whole block, the item of `target` in a line of items with
+// Finds the item of `target` in a line of items with
 // count(b) places each (b < Q): item, the places before it, and the total.
-// Every thread gets the result; item = Q if target is behind the line.
-// `scratch`: kFindWords ints of shared memory.
+// Every thread gets the result; item = Q if target is behind the line.  Up to
+// kFindWarp items each warp finds it by itself (no barrier), above with the whole
+// block.  `scratch`: kFindWords ints of shared memory.
 constexpr int kFindWords = 40;
+constexpr int kFindWarp = 128;
 struct Found {
     int item;
     int before;
@@ -77,6 +79,37 @@ struct Found {
 template <int THREADS, typename Total, typename Count>
 __device__ __forceinline__ Found block_find(int Q, int* scratch, Total target_of, Count count) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (Q <= kFindWarp) {
+        constexpr int kPer = kFindWarp / 32;
+        int c[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int b = lane * kPer + i;
+            c[i] = b < Q ? count(b) : 0;
+            sum += c[i];
+        }
+        int inc = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        const int total = __shfl_sync(0xffffffffu, inc, 31);
+        const int target = target_of(total);
+        int at = inc - sum, item = lane * kPer;
+        const bool mine = target >= at && target < inc;
+#pragma unroll
+        for (int i = 0; i + 1 < kPer; ++i)
+            if (mine && target >= at + c[i] && item == lane * kPer + i) {
+                at += c[i];
+                ++item;
+            }
+        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        const int src = who ? __ffs(who) - 1 : 0;
+        item = __shfl_sync(0xffffffffu, item, src);
+        at = __shfl_sync(0xffffffffu, at, src);
+        return Found{who ? item : Q, at, total};
+    }
     const int per = (Q + THREADS - 1) / THREADS;
     const int lo = min(tid * per, Q), hi = min(lo + per, Q);
     int sum = 0;
@@ -129,9 +162,7 @@ __device__ __forceinline__ int used_workers(const LatentArgs& a, int tot) {
 
 // Merges the partial rows of sequences that several workers share.
 cudaError_t launch_latent_combine(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream);
-int latent_piece(int BS);
-cudaError_t launch_latent_mma(const LatentArgs& a, const CUtensorMap& lmap, const CUtensorMap& rmap,
-                              cudaStream_t stream);
+cudaError_t launch_latent_mma(const LatentArgs& a, cudaStream_t stream);
 cudaError_t launch_latent_simt(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream);
 
 struct ExpandedArgs {

@@ -10,8 +10,9 @@
 // the lanes of a 512-column accumulator empty.
 //
 // Warps 0-3: softmax (a row a thread, so no shuffles), rescaling, epilogue.
-// Warp 4: tensor copies of the pages.  Warp 5: MMA issue; the scores of tile
-// i + 1 are issued before the values of tile i, so they run during softmax i.
+// Warps 4 and 5 issue the MMAs of the scores and of the values; the scores run
+// up to two tiles ahead of the softmax.  Warps 6-9: tensor copies of the pages.
+// Warp 10: of the queries.
 // The running output is rescaled only when some row's maximum rose by more
 // than 8 (log2 units), as in the decode kernel: weights stay below 2^8.
 #include "kvd_internal.h"
@@ -22,21 +23,24 @@ namespace kvd {
 namespace {
 
 constexpr int kSoftmax = 128;            // threads of warps 0-3
-constexpr int kThreads = kSoftmax + 64;
+constexpr int kCopyWarp = 6;              // the first of the copying warps, one per pair
+constexpr int kQueryWarp = kCopyWarp + 4;  // copies the queries
+constexpr int kThreads = 32 * (kQueryWarp + 1);
 constexpr int kTile = 64;                // keys of an MMA tile, rows of the query tile
 constexpr int kChunk = kTile * 128;      // bytes of 64 rows x 64 bf16
 constexpr int kMaxStages = 4;
+constexpr int kValid = 2 * kMaxStages;
 constexpr int kMaxPairs = 4;             // R / 128
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSkip = 8.f;             // log2 units
 
 struct MmaShared {
-    uint64_t full[kMaxStages][kMaxPairs];
-    uint64_t empty[kMaxStages];
-    uint64_t s_full[2];
-    uint64_t p_full, pv_done, q_full, drain;
-    unsigned long long valid[kMaxStages];
-    float factor[kTile];
+    uint64_t full[kMaxStages][2];  // the first (pairs + 1) / 2 pairs, the rest
+    uint64_t empty[kMaxStages][kMaxPairs];
+    uint64_t s_full[2], s_free[2];
+    uint64_t p_full, pv_done, q_full, q_free, drain[2];
+    unsigned long long valid[kValid];  // tile it's at it % kValid
+    alignas(16) float factor[kTile];
     uint32_t tmem;
     int abort;
     int scratch[kFindWords];
@@ -87,9 +91,82 @@ __device__ __forceinline__ void advance(Walk& k, const Segment& s) {
     ++k.b;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// Reads this lane's dims of the transposed output (a dim per lane and pair of
+// chunks, a row per column), multiplies each row by its factor and hands it on.
+template <typename Put>
+__device__ __forceinline__ void store_rows(uint32_t tm, int pairs, int N, int nrows,
+                                           const float* factor, int R, Put put) {
+    for (int c = 0; c < nrows; c += 16) {
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(factor + c + i);
+            f[i] = x.x;
+            f[i + 1] = x.y;
+            f[i + 2] = x.z;
+            f[i + 3] = x.w;
+        }
+        const int n = min(16, nrows - c);
+#pragma unroll 1
+        for (int j = 0; j < pairs; ++j) {
+            float o[16];
+            tmem_ld16(tm + j * N + c, o);
+            tmem_wait_ld();
+            const size_t at = (size_t)c * R + 128 * j;
+            if (n == 16) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) put(at + i * R, o[i] * f[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (i < n) put(at + i * R, o[i] * f[i]);
+            }
+        }
+    }
+}
+
+// mbar_wait by a whole converged warp: every branch is a vote, so that the
+// compiler sees a uniform control flow behind it.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    unsigned long long since = 0;
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        const unsigned long long now = global_timer_ns();
+        if (since == 0) since = now;
+        if (__any_sync(0xffffffffu, *abort_flag || now - since > kWaitLimitNs)) return false;
+    }
+    return true;
+}
+
+// Scores of the pairs [j0, j1) of a tile's chunks, added to D.
+__device__ __forceinline__ void score_pairs(uint32_t d, uint32_t q_low, uint32_t k_low,
+                                            uint32_t desc, int j0, int j1) {
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t off = ((2 * j + (i >> 2)) * kChunk + (i & 3) * 32) >> 4;
+            mma_ss(d, desc_of(q_low + off), desc_of(k_low + off), desc, true);
+        }
+    }
+}
+
+// A wait ran out: tells the others and waits for this warp's own MMAs.
+__device__ __forceinline__ void drain(uint64_t* bar, int* abort_flag) {
+    *reinterpret_cast<volatile int*>(abort_flag) = 1;
+    __syncwarp();
+    if (elect_one()) mma_commit(bar);
+    __syncwarp();
+    const unsigned long long since = global_timer_ns();
+    while (!mbar_try_wait(bar, 0) && global_timer_ns() - since < kWaitLimitNs) {
+    }
+    __syncwarp();
+}
+
+__global__ void __maxnreg__(128)
 latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ CUtensorMap lmap,
-                  const __grid_constant__ CUtensorMap rmap) {
+                  const __grid_constant__ CUtensorMap rmap,
+                  const __grid_constant__ CUtensorMap qlmap,
+                  const __grid_constant__ CUtensorMap qrmap) {
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char* sm = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const MmaLayout L(a.R);
@@ -100,23 +177,30 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
     const int KT = kTile / piece * piece;  // keys of a tile
     const int row0 = g * a.rpg, nrows = min(a.rpg, a.rows - row0);
     const int N = (a.rpg + 15) / 16 * 16;  // rows of the MMA
+    const uint32_t stage_bytes = L.chunks * kChunk;
+    const int front = (pairs + 1) / 2;  // pairs of the first half of a tile's copies
 
     if (tid == 0) {
         for (int s = 0; s < L.stages; ++s) {
-            for (int j = 0; j < pairs; ++j) mbar_init(&sh.full[s][j], 1);
-            mbar_init(&sh.empty[s], 1);
+            for (int j = 0; j < pairs; ++j) mbar_init(&sh.empty[s][j], 1);
+            mbar_init(&sh.full[s][0], front);
+            mbar_init(&sh.full[s][1], pairs - front + (pairs == front));
         }
-        mbar_init(&sh.s_full[0], 1);
-        mbar_init(&sh.s_full[1], 1);
+        mbar_init(&sh.s_full[0], 2);
+        mbar_init(&sh.s_full[1], 2);
+        mbar_init(&sh.s_free[0], kSoftmax);
+        mbar_init(&sh.s_free[1], kSoftmax);
         mbar_init(&sh.p_full, kSoftmax);
         mbar_init(&sh.pv_done, 1);
-        mbar_init(&sh.q_full, kSoftmax);
-        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_free, 1);
+        mbar_init(&sh.drain[0], 1);
+        mbar_init(&sh.drain[1], 1);
         sh.abort = 0;
         fence_barrier_init();
     }
     if (warp == 4) tmem_alloc(&sh.tmem, kTmemCols);
-    if (warp == 5 && lane == 0) {
+    if (warp >= kCopyWarp && lane == 0) {
         prefetch_tensormap(&lmap);
         prefetch_tensormap(&rmap);
     }
@@ -151,24 +235,56 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
     const int t0 = walk.t;
     bool bad = false;
 
-    if (warp == 4) {
+    if (warp == kQueryWarp) {
+        // ------------------------------------------------------------ queries
+        // N rows from the group's first on.  Where the group has fewer, the rest are
+        // other rows or zeros: their scores and outputs are never read.
+        const uint64_t policy = policy_evict_first();
+        int seg = 0;
+        while (walk.more() && !bad) {
+            const Segment s = segment(a, walk, KT);
+            const int row = uniform(walk.b * a.rows + row0);
+            if (seg > 0 && !warp_wait(&sh.q_free, (seg - 1) & 1, abort_flag)) {
+                bad = true;
+                break;
+            }
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&sh.q_full, (uint32_t)(N * 128 * L.chunks));
+                for (int c = 0; c < 2 * pairs; ++c)
+                    tma_g2s_3d(sm + L.q + c * kChunk, &qlmap, 0, row, c, &sh.q_full, policy);
+                tma_g2s_3d(sm + L.q + 2 * pairs * kChunk, &qrmap, 0, row, 0, &sh.q_full, policy);
+            }
+            __syncwarp();
+            advance(walk, s);
+            ++seg;
+        }
+        if (seg > 0) {  // nothing of its own may be in flight when it leaves
+            const unsigned long long since = global_timer_ns();
+            while (!mbar_try_wait(&sh.q_full, (seg - 1) & 1) &&
+                   global_timer_ns() - since < kWaitLimitNs) {
+            }
+        }
+    } else if (warp >= kCopyWarp) {
         // ------------------------------------------------------------ copies
+        // Warp j brings pair j of the chunks (the rotary chunk goes with pair 0) as
+        // the values MMAs free it: one wait, one count and one copy take a warp
+        // about 500 cycles from end to end, and four pairs by one warp set the
+        // pace of the whole kernel.  Lane p looks up piece p (and p + 32) of a tile
+        // before the wait and issues its copies: a box is one chunk of a piece, or a
+        // pair of chunks of a whole tile.
+        const int j = warp - kCopyWarp;
         const uint64_t policy = policy_evict_first();
         const int pieces = kTile / piece;
-        const uint32_t bytes = (uint32_t)piece * 128u;
-        int it = 0;
+        const uint32_t bytes = (uint32_t)piece * 128u, total = bytes * (j == 0 ? 3u : 2u);
+        unsigned char* dst = sm + L.kv + 2 * j * kChunk;
+        unsigned char* rdst = sm + L.kv + 2 * pairs * kChunk;
+        int it = 0, st = 0, par = 1;
+        if (j >= pairs) walk.t = walk.t1;
         while (walk.more() && !bad) {
             const Segment s = segment(a, walk, KT);
             for (int k = s.first; k < s.end; ++k, ++it) {
-                const int st = it % L.stages, use = it / L.stages;
-                if (use > 0 && !mbar_wait(&sh.empty[st], (use - 1) & 1, abort_flag)) bad = true;
-                if (__any_sync(0xffffffffu, bad)) {
-                    bad = true;
-                    break;
-                }
                 unsigned long long valid = 0;
                 int src[2];  // first row of this lane's pieces in the cache, or -1
-                int loads = 0;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int p = lane + 32 * u;
@@ -185,180 +301,269 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                             valid |= (n == 64 ? ~0ull : (1ull << n) - 1ull) << (p * piece);
                         }
                     }
-                    loads += __popc(__ballot_sync(0xffffffffu, src[u] >= 0));
                 }
+                const int loads = __popc(__ballot_sync(0xffffffffu, src[0] >= 0)) +
+                                  __popc(__ballot_sync(0xffffffffu, src[1] >= 0));
+                if (j == 0) {
+                    if (pieces > 1) {
 #pragma unroll
-                for (int d = 16; d; d >>= 1) valid |= __shfl_xor_sync(0xffffffffu, valid, d);
-                if (lane == 0) {
-                    sh.valid[st] = valid;
-                    for (int j = 0; j < pairs; ++j)
-                        mbar_arrive_expect_tx(&sh.full[st][j],
-                                              (uint32_t)loads * bytes * (j == 0 ? 3u : 2u));
+                        for (int d = 16; d; d >>= 1)
+                            valid |= __shfl_xor_sync(0xffffffffu, valid, d);
+                    }
+                    if (lane == 0) sh.valid[it % kValid] = valid;
+                    __syncwarp();
+                }
+                uint64_t* full = &sh.full[st][j >= front];
+                if (it >= L.stages) {
+                    // the stage is still in use: meanwhile the tile comes to L2
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (src[u] < 0) continue;
+                        tma_prefetch_3d(&lmap, 0, src[u], 2 * j);
+                        if (piece != kTile) tma_prefetch_3d(&lmap, 0, src[u], 2 * j + 1);
+                        if (j == 0) tma_prefetch_3d(&rmap, 0, src[u], 0);
+                    }
+                    __syncwarp();
+                    if (!warp_wait(&sh.empty[st][j], par, abort_flag)) {
+                        bad = true;
+                        break;
+                    }
+                }
+                if (pieces == 1) {
+                    const int row = uniform(src[0]);
+                    unsigned char* x = dst + st * stage_bytes;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(full, loads * total);
+                        if (row >= 0) {
+                            tma_g2s_3d(x, &lmap, 0, row, 2 * j, full, policy);
+                            if (piece != kTile)
+                                tma_g2s_3d(x + kChunk, &lmap, 0, row, 2 * j + 1, full, policy);
+                            if (j == 0)
+                                tma_g2s_3d(rdst + st * stage_bytes, &rmap, 0, row, 0, full, policy);
+                        }
+                    }
+                } else {
+                    if (lane == 0) mbar_arrive_expect_tx(full, loads * total);
+                    __syncwarp();
+                    const uint32_t at = st * stage_bytes + lane * bytes;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (src[u] < 0) continue;
+                        unsigned char* x = dst + at + u * 32 * bytes;
+                        tma_g2s_3d(x, &lmap, 0, src[u], 2 * j, full, policy);
+                        tma_g2s_3d(x + kChunk, &lmap, 0, src[u], 2 * j + 1, full, policy);
+                        if (j == 0)
+                            tma_g2s_3d(rdst + at + u * 32 * bytes, &rmap, 0, src[u], 0, full, policy);
+                    }
                 }
                 __syncwarp();
-                unsigned char* base = sm + L.kv + st * L.chunks * kChunk;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (src[u] < 0) continue;
-                    unsigned char* dst = base + (lane + 32 * u) * bytes;
-                    for (int c = 0; c < 2 * pairs; ++c) {
-                        tma_g2s_2d(dst + c * kChunk, &lmap, 64 * c, src[u], &sh.full[st][c >> 1],
-                                   policy);
-                        if (c == 1)
-                            tma_g2s_2d(dst + 2 * pairs * kChunk, &rmap, 0, src[u],
-                                       &sh.full[st][0], policy);
-                    }
+                if (++st == L.stages) {
+                    st = 0;
+                    par ^= 1;
                 }
             }
             advance(walk, s);
         }
         if (bad) {  // a wait ran out: leave only when the copies in flight have landed
             if (lane == 0) sh.abort = 1;
+            const unsigned long long since = global_timer_ns();
             for (int i = max(0, it - L.stages); i < it; ++i)
-                for (int j = 0; j < pairs; ++j) {
-                    const unsigned long long since = global_timer_ns();
-                    while (!mbar_try_wait(&sh.full[i % L.stages][j], (i / L.stages) & 1) &&
-                           global_timer_ns() - since < kWaitLimitNs) {
-                    }
+                while (!mbar_try_wait(&sh.full[i % L.stages][j >= front],
+                                      (i / L.stages) & 1) &&
+                       global_timer_ns() - since < kWaitLimitNs) {
                 }
         }
-    } else if (warp == 5) {
-        // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            const uint32_t sdesc = mma_desc(64, 64), odesc = mma_desc(128, N, kAMn);
-            const uint32_t q = smem_u32(sm + L.q), kv = smem_u32(sm + L.kv), p = smem_u32(sm + L.p);
-            // scores of tile `it`, the first of its segment if `fresh`
-            auto scores = [&](int it, int seg, bool fresh) {
-                const int st = it % L.stages;
-                if (fresh && !mbar_wait(&sh.q_full, seg & 1, abort_flag)) return false;
-                const uint32_t k = kv + st * L.chunks * kChunk, d = tmem_s + 64 * (it & 1);
-                for (int j = 0; j < pairs; ++j) {
-                    if (!mbar_wait(&sh.full[st][j], (it / L.stages) & 1, abort_flag)) return false;
-                    tc_fence_after();
-#pragma unroll
-                    for (int i = 0; i < 12; ++i) {
-                        if (j > 0 && i >= 8) break;
-                        const int c = i < 8 ? 2 * j + (i >> 2) : 2 * pairs;
-                        const uint32_t off = c * kChunk + (i & 3) * 32;
-                        mma_ss(d, smem_desc(q + off, 16), smem_desc(k + off, 16), sdesc,
-                               j > 0 || i > 0);
-                    }
+    } else if (warp == 4) {
+        // ------------------------------------------------------------ scores
+        // Everything that an issue loop branches on or addresses with goes through
+        // uniform(): MMA operands live in uniform registers, and with operands (or
+        // a control flow) that the compiler cannot prove to be the same in all
+        // lanes an MMA took 50 to 140 cycles to issue instead of 32 to 48.  Scores
+        // and values have a warp each, so that neither waits for the other's turn.
+        const uint32_t desc = mma_desc(kTile, kTile);
+        const uint32_t q = uniform(smem_u32(sm + L.q)), kv = uniform(smem_u32(sm + L.kv));
+        const uint32_t tm = uniform(tmem) + 256;
+        int it = 0, st = 0, par = 0, seg = 0;
+        while (uniform((int)walk.more()) && !bad) {
+            const Segment s = segment(a, walk, KT);
+            const int tiles = uniform(s.end - s.first);
+            bad = !warp_wait(&sh.q_full, seg & 1, abort_flag);
+            for (int k = 0; k < tiles && !bad; ++k, ++it) {
+                const uint32_t d = tm + 64 * (it & 1);
+                if (it > 1) bad = !warp_wait(&sh.s_free[it & 1], ((it >> 1) - 1) & 1, abort_flag);
+                // in two halves: the first runs while the second arrives
+                const uint32_t q_low = uniform(desc_low(q, 16));
+                const uint32_t k_low = uniform(desc_low(kv + st * stage_bytes, 16));
+                if (bad || !warp_wait(&sh.full[st][0], par, abort_flag)) {
+                    bad = true;
+                    break;
                 }
-                mma_commit(&sh.s_full[it & 1]);
-                return true;
-            };
-            int it = 0, seg = 0;
-            Segment s = walk.more() ? segment(a, walk, KT) : Segment{};
-            if (walk.more()) bad = !scores(0, 0, true);
-            while (walk.more() && !bad) {
-                for (int k = s.first; k < s.end && !bad; ++k, ++it) {
-                    // the next tile's scores first; the first of the next segment
-                    // only behind this segment's last values, since they wait for
-                    // other queries
-                    if (k + 1 < s.end) bad = !scores(it + 1, seg, false);
-                    if (bad || !mbar_wait(&sh.p_full, it & 1, abort_flag)) {
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t rope = (2 * pairs * kChunk) >> 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mma_ss(d, desc_of(q_low + rope + 2 * i), desc_of(k_low + rope + 2 * i), desc,
+                               i > 0);
+                    score_pairs(d, q_low, k_low, desc, 0, front);
+                    // the copying warps' writes (which this warp has waited for) are
+                    // ordered before the softmax's reads by an arrival of its own
+                    mbar_arrive(&sh.s_full[it & 1]);
+                }
+                __syncwarp();
+                if (front < pairs) {
+                    if (!warp_wait(&sh.full[st][1], par, abort_flag)) {
                         bad = true;
                         break;
                     }
                     tc_fence_after();
-                    const int st = it % L.stages;
-                    const uint32_t v = kv + st * L.chunks * kChunk;
+                }
+                if (elect_one()) {
+                    score_pairs(d, q_low, k_low, desc, front, pairs);
+                    mma_commit(&sh.s_full[it & 1]);
+                    if (k + 1 == tiles) mma_commit(&sh.q_free);
+                }
+                __syncwarp();
+                if (++st == L.stages) {
+                    st = 0;
+                    par ^= 1;
+                }
+            }
+            advance(walk, s);
+            ++seg;
+        }
+        if (bad) drain(&sh.drain[0], &sh.abort);
+    } else if (warp == 5) {
+        // ------------------------------------------------------------ values
+        const uint32_t desc = mma_desc(128, N, kAMn);
+        const uint32_t kv = uniform(smem_u32(sm + L.kv)), tm = uniform(tmem);
+        const uint32_t p_low = uniform(desc_low(smem_u32(sm + L.p), 16));
+        int it = 0, st = 0;
+        while (uniform((int)walk.more()) && !bad) {
+            const Segment s = segment(a, walk, KT);
+            const int tiles = uniform(s.end - s.first);
+            for (int k = 0; k < tiles && !bad; ++k, ++it) {
+                if (!warp_wait(&sh.p_full, it & 1, abort_flag)) {
+                    bad = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t v_low = uniform(desc_low(kv + st * stage_bytes, kChunk));
+                if (elect_one()) {
+#pragma unroll 1
                     for (int j = 0; j < pairs; ++j) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            mma_ss(tmem + j * N, smem_desc(v + 2 * j * kChunk + i * 2048, kChunk),
-                                   smem_desc(p + i * 32, 16), odesc, k > s.first || i > 0);
+                            mma_ss(tm + j * N, desc_of(v_low + ((2 * j * kChunk + i * 2048) >> 4)),
+                                   desc_of(p_low + i * 2), desc, i > 0 || k > 0);
+                        mma_commit(&sh.empty[st][j]);
                     }
-                    mma_commit(&sh.empty[st]);
                     mma_commit(&sh.pv_done);
                 }
-                if (bad) break;
-                advance(walk, s);
-                ++seg;
-                if (walk.more()) {
-                    s = segment(a, walk, KT);
-                    bad = !scores(it, seg, true);
-                }
+                __syncwarp();
+                if (++st == L.stages) st = 0;
             }
-            if (bad) {
-                sh.abort = 1;
-                mma_commit(&sh.drain);
-                const unsigned long long since = global_timer_ns();
-                while (!mbar_try_wait(&sh.drain, 0) && global_timer_ns() - since < kWaitLimitNs) {
-                }
-            }
+            advance(walk, s);
         }
-        __syncwarp();
+        if (bad) drain(&sh.drain[1], &sh.abort);
     } else {
         // ------------------------------------------------------------ softmax
-        // A 64-row accumulator lies on lanes 0-15 of every warp's quarter.
-        const int row = 16 * warp + (lane & 15);
-        const bool live = lane < 16 && row < nrows;
+        // A 64-row accumulator lies on lanes 0-15 of every warp's quarter, and four
+        // threads share a row (16 keys of it each): thread i has rows i / 4 and
+        // i / 4 + 8 of its warp's sixteen.
+        const int quad = lane & 3;
         const uint32_t quarter = (uint32_t)(32 * warp) << 16;
-        const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(a.q_latent);
-        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q_rope);
-        // Query rows of sequence b into the swizzled tile.  Rows at and behind
-        // nrows are not written: their scores and outputs are never read.
-        auto load_q = [&](int b) {
-            const int vecs = L.chunks * 8;
-            for (int i = tid; i < nrows * vecs; i += kSoftmax) {
-                const int r = i / vecs, v = i % vecs, c = v >> 3, j = v & 7;
-                const size_t at = (size_t)b * a.rows + row0 + r;
-                const uint4 x = __ldg(reinterpret_cast<const uint4*>(
-                    c < 2 * pairs ? ql + at * a.R + 8 * v : qr + at * 64 + 8 * j));
-                *reinterpret_cast<uint4*>(sm + L.q + c * kChunk + r * 128 + ((j ^ (r & 7)) << 4)) = x;
-            }
-            fence_async_smem();
-            mbar_arrive(&sh.q_full);
-        };
-        int it = 0;
-        if (walk.more()) load_q(walk.b);
+        const int rows[2] = {16 * warp + (lane >> 2), 16 * warp + (lane >> 2) + 8};
+        const bool busy = 16 * warp < nrows;  // the warp has rows at all
+        // The largest score is the largest product where the scale is positive;
+        // products change sign where it is negative, and a scale of zero is a very
+        // small one.
+        const bool flip = a.qscale < 0.f;
+        const float qs = fmaxf(fabsf(a.qscale), 1e-30f);
+        // where this lane's row of a group of four 8 x 8 weight tiles goes
+        const int prow = 16 * warp + 8 * ((lane >> 3) & 1) + (lane & 7);
+        const uint32_t p_row = smem_u32(sm + L.p) + prow * 128;
+        const uint32_t p_group = lane >> 4, p_swizzle = lane & 7;
+        int it = 0, st = 0;
+        uint32_t par = 0;
         while (walk.more()) {
             const Segment s = segment(a, walk, KT);
-            // newest key that the row sees
-            const int last = live ? s.seq.n - a.T + (row0 + row) / a.H : -1;
-            float m = -INFINITY, l = 0.f;
+            int last[2];  // newest key that the row sees
+            float m[2], l[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                last[h] = rows[h] < nrows ? s.seq.n - a.T + (row0 + rows[h]) / a.H : 0x3fffffff;
+                m[h] = -INFINITY;
+                l[h] = 0.f;
+            }
             for (int k = s.first; k < s.end; ++k, ++it) {
-                const int st = it % L.stages;
-                const uint32_t par = (it / L.stages) & 1;
-                if (!mbar_wait(&sh.full[st][0], par, abort_flag)) bad = true;
                 if (!mbar_wait(&sh.s_full[it & 1], (it >> 1) & 1, abort_flag)) bad = true;
                 __syncwarp();
                 tc_fence_after();
-                float x[kTile];
-                tmem_ld32(tmem_s + 64 * (it & 1) + quarter, reinterpret_cast<uint32_t*>(x));
-                tmem_ld32(tmem_s + 64 * (it & 1) + 32 + quarter,
-                          reinterpret_cast<uint32_t*>(x + 32));
-                tmem_wait_ld();
-                const unsigned long long valid = sh.valid[st];
-                const int lim = last - k * KT;  // keys 0 .. lim of the tile
-                const unsigned long long sees =
-                    valid & (lim >= 63 ? ~0ull : lim < 0 ? 0ull : (2ull << lim) - 1ull);
-                float mt = -INFINITY;
-                if (__all_sync(0xffffffffu, sees == ~0ull || !live)) {
+                float x[32];
+                float mn[2] = {m[0], m[1]};
+                bool need = false;
+                const unsigned long long valid = sh.valid[it % kValid];
+                if (busy) {
+                    tmem_ld16x64(tmem_s + 64 * (it & 1) + quarter, reinterpret_cast<uint32_t*>(x));
+                    tmem_wait_ld();
+                    tc_fence_before();
+                }
+                mbar_arrive(&sh.s_free[it & 1]);
+                if (busy) {
+                    if (flip) {
 #pragma unroll
-                    for (int i = 0; i < kTile; ++i) {
-                        x[i] *= a.qscale;
-                        mt = fmaxf(mt, x[i]);
+                        for (int i = 0; i < 32; ++i) x[i] = -x[i];
                     }
-                } else {
+                    unsigned long long sees[2];
 #pragma unroll
-                    for (int i = 0; i < kTile; ++i) {
-                        x[i] = (sees >> i) & 1ull ? x[i] * a.qscale : -INFINITY;
-                        mt = fmaxf(mt, x[i]);
+                    for (int h = 0; h < 2; ++h) {
+                        const int lim = last[h] - k * KT;  // keys 0 .. lim of the tile
+                        sees[h] = valid & (lim >= 63 ? ~0ull : lim < 0 ? 0ull : (2ull << lim) - 1ull);
+                    }
+                    if (!__all_sync(0xffffffffu, (sees[0] & sees[1]) == ~0ull)) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const unsigned long long z = sees[h] >> (2 * quad);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (!((z >> (8 * (i >> 1) + (i & 1))) & 1ull))
+                                    x[4 * (i >> 1) + 2 * h + (i & 1)] = -INFINITY;
+                        }
+                    }
+                    float mx[2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mx[h][i] = fmaxf(fmaxf(x[4 * i + 2 * h], x[4 * i + 2 * h + 1]),
+                                             fmaxf(x[4 * i + 16 + 2 * h], x[4 * i + 17 + 2 * h]));
+                        mn[h] = fmaxf(fmaxf(mx[h][0], mx[h][1]), fmaxf(mx[h][2], mx[h][3]));
+                    }
+#pragma unroll
+                    for (int d = 1; d < 4; d <<= 1)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            mn[h] = fmaxf(mn[h], __shfl_xor_sync(0xffffffffu, mn[h], d));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mn[h] = fmaxf(m[h], mn[h] * qs);
+                        if (k == s.first) m[h] = mn[h];
+                        need |= rows[h] < nrows && mn[h] > m[h] + kSkip;
                     }
                 }
-                const float mn = fmaxf(m, mt);
-                const bool need = live && k > s.first && mn > m + kSkip;
-                if (k == s.first) m = mn;
                 bool waited = false;
                 if (bar_any(1, kSoftmax, need || bad)) {
                     if (it > 0 && !mbar_wait(&sh.pv_done, (it - 1) & 1, abort_flag)) bad = true;
                     waited = true;
-                    const float fac = need ? exp2f(m - mn) : 1.f;
-                    if (need) m = mn;
-                    l *= fac;
-                    if (lane < 16) sh.factor[row] = fac;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const bool up = mn[h] > m[h] + kSkip;
+                        const float fac = up ? exp2f(m[h] - mn[h]) : 1.f;
+                        if (up) m[h] = mn[h];
+                        l[h] *= fac;
+                        if (quad == 0) sh.factor[rows[h]] = fac;
+                    }
                     __syncwarp();
                     if (bar_any(1, kSoftmax, bad)) {
                         bad = true;
@@ -369,36 +574,42 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                         float o[16];
                         tmem_ld16(tmem + c + quarter, o);
                         tmem_wait_ld();
+                        const float* fac = sh.factor + c % N;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] *= sh.factor[c % N + i];
+                        for (int i = 0; i < 16; ++i) o[i] *= fac[i];
                         tmem_st16(tmem + c + quarter, o);
                     }
                     tmem_wait_st();
                 }
-                const float base = m == -INFINITY ? 0.f : m;
-                uint32_t p[kTile / 2];
-                float sum = 0.f;
+                uint32_t p[2][8];
+                if (busy) {
 #pragma unroll
-                for (int i = 0; i < kTile; i += 2) {
-                    const float e0 = fast_exp2(x[i] - base), e1 = fast_exp2(x[i + 1] - base);
-                    sum += e0 + e1;
-                    p[i / 2] = pack_bf16(e0, e1);
+                    for (int h = 0; h < 2; ++h) {
+                        const float base = m[h] == -INFINITY ? 0.f : m[h];
+                        float sum[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int g8 = 0; g8 < 8; ++g8) {
+                            const float e0 = fast_exp2(fmaf(x[4 * g8 + 2 * h], qs, -base));
+                            const float e1 = fast_exp2(fmaf(x[4 * g8 + 2 * h + 1], qs, -base));
+                            sum[g8 & 1] += e0 + e1;
+                            p[h][g8] = pack_bf16(e0, e1);
+                        }
+                        l[h] += sum[0] + sum[1];
+                    }
                 }
-                l += sum;
                 if (!waited && it > 0 && !mbar_wait(&sh.pv_done, (it - 1) & 1, abort_flag))
                     bad = true;
-                if (live) {
+                __syncwarp();
+                if (busy) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(sm + L.p + row * 128 + ((j ^ (row & 7)) << 4)) =
-                            make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+                    for (int i = 0; i < 4; ++i)
+                        stsm_x4(p_row + (((2 * i + p_group) ^ p_swizzle) << 4), p[0][2 * i],
+                                p[1][2 * i], p[0][2 * i + 1], p[1][2 * i + 1]);
                 }
                 if (valid != ~0ull) {
                     // rows that hold no token of the sequence: a weight of zero does
                     // not keep what they contain (NaN) out of the sum
-                    for (int j = 1; j < pairs; ++j)
-                        if (!mbar_wait(&sh.full[st][j], par, abort_flag)) bad = true;
-                    unsigned char* v = sm + L.kv + st * L.chunks * kChunk;
+                    unsigned char* v = sm + L.kv + st * stage_bytes;
                     for (int i = tid; i < 2 * pairs * kTile * 8; i += kSoftmax) {
                         const int r = (i >> 3) & 63;
                         if (!((valid >> r) & 1ull))
@@ -409,19 +620,38 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                 fence_async_smem();
                 tc_fence_before();
                 mbar_arrive(&sh.p_full);
+                if (++st == L.stages) {
+                    st = 0;
+                    par ^= 1;
+                }
             }
             __syncwarp();
             if (bar_any(1, kSoftmax, bad)) {
                 bad = true;
                 break;
             }
-            // the segment's score MMAs are complete: the next segment's queries may
-            // replace its own
             const int b = walk.b;
             const bool head = walk.t == t0;
             const int before = walk.before;
             advance(walk, s);
-            if (walk.more()) load_q(walk.b);
+            const bool whole = s.first == 0 && s.end == s.nt;
+            const size_t slot = ((size_t)w * a.groups + g) * 2 + (head ? 0 : 1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+                if (quad == 0) sh.factor[rows[h]] = l[h] == 0.f ? 0.f : 1.f / l[h];
+                if (quad == 0 && rows[h] < nrows) {
+                    const float z = l[h] > 0.f ? m[h] + log2f(l[h]) : (l[h] == 0.f ? -INFINITY : NAN);
+                    if (!whole)
+                        a.part_lse[slot * a.rpg + rows[h]] = z;
+                    else if (a.lse_out)
+                        a.lse_out[(size_t)b * a.rows + row0 + rows[h]] = z * kLn2;
+                }
+            }
+            if (g == 0 && tid == 0 && s.first == 0)
+                a.meta[b] = make_int4(w, worker_of(before + s.nt - 1, walk.tot, walk.W),
+                                      head ? 0 : 1, 0);
             if (it > 0 && !mbar_wait(&sh.pv_done, (it - 1) & 1, abort_flag)) bad = true;
             __syncwarp();
             if (bar_any(1, kSoftmax, bad)) {
@@ -429,38 +659,19 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                 break;
             }
             tc_fence_after();
-            const bool whole = s.first == 0 && s.end == s.nt;
-            const size_t slot = ((size_t)w * a.groups + g) * 2 + (head ? 0 : 1);
-            if (lane < 16) sh.factor[row] = l == 0.f ? 0.f : 1.f / l;
-            if (live) {
-                const float z = l > 0.f ? m + log2f(l) : (l == 0.f ? -INFINITY : NAN);
-                if (!whole)
-                    a.part_lse[slot * a.rpg + row] = z;
-                else if (a.lse_out)
-                    a.lse_out[(size_t)b * a.rows + row0 + row] = z * kLn2;
-            }
-            if (g == 0 && tid == 0 && s.first == 0)
-                a.meta[b] = make_int4(w, worker_of(before + s.nt - 1, walk.tot, walk.W),
-                                      head ? 0 : 1, 0);
-            bar_sync(1, kSoftmax);
-            for (int j = 0; j < pairs; ++j) {
-                const int d = 128 * j + 32 * warp + lane;
-                for (int c = 0; c < nrows; c += 16) {
-                    float o[16];
-                    tmem_ld16(tmem + j * N + c + quarter, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (c + i >= nrows) continue;
-                        const float y = o[i] * sh.factor[c + i];
-                        if (whole)
-                            static_cast<__nv_bfloat16*>(
-                                a.out)[((size_t)b * a.rows + row0 + c + i) * a.R + d] =
-                                __float2bfloat16_rn(y);
-                        else
-                            a.part_o[(slot * a.rpg + c + i) * a.R + d] = y;
-                    }
-                }
+            // 32 lanes are 32 consecutive dims: every store is a whole 64- or
+            // 128-byte line part
+            const int d = 32 * warp + lane;
+            if (whole) {
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) +
+                                   ((size_t)b * a.rows + row0) * a.R + d;
+                store_rows(tmem + quarter, pairs, N, nrows, sh.factor, a.R, [&](size_t at, float y) {
+                    o[at] = __float2bfloat16_rn(y);
+                });
+            } else {
+                float* o = a.part_o + slot * a.rpg * a.R + d;
+                store_rows(tmem + quarter, pairs, N, nrows, sh.factor, a.R,
+                           [&](size_t at, float y) { o[at] = y; });
             }
             tc_fence_before();
         }
@@ -474,20 +685,27 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
 }  // namespace
 
 // Keys of a copy box: the largest divisor of the page size not above a tile.
-int latent_piece(int BS) {
+static int latent_piece(int BS) {
     int t = BS < kTile ? BS : kTile;
     while (BS % t) --t;
     return t;
 }
 
-cudaError_t launch_latent_mma(const LatentArgs& a, const CUtensorMap& lmap, const CUtensorMap& rmap,
-                              cudaStream_t stream) {
+cudaError_t launch_latent_mma(const LatentArgs& a, cudaStream_t stream) {
+    const int piece = latent_piece(a.BS), N = (a.rpg + 15) / 16 * 16;
+    const long long rows = (long long)a.NB * a.BS, qrows = (long long)a.Q * a.rows;
+    CUtensorMap lmap, rmap, qlmap, qrmap;
+    cudaError_t e = encode_rows(&lmap, a.latent, a.R, a.R, rows, piece, piece == kTile ? 2 : 1);
+    if (e == cudaSuccess) e = encode_rows(&rmap, a.rope, a.P, a.P, rows, piece, 1);
+    if (e == cudaSuccess) e = encode_rows(&qlmap, a.q_latent, a.R, a.R, qrows, N, 1);
+    if (e == cudaSuccess) e = encode_rows(&qrmap, a.q_rope, a.P, a.P, qrows, N, 1);
+    if (e != cudaSuccess) return e;
     const MmaLayout L(a.R);
-    const cudaError_t e = cudaFuncSetAttribute(
-        latent_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+    e = cudaFuncSetAttribute(latent_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             L.total);
     if (e != cudaSuccess) return e;
     return launch_pdl(latent_mma_kernel, dim3(a.groups, a.workers), dim3(kThreads), L.total, stream,
-                      a, latent_piece(a.BS), lmap, rmap);
+                      a, piece, lmap, rmap, qlmap, qrmap);
 }
 
 }  // namespace kvd

@@ -362,31 +362,57 @@ __global__ void __launch_bounds__(128) latent_combine_kernel(const LatentArgs a)
     const int4 meta = a.meta[b];
     const int w0 = meta.x, w1 = meta.y;
     if (w0 == w1) return;
+    // a launch that gave up on a wait may have left no division behind
+    if (w0 < 0 || w1 < w0 || w1 >= a.workers || (meta.z & ~1)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x, g = row / a.rpg, r = row % a.rpg;
     const int d = 128 * warp + 4 * lane;
     if (128 * warp >= a.R) return;
-    float M = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 32) {
-        const size_t slot = ((size_t)w * a.groups + g) * 2 + (w == w0 ? meta.z : 0);
-        M = fmaxf(M, a.part_lse[slot * a.rpg + r]);
-    }
-#pragma unroll
-    for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
-    const float base = M == -INFINITY ? 0.f : M;
+    // a lane a worker: its log-sum-exp, then its weight; 32 workers at a time
+    // against a running maximum
+    const float* base_o = a.part_o + d;
+    float M = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int w = w0; w <= w1; ++w) {
-        const size_t slot = ((size_t)w * a.groups + g) * 2 + (w == w0 ? meta.z : 0);
-        const float e = exp2f(a.part_lse[slot * a.rpg + r] - base);
-        const float4 x = *reinterpret_cast<const float4*>(a.part_o + (slot * a.rpg + r) * a.R + d);
-        l += e;
-        acc.x = fmaf(e, x.x, acc.x);
-        acc.y = fmaf(e, x.y, acc.y);
-        acc.z = fmaf(e, x.z, acc.z);
-        acc.w = fmaf(e, x.w, acc.w);
+    for (int wb = w0; wb <= w1; wb += 32) {
+        const int w = wb + lane, n = min(32, w1 - wb + 1);
+        const int slot = (w * a.groups + g) * 2 + (w == w0 ? meta.z : 0);
+        const float z = w <= w1 ? a.part_lse[(size_t)slot * a.rpg + r] : -INFINITY;
+        float top = z;
+#pragma unroll
+        for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        top = fmaxf(top, M);
+        const float base = top == -INFINITY ? 0.f : top;
+        const float corr = exp2f(M - base), e = exp2f(z - base);
+        M = top;
+        l *= corr;
+        acc.x *= corr;
+        acc.y *= corr;
+        acc.z *= corr;
+        acc.w *= corr;
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            float4 x[8];
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int from = min(i0 + i, n - 1);
+                const int sl = __shfl_sync(0xffffffffu, slot, from);
+                f[i] = __shfl_sync(0xffffffffu, e, from);
+                if (i0 + i >= n) f[i] = 0.f;
+                x[i] = i0 + i < n ? *reinterpret_cast<const float4*>(
+                                        base_o + ((size_t)sl * a.rpg + r) * a.R)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                l += f[i];
+                acc.x = fmaf(f[i], x[i].x, acc.x);
+                acc.y = fmaf(f[i], x[i].y, acc.y);
+                acc.z = fmaf(f[i], x[i].z, acc.z);
+                acc.w = fmaf(f[i], x[i].w, acc.w);
+            }
+        }
     }
+    const float base = M == -INFINITY ? 0.f : M;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const size_t at = (size_t)b * a.rows + row;
     ElemTraits<Out>::store4(a.out, at * a.R + d,

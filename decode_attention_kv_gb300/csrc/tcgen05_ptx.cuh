@@ -63,6 +63,31 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* u) {
         : "r"(addr));
 }
 
+// 16 lanes x 64 columns, as the accumulators of m16n8 tiles: thread i holds, of
+// the columns 8 g + 2 (i % 4) and the one behind it, lane i / 4 in u[4 g],
+// u[4 g + 1] and lane i / 4 + 8 in u[4 g + 2], u[4 g + 3].
+__device__ __forceinline__ void tmem_ld16x64(uint32_t addr, uint32_t* u) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+          "=r"(u[14]), "=r"(u[15]), "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]),
+          "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]), "=r"(u[25]),
+          "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(addr));
+}
+
+// Four 8 x 8 tiles of 16-bit elements (the layout above, packed in pairs) to
+// shared memory; lane i gives the address of row i % 8 of tile i / 8.
+__device__ __forceinline__ void stsm_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                        uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&r)[16]) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
     asm volatile(
@@ -93,9 +118,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* u) {
 // of the inner dimension a row) that is the K-major form and `lead` is unused;
 // with rows along the inner dimension (64 elements of M or N a row) it is the
 // MN-major form and `lead` is the distance of the next 64 elements.
+//
+// The upper word is constant; the lower one takes byte offsets as (offset >> 4).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) {
+    return ((addr & 0x3ffffu) >> 4) | ((lead >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t low) {
+    return ((uint64_t)kDescHigh << 32) | low;
+}
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
-           ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) | (2ull << 61);
+    return desc_of(desc_low(addr, lead));
 }
 
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N.
@@ -106,7 +139,21 @@ __host__ __device__ constexpr uint32_t mma_desc(int M, int N, uint32_t major = 0
            ((uint32_t)(M >> 4) << 24);
 }
 
-// D (+)= A * B, inner dimension 16; one thread issues it.
+// One thread of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// A value that is the same in every lane, in a form the compiler knows to be:
+// MMA operands live in uniform registers.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// D (+)= A * B, inner dimension 16; one elected thread issues a batch.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
                                        bool accumulate) {
     asm volatile(
