@@ -179,6 +179,13 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
     return p;
 }
 
+// L2 policy for data that other CTAs read again.
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 // ------------------------------------------------------------ packed fp32x2
 
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {

@@ -37,7 +37,7 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // How kvd_attend_latent divides a call (a function of the sizes only).
 struct LatentPlan {
-    int groups, rpg, workers, min_tiles;
+    int groups, rpg, workers, min_tiles, lead;
     size_t off_lse, off_o, bytes;
 };
 
@@ -58,7 +58,8 @@ kvd_status latent_plan(const char* fn, int Q, int T, int H, int BS, int cols, in
     pl->groups = (rows + most - 1) / most;
     pl->rpg = (rows + pl->groups - 1) / pl->groups;
     pl->workers = pl->groups < ctas ? ctas / pl->groups : 1;
-    pl->min_tiles = 2;
+    pl->min_tiles = mma ? 2 : 1;
+    pl->lead = mma ? 2 : 1;
     const size_t slots = (size_t)pl->workers * pl->groups * 2;
     pl->off_lse = round256((size_t)(Q < 1 ? 1 : Q) * sizeof(int4));
     pl->off_o = pl->off_lse + round256(slots * pl->rpg * 4);
@@ -157,6 +158,7 @@ kvd_status kvd_attend_latent(const void* q_latent, const void* q_rope, const voi
     a.rpg = pl.rpg;
     a.workers = pl.workers;
     a.min_tiles = pl.min_tiles;
+    a.lead = pl.lead;
     a.meta = reinterpret_cast<int4*>(ws);
     a.part_lse = reinterpret_cast<float*>(ws + pl.off_lse);
     a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
@@ -179,8 +181,8 @@ kvd_status kvd_attend_expanded(const void* q, const void* kv, const void* k_rope
         return fail(KVD_ERR_UNSUPPORTED, "%s: Dn = %d, Dv = %d, P = %d (supported: 64 or 128, 64 or 128, 64)",
                     fn, Dn, Dv, P);
     if (H > 65535) return fail(KVD_ERR_UNSUPPORTED, "%s: H > 65535", fn);
-    if (Nq > (1 << 30) || Nk > (1 << 30) || Q > (1 << 30))
-        return fail(KVD_ERR_UNSUPPORTED, "%s: Q, Nq or Nk > 2^30", fn);
+    if (Nq > (1 << 23) || Nk > (1 << 30) || Q > (1 << 14))
+        return fail(KVD_ERR_UNSUPPORTED, "%s: Q > 2^14, Nq > 2^23 or Nk > 2^30", fn);
     if (Q == 0 || Nq == 0) return ok();
     if (!q || !q_lens || !k_lens || !out || (Nk > 0 && (!kv || !k_rope)))
         return fail(KVD_ERR_INVALID_ARG, "%s: null pointer", fn);
@@ -206,7 +208,8 @@ kvd_status kvd_attend_expanded(const void* q, const void* kv, const void* k_rope
     a.P = P;
     a.qscale = scale * kLog2e;
     a.causal = causal != 0;
-    return launched(fn, launch_expanded_simt(a, dtype, (cudaStream_t)stream));
+    return launched(fn, dtype == KVD_BF16 ? launch_expanded_mma(a, (cudaStream_t)stream)
+                                          : launch_expanded_simt(a, dtype, (cudaStream_t)stream));
 }
 
 kvd_status kvd_verify_drafts(const void* target_probs, const void* draft_probs,

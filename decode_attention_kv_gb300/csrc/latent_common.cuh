@@ -8,7 +8,9 @@
 // the first and the last sequence of a run can be shared with other workers,
 // so a worker leaves at most two partial results (slots 2w and 2w + 1) and
 // every other sequence of its run goes straight to the output.  A grid of one
-// CTA per SM is then balanced to one tile, whatever the lengths are.
+// CTA per SM is then balanced to one tile, whatever the lengths are.  A sequence
+// counts `lead` tiles more than it has, laid before its first one: what a run
+// spends on starting and finishing it.
 #pragma once
 
 #include "kvd_device.cuh"
@@ -34,6 +36,7 @@ struct LatentArgs {
     int groups, rpg;        // row groups of a sequence, rows per group
     int workers;            // W at most (the grid's x extent)
     int min_tiles;          // fewest tiles worth a worker of its own
+    int lead;               // tiles that a sequence counts above its own
     int4* meta;             // [Q] first worker, last worker, first slot's parity
     float* part_lse;        // [workers * groups * 2, rpg], log2 units
     float* part_o;          // [workers * groups * 2, rpg, R], normalised
@@ -204,6 +207,7 @@ __device__ __forceinline__ PackedSeq packed_seq(const ExpandedArgs& a, int b) {
     return s;
 }
 
+cudaError_t launch_expanded_mma(const ExpandedArgs& a, cudaStream_t stream);
 cudaError_t launch_expanded_simt(const ExpandedArgs& a, kvd_dtype dt, cudaStream_t stream);
 
 cudaError_t launch_append_latent(void* latent, void* rope, const void* latent_new,

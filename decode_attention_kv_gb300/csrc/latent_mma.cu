@@ -81,13 +81,16 @@ __device__ __forceinline__ Segment segment(const LatentArgs& a, const Walk& k, i
     Segment s;
     s.seq = latent_seq(a, k.b);
     s.nt = max(1, (s.seq.n + KT - 1) / KT);
-    s.first = k.t - k.before;
-    s.end = min(s.nt, k.t1 - k.before);
+    // the run's part of the sequence's places: `lead` of them, then its tiles
+    s.first = max(0, k.t - k.before - a.lead);
+    s.end = min(s.nt, k.t1 - k.before - a.lead);
     return s;
 }
-__device__ __forceinline__ void advance(Walk& k, const Segment& s) {
-    k.t = k.before + s.end;
-    k.before += s.nt;
+// To the next sequence; a run that ends before that one's first tile is over.
+__device__ __forceinline__ void advance(const LatentArgs& a, Walk& k, const Segment& s) {
+    k.before += a.lead + s.nt;
+    k.t = min(k.before, k.t1);
+    if (k.t1 <= k.before + a.lead) k.t = k.t1;
     ++k.b;
 }
 
@@ -162,7 +165,7 @@ __device__ __forceinline__ void drain(uint64_t* bar, int* abort_flag) {
     __syncwarp();
 }
 
-__global__ void __maxnreg__(128)
+__global__ void __maxnreg__(144)
 latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ CUtensorMap lmap,
                   const __grid_constant__ CUtensorMap rmap,
                   const __grid_constant__ CUtensorMap qlmap,
@@ -224,7 +227,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
         [&](int b) {
             const SeqInfo s = latent_seq(a, b);
             if (s.bad && g == 0 && w == 0) report(a.dev_status, s.bad);
-            return max(1, (s.n + KT - 1) / KT);
+            return a.lead + max(1, (s.n + KT - 1) / KT);
         });
     const bool some = f.item < a.Q;
     walk.b = f.item;
@@ -232,6 +235,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
     walk.tot = f.total;
     walk.t = some ? run_start(w, f.total, walk.W) : 0;
     walk.t1 = some ? run_start(w + 1, f.total, walk.W) : 0;
+    if (walk.t1 <= walk.before + a.lead) walk.t = walk.t1;  // no tile of its first sequence
     const int t0 = walk.t;
     bool bad = false;
 
@@ -255,7 +259,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                 tma_g2s_3d(sm + L.q + 2 * pairs * kChunk, &qrmap, 0, row, 0, &sh.q_full, policy);
             }
             __syncwarp();
-            advance(walk, s);
+            advance(a, walk, s);
             ++seg;
         }
         if (seg > 0) {  // nothing of its own may be in flight when it leaves
@@ -362,7 +366,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                     par ^= 1;
                 }
             }
-            advance(walk, s);
+            advance(a, walk, s);
         }
         if (bad) {  // a wait ran out: leave only when the copies in flight have landed
             if (lane == 0) sh.abort = 1;
@@ -429,7 +433,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                     par ^= 1;
                 }
             }
-            advance(walk, s);
+            advance(a, walk, s);
             ++seg;
         }
         if (bad) drain(&sh.drain[0], &sh.abort);
@@ -463,7 +467,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                 __syncwarp();
                 if (++st == L.stages) st = 0;
             }
-            advance(walk, s);
+            advance(a, walk, s);
         }
         if (bad) drain(&sh.drain[1], &sh.abort);
     } else {
@@ -633,7 +637,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
             const int b = walk.b;
             const bool head = walk.t == t0;
             const int before = walk.before;
-            advance(walk, s);
+            advance(a, walk, s);
             const bool whole = s.first == 0 && s.end == s.nt;
             const size_t slot = ((size_t)w * a.groups + g) * 2 + (head ? 0 : 1);
 #pragma unroll
@@ -650,7 +654,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                 }
             }
             if (g == 0 && tid == 0 && s.first == 0)
-                a.meta[b] = make_int4(w, worker_of(before + s.nt - 1, walk.tot, walk.W),
+                a.meta[b] = make_int4(w, worker_of(before + a.lead + s.nt - 1, walk.tot, walk.W),
                                       head ? 0 : 1, 0);
             if (it > 0 && !mbar_wait(&sh.pv_done, (it - 1) & 1, abort_flag)) bad = true;
             __syncwarp();

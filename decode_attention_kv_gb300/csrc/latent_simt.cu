@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
         [&](int b) {
             const SeqInfo s = latent_seq(a, b);
             if (s.bad && g == 0 && w == 0) report(a.dev_status, s.bad);
-            return max(1, (s.n + kKeys - 1) / kKeys);
+            return a.lead + max(1, (s.n + kKeys - 1) / kKeys);
         });
     if (f.item >= a.Q) return;
     const int t0 = run_start(w, f.total, W), t1 = run_start(w + 1, f.total, W);
@@ -193,7 +193,9 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
     for (int t = t0; t < t1; ++b) {
         const SeqInfo seq = latent_seq(a, b);
         const int nt = max(1, (seq.n + kKeys - 1) / kKeys);
-        const int first = t - before, end = min(nt, t1 - before);
+        // the run's part of the sequence's places: `lead` of them, then its tiles
+        const int first = max(0, t - before - a.lead), end = min(nt, t1 - before - a.lead);
+        if (end <= first) break;  // the run ends before the first tile
         // the group's queries
         for (int i = tid; i < kRows * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = 4 * (i % (D / 4));
@@ -268,10 +270,11 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
                 a.lse_out[(size_t)b * a.rows + row0 + tid] = z * kLn2;
         }
         if (g == 0 && tid == 0 && first == 0)
-            a.meta[b] = make_int4(w, worker_of(before + nt - 1, f.total, W), t == t0 ? 0 : 1, 0);
+            a.meta[b] = make_int4(w, worker_of(before + a.lead + nt - 1, f.total, W),
+                                  t == t0 ? 0 : 1, 0);
         __syncthreads();
-        t = before + end;
-        before += nt;
+        before += a.lead + nt;
+        t = before;
     }
 }
 
