@@ -13,7 +13,9 @@ namespace cg = cooperative_groups;
 // ------------------------------------------------------------ append_latent
 // One warp a row: 16-byte vectors of the latent row, then of the rotary row.
 // The sequence of a packed row comes from a binary search in new_lens.  The
-// row's own loads do not depend on the search, so they are issued first.
+// row's own loads do not depend on the search, so they are issued first.  (2, 4
+// and 8 rows a warp copied 21000 rows of 1152 bytes no faster: 11.2, 11.9 and
+// 13.3 against 11.1 us.)
 constexpr int kAppendWarps = 8;
 constexpr int kAppendVecs = 4;  // vectors a lane holds across the search
 
@@ -92,25 +94,45 @@ append_latent_kernel(unsigned char* __restrict__ latent, unsigned char* __restri
 }
 
 // ------------------------------------------------------------ verify_drafts
-// A cluster of kVerifyCtas CTAs a sequence, a contiguous share of the row each,
-// a contiguous share of that per warp.  Pass 1 sums the weights of every warp's
-// share; the cluster exchanges the sums through distributed shared memory, so
-// every CTA knows where the target sum falls; the one warp whose share holds it
-// reads that share again (from L2) in order.
+// A cluster of 1 to 8 CTAs a sequence (as many as keep the GPU full), a
+// contiguous share of the row per CTA and of that per warp.  The row is read
+// once: every warp sums its share, the CTAs push their sums to one another
+// through distributed shared memory, and the CTA whose share the wanted sum
+// falls into reads that one warp's share again (from L2), first a sixteenth of
+// it per warp, then in order by the warp that holds the place.
 //
 // A sum must decide the same token as one in 64 bits, and 64-bit additions run
 // at a small fraction of the fp32 rate here: the difference p - q is taken
-// exactly as two fp32 words and the running sum is held in two (Knuth's
-// two-sum), about 2^-48 relative, and only the sums of the threads are added in
-// 64 bits.
-constexpr int kVerifyCtas = 8;
+// exactly as two fp32 words and the sums of a share are held in two (Knuth's
+// two-sum), about 2^-48 relative; only the shares' sums are added in 64 bits, by
+// one warp (a 64-bit addition holds an SM's unit for 16 cycles a warp: with all
+// warps at it these few sums took longer than the row).
+constexpr int kVerifyMaxCtas = 8;
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyBatch = 8;  // loads in flight a lane and array
+constexpr int kVerifyBatch = 16;  // elements a lane loads at once
 
-__device__ __forceinline__ float prob(const float* p, size_t i) { return p[i]; }
-__device__ __forceinline__ float prob(const __nv_bfloat16* p, size_t i) {
-    return __uint_as_float((uint32_t)reinterpret_cast<const unsigned short*>(p)[i] << 16);
+__device__ __forceinline__ float as_prob(float x) { return x; }
+__device__ __forceinline__ float as_prob(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// kVerifyBatch elements a lane of [i0, hi): element 32 * VEC * k + VEC * lane + e
+// in x[VEC * k + e]; zeros behind hi.  VEC elements are one 16-byte load.
+template <typename Elem, int VEC>
+__device__ __forceinline__ void load_batch(const Elem* p, int i0, int hi, float (&x)[kVerifyBatch]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < kVerifyBatch / VEC; ++k) {
+        const int i = i0 + 32 * VEC * k + VEC * lane;
+        if constexpr (VEC == 1) {
+            x[k] = i < hi ? as_prob(p[i]) : 0.f;
+        } else {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (i < hi) w = *reinterpret_cast<const uint4*>(p + i);
+            const Elem* e = reinterpret_cast<const Elem*>(&w);
+#pragma unroll
+            for (int z = 0; z < VEC; ++z) x[VEC * k + z] = as_prob(e[z]);
+        }
+    }
 }
 
 // a + b = s + e exactly
@@ -122,95 +144,204 @@ __device__ __forceinline__ float two_sum(float a, float b, float& e) {
 }
 
 // The weight max(p - q, 0) as two words; NaN counts as zero.
+template <bool kRest>
 __device__ __forceinline__ float2 weight(float p, float q) {
+    if (!kRest) return make_float2(p > 0.f ? p : 0.f, 0.f);
     float e;
     const float d = two_sum(p, -q, e);
-    if (!(d > 0.f)) return make_float2(0.f, 0.f);  // d = 0 only where p = q
-    return make_float2(d, isinf(d) ? 0.f : e);
+    const bool some = d > 0.f;  // d = 0 only where p = q
+    return make_float2(some ? d : 0.f, some && d < INFINITY ? e : 0.f);
 }
 
-struct VerifyShared {
-    double warp_sum[kVerifyWarps];
-    double cta_sum;
-    int n, m, bad;
-    int last;          // largest index of this CTA with a positive weight, or -1
-    int warp_last[kVerifyWarps];
-};
-
-// Sum and largest positive index of this warp's share [lo, hi) of the row.
-template <typename Elem, bool kRest>
-__device__ __forceinline__ double share_sum(const Elem* p, const Elem* q, int lo, int hi,
-                                            int& last) {
-    const int lane = threadIdx.x & 31;
+// This warp's sum over [lo, hi), in lane 0 at least.
+template <typename Elem, int VEC, bool kRest>
+__device__ __forceinline__ double share_sum(const Elem* p, const Elem* q, int lo, int hi) {
     float s = 0.f, c = 0.f;
-    last = -1;
     for (int i0 = lo; i0 < hi; i0 += 32 * kVerifyBatch) {
-        float a[kVerifyBatch], b[kVerifyBatch];
+        float a[kVerifyBatch], b[kVerifyBatch] = {};
+        load_batch<Elem, VEC>(p, i0, hi, a);
+        if (kRest) load_batch<Elem, VEC>(q, i0, hi, b);
 #pragma unroll
         for (int k = 0; k < kVerifyBatch; ++k) {
-            const int i = i0 + 32 * k + lane;
-            a[k] = i < hi ? prob(p, i) : 0.f;
-            b[k] = kRest && i < hi ? prob(q, i) : 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < kVerifyBatch; ++k) {
-            const float2 w = weight(a[k], b[k]);
+            const float2 w = weight<kRest>(a[k], b[k]);
             float e;
             s = two_sum(s, w.x, e);
             c += e + w.y;
-            if (w.x > 0.f) last = i0 + 32 * k + lane;
         }
     }
-    double sum = (double)s + (isinf(s) ? 0.0 : (double)c);
+    if (!(s < INFINITY)) c = 0.f;
 #pragma unroll
     for (int k = 16; k; k >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, k);
-        last = max(last, __shfl_xor_sync(0xffffffffu, last, k));
+        float e;
+        const float so = __shfl_xor_sync(0xffffffffu, s, k), co = __shfl_xor_sync(0xffffffffu, c, k);
+        s = two_sum(s, so, e);
+        c += s < INFINITY ? e + co : 0.f;
     }
-    return sum;
+    return (double)s + (s < INFINITY ? (double)c : 0.0);
+}
+
+// Running sums of the first n (at most 32) values, lane by lane.
+__device__ __forceinline__ double lane_sums(double x, int n) {
+    const int lane = threadIdx.x & 31;
+    for (int d = 1; d < n; d <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += o;
+    }
+    return x;
+}
+
+// By one warp: the first of n shares whose running sum, from `border`, is above
+// `want` (the last one where rounding leaves none); `border` becomes its start.
+__device__ __forceinline__ int pick(const double* sums, int n, double want, double& border) {
+    const int lane = threadIdx.x & 31;
+    const double run = border + lane_sums(lane < n ? sums[lane] : 0.0, n);
+    const uint32_t above = __ballot_sync(0xffffffffu, lane < n && run > want);
+    const int w = above ? __ffs(above) - 1 : n - 1;
+    const double prev = __shfl_sync(0xffffffffu, run, w > 0 ? w - 1 : 0);
+    if (w > 0) border = prev;
+    return w;
 }
 
 // The first index of [lo, hi) whose running sum, from `border`, is above
-// `want`; -1 if there is none.  Steps of 32 elements; the sums of a batch of
-// steps are independent of one another, only the step that holds `want` is
-// summed in order.
+// `want`, or -1: 32 elements at a time, in order, by one warp.
 template <typename Elem, bool kRest>
 __device__ __forceinline__ int find(const Elem* p, const Elem* q, int lo, int hi, double border,
                                     double want) {
     const int lane = threadIdx.x & 31;
-    for (int i0 = lo; i0 < hi; i0 += 32 * kVerifyBatch) {
-        double w[kVerifyBatch], s[kVerifyBatch];
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        const float2 x = weight<kRest>(i < hi ? as_prob(p[i]) : 0.f,
+                                       kRest && i < hi ? as_prob(q[i]) : 0.f);
+        const double w = (double)x.x + (double)x.y;
+        double cum = w;
 #pragma unroll
-        for (int k = 0; k < kVerifyBatch; ++k) {
-            const int i = i0 + 32 * k + lane;
-            const float2 x = weight(i < hi ? prob(p, i) : 0.f, kRest && i < hi ? prob(q, i) : 0.f);
-            s[k] = w[k] = (double)x.x + (double)x.y;
+        for (int d = 1; d < 32; d <<= 1) {
+            const double o = __shfl_up_sync(0xffffffffu, cum, d);
+            if (lane >= d) cum += o;
         }
-#pragma unroll
-        for (int d = 16; d; d >>= 1)
-#pragma unroll
-            for (int k = 0; k < kVerifyBatch; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], d);
-#pragma unroll
-        for (int k = 0; k < kVerifyBatch; ++k) {
-            if (border + s[k] > want) {
-                double cum = w[k];
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const double o = __shfl_up_sync(0xffffffffu, cum, d);
-                    if (lane >= d) cum += o;
-                }
-                const uint32_t above =
-                    __ballot_sync(0xffffffffu, w[k] > 0.0 && border + cum > want);
-                if (above) return i0 + 32 * k + __ffs(above) - 1;
-            }
-            border += s[k];
-        }
+        const uint32_t above = __ballot_sync(0xffffffffu, w > 0.0 && border + cum > want);
+        if (above) return i0 + __ffs(above) - 1;
+        border += __shfl_sync(0xffffffffu, cum, 31);
     }
     return -1;
 }
 
-template <typename Elem>
-__global__ void __cluster_dims__(kVerifyCtas, 1, 1) __launch_bounds__(kVerifyThreads)
+// The largest index below `hi` with a weight above zero, or -1, by one warp.
+template <typename Elem, bool kRest>
+__device__ __forceinline__ int newest(const Elem* p, const Elem* q, int hi) {
+    const int lane = threadIdx.x & 31;
+    for (int i0 = hi; i0 > 0; i0 -= 32) {
+        const int i = i0 - 32 + lane;
+        const bool some = i >= 0 && weight<kRest>(as_prob(p[i]), kRest ? as_prob(q[i]) : 0.f).x > 0.f;
+        const uint32_t any = __ballot_sync(0xffffffffu, some);
+        if (any) return i0 - 32 + 31 - __clz(any);
+    }
+    return -1;
+}
+
+struct VerifyShared {
+    double cta_sum[2][kVerifyMaxCtas];  // of every CTA of the cluster; of p - q, of p
+    double warp_sum[kVerifyWarps];
+    double part_sum[kVerifyWarps];
+    double border, want;
+    int what, share;
+    int n, m, bad;
+};
+
+// Where the wanted sum falls: no sum above zero, a sum that is not finite, not
+// below the total, into this CTA's share, into another's.
+enum : int { kNothing, kRefused, kNewest, kHere, kElsewhere };
+
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The replacement (or the token behind the last draft) from the weights of one
+// row; returns false where they have no sum above zero.
+template <typename Elem, int VEC, bool kRest>
+__device__ __forceinline__ bool sample(VerifyShared& sh, cg::cluster_group& cluster, const Elem* p,
+                                       const Elem* q, int V, float u, int32_t* token,
+                                       int32_t* dev_status) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    // whole vectors to a share
+    const int share = ((V + ctas - 1) / ctas + VEC - 1) / VEC * VEC;
+    const int lo = min(rank * share, V), hi = min(lo + share, V);
+    const int part = ((hi - lo + kVerifyWarps - 1) / kVerifyWarps + VEC - 1) / VEC * VEC;
+    const int wlo = min(lo + warp * part, hi), whi = min(wlo + part, hi);
+    const double sum = share_sum<Elem, VEC, kRest>(p, q, wlo, whi);
+    if (lane == 0) sh.warp_sum[warp] = sum;
+    __syncthreads();
+    double* sums = sh.cta_sum[kRest];
+    if (warp == 0) {
+        const double s = __shfl_sync(
+            0xffffffffu, lane_sums(lane < kVerifyWarps ? sh.warp_sum[lane] : 0.0, kVerifyWarps),
+            kVerifyWarps - 1);
+        if (lane < ctas) *cluster.map_shared_rank(&sums[rank], lane) = s;
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 0) {
+        // the same sums, and so the same choice, in every CTA
+        const double total =
+            __shfl_sync(0xffffffffu, lane_sums(lane < ctas ? sums[lane] : 0.0, ctas), ctas - 1);
+        const double want = (double)u * total;
+        int what = kElsewhere, w = 0;
+        double border = 0.0;
+        if (!(total > 0.0)) {
+            what = kNothing;
+        } else if (!(total < (double)INFINITY)) {
+            what = kRefused;
+        } else if (!(want < total)) {  // u = 1, or rounding
+            what = kNewest;
+        } else if (pick(sums, ctas, want, border) == rank) {
+            what = kHere;
+            w = pick(sh.warp_sum, kVerifyWarps, want, border);
+        }
+        if (lane == 0) {
+            sh.what = what;
+            sh.share = w;
+            sh.border = border;
+            sh.want = want;
+        }
+    }
+    __syncthreads();
+    const int what = sh.what;
+    if (what == kNothing) return false;
+    if (what == kRefused && rank == 0 && tid == 0) {
+        *token = -1;
+        report(dev_status, KVD_DEV_PROBS);
+    }
+    if (what == kNewest && rank == 0 && warp == 0) {
+        const int v = newest<Elem, kRest>(p, q, V);
+        if (lane == 0) *token = v;
+    }
+    if (what != kHere) return true;
+    const int slo = min(lo + sh.share * part, hi), shi = min(slo + part, hi);
+    const int sub = ((shi - slo + kVerifyWarps - 1) / kVerifyWarps + VEC - 1) / VEC * VEC;
+    const double ps = share_sum<Elem, VEC, kRest>(p, q, min(slo + warp * sub, shi),
+                                                  min(slo + (warp + 1) * sub, shi));
+    if (lane == 0) sh.part_sum[warp] = ps;
+    __syncthreads();
+    if (warp == 0) {
+        double border = sh.border;
+        const double want = sh.want;
+        const int z = pick(sh.part_sum, kVerifyWarps, want, border);
+        const int plo = min(slo + z * sub, shi), phi = min(plo + sub, shi);
+        int v = find<Elem, kRest>(p, q, plo, phi, border, want);
+        // rounding between the passes may leave none there
+        if (v < 0) v = newest<Elem, kRest>(p, q, phi);
+        if (v < 0) v = newest<Elem, kRest>(p, q, V);
+        if (lane == 0) *token = v;
+    }
+    return true;
+}
+
+template <typename Elem, int VEC>
+__global__ void __launch_bounds__(kVerifyThreads, 2)
 verify_drafts_kernel(const Elem* __restrict__ target, const Elem* __restrict__ draft,
                      const int32_t* __restrict__ drafts, const float* __restrict__ u_accept,
                      const float* __restrict__ u_sample, const int32_t* __restrict__ num_drafts,
@@ -218,12 +349,12 @@ verify_drafts_kernel(const Elem* __restrict__ target, const Elem* __restrict__ d
                      int32_t* dev_status) {
     __shared__ VerifyShared sh;
     cg::cluster_group cluster = cg::this_cluster();
+    cluster_arrive();  // waited for before the first write into another CTA
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = (int)cluster.block_rank();
-    const int b = blockIdx.x / kVerifyCtas;
-    const bool lead = rank == 0;
+    const int b = blockIdx.x / (int)cluster.num_blocks();
+    const bool lead = cluster.block_rank() == 0;
     if (warp == 0) {
         int m = num_drafts ? num_drafts[b] : T;
         const bool bad = m < 0 || m > T;
@@ -235,10 +366,10 @@ verify_drafts_kernel(const Elem* __restrict__ target, const Elem* __restrict__ d
             bool ok = true, in = true;
             if (i < m) {
                 const int x = drafts[(size_t)b * T + i];
+                const float u = u_accept[(size_t)b * T + i];
                 in = x >= 0 && x < V;
-                ok = in && (double)u_accept[(size_t)b * T + i] *
-                                   (double)prob(draft, ((size_t)b * T + i) * V + x) <
-                               (double)prob(target, ((size_t)b * (T + 1) + i) * V + x);
+                ok = in && (double)u * (double)as_prob(draft[((size_t)b * T + i) * V + x]) <
+                               (double)as_prob(target[((size_t)b * (T + 1) + i) * V + x]);
             }
             const uint32_t no = __ballot_sync(0xffffffffu, !ok);
             const uint32_t out = __ballot_sync(0xffffffffu, !in);
@@ -257,6 +388,7 @@ verify_drafts_kernel(const Elem* __restrict__ target, const Elem* __restrict__ d
         }
     }
     __syncthreads();
+    cluster_wait();
     const int n = sh.n;
     if (lead) {
         for (int i = tid; i <= T; i += kVerifyThreads)
@@ -264,80 +396,65 @@ verify_drafts_kernel(const Elem* __restrict__ target, const Elem* __restrict__ d
                 tokens[(size_t)b * (T + 1) + i] = i < n ? drafts[(size_t)b * T + i] : -1;
         if (tid == 0) accepted[b] = n;
     }
-    if (sh.bad) return;  // the same in all CTAs of the cluster
-    const Elem* p = target + ((size_t)b * (T + 1) + n) * V;
-    const Elem* q = draft + ((size_t)b * T + n) * V;
-    const int share = (V + kVerifyCtas - 1) / kVerifyCtas;
-    const int lo = min(rank * share, V), hi = min(lo + share, V);
-    const int part = (hi - lo + kVerifyWarps - 1) / kVerifyWarps;
-    const int wlo = min(lo + warp * part, hi), whi = min(wlo + part, hi);
-    bool rest = n < sh.m;
-    double total = 0.0, before = 0.0, behind = 0.0;
-    int newest = -1;
-    while (true) {
-        int last;
-        const double sum = rest ? share_sum<Elem, true>(p, q, wlo, whi, last)
-                                : share_sum<Elem, false>(p, q, wlo, whi, last);
-        if (lane == 0) {
-            sh.warp_sum[warp] = sum;
-            sh.warp_last[warp] = last;
-        }
-        __syncthreads();
-        if (tid == 0) {
-            double s = 0.0;
-            int z = -1;
-            for (int k = 0; k < kVerifyWarps; ++k) {
-                s += sh.warp_sum[k];
-                z = max(z, sh.warp_last[k]);
-            }
-            sh.cta_sum = s;
-            sh.last = z;
-        }
-        cluster.sync();
-        total = before = 0.0;
-        newest = -1;
-        for (int k = 0; k < kVerifyCtas; ++k) {
-            const double s = *cluster.map_shared_rank(&sh.cta_sum, k);
-            if (k == rank) before = total;
-            total += s;
-            if (k == rank) behind = total;
-            newest = max(newest, *cluster.map_shared_rank(&sh.last, k));
-        }
-        cluster.sync();  // no CTA leaves or writes its sums again before all have read them
-        if (!rest || newest >= 0) break;
-        rest = false;    // nothing left of the target: the target itself
-    }
-    int32_t* token = tokens + (size_t)b * (T + 1) + n;
-    if (newest < 0 || !isfinite(total)) {
-        if (lead && tid == 0) {
+    if (!sh.bad) {
+        const Elem* p = target + ((size_t)b * (T + 1) + n) * V;
+        const Elem* q = draft + ((size_t)b * T + n) * V;
+        const float u = u_sample[b];
+        int32_t* token = tokens + (size_t)b * (T + 1) + n;
+        bool done = false;
+        if (n < sh.m) done = sample<Elem, VEC, true>(sh, cluster, p, q, V, u, token, dev_status);
+        // behind the last draft, or nothing of the target left: the target itself
+        if (!done) done = sample<Elem, VEC, false>(sh, cluster, p, q, V, u, token, dev_status);
+        if (!done && lead && tid == 0) {
             *token = -1;
             report(dev_status, KVD_DEV_PROBS);
         }
-        return;
     }
-    const double want = (double)u_sample[b] * total;
-    if (!(want < total)) {
-        if (lead && tid == 0) *token = newest;
-        return;
-    }
-    // The CTAs' borders are the same sums in every CTA, so exactly one of them
-    // has before <= want < behind; in it, one warp has the last border that is
-    // not above `want`.
-    if (!(before <= want && want < behind)) return;
-    double border = before;
-    for (int k = 0; k < warp; ++k) border += sh.warp_sum[k];
-    if (!(border <= want) || (warp + 1 < kVerifyWarps && border + sh.warp_sum[warp] <= want))
-        return;
-    const int found = rest ? find<Elem, true>(p, q, wlo, whi, border, want)
-                           : find<Elem, false>(p, q, wlo, whi, border, want);
-    if (lane == 0) {
-        // rounding between the two passes may leave none in the share: then its
-        // largest positive index, or the nearest larger set's
-        int v = found;
-        if (v < 0) v = sh.warp_last[warp];
-        if (v < 0) v = sh.last;
-        *token = v < 0 ? newest : v;
-    }
+}
+
+template <typename Elem, int VEC>
+cudaError_t go_verify(const Elem* target, const Elem* draft, const int32_t* drafts,
+                      const float* u_accept, const float* u_sample, const int32_t* num_drafts,
+                      int32_t* tokens, int32_t* accepted, int Q, int T, int V, int32_t* dev_status,
+                      cudaStream_t stream) {
+    // CTAs a sequence: while two CTAs an SM are not passed; shares of at least
+    // half a batch a warp
+    int ctas = 1;
+    while (ctas < kVerifyMaxCtas && 2 * ctas * Q <= 2 * kLatentSMs &&
+           V / (2 * ctas) >= 8 * 32 * kVerifyWarps)
+        ctas *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(Q * ctas);
+    cfg.blockDim = dim3(kVerifyThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, verify_drafts_kernel<Elem, VEC>, target, draft, drafts, u_accept,
+                              u_sample, num_drafts, tokens, accepted, T, V, dev_status);
+}
+
+template <typename Elem>
+cudaError_t go_verify(const void* target, const void* draft, const int32_t* drafts,
+                      const float* u_accept, const float* u_sample, const int32_t* num_drafts,
+                      int32_t* tokens, int32_t* accepted, int Q, int T, int V, int32_t* dev_status,
+                      cudaStream_t stream) {
+    constexpr int kVec = 16 / (int)sizeof(Elem);
+    const Elem* p = static_cast<const Elem*>(target);
+    const Elem* q = static_cast<const Elem*>(draft);
+    // 16-byte loads where every row starts on a 16-byte boundary
+    const bool vec = V % kVec == 0 && reinterpret_cast<uintptr_t>(target) % 16 == 0 &&
+                     reinterpret_cast<uintptr_t>(draft) % 16 == 0;
+    return vec ? go_verify<Elem, kVec>(p, q, drafts, u_accept, u_sample, num_drafts, tokens,
+                                       accepted, Q, T, V, dev_status, stream)
+               : go_verify<Elem, 1>(p, q, drafts, u_accept, u_sample, num_drafts, tokens, accepted,
+                                    Q, T, V, dev_status, stream);
 }
 
 }  // namespace
@@ -362,15 +479,11 @@ cudaError_t launch_verify_drafts(const void* target, const void* draft, const in
                                  const int32_t* num_drafts, int32_t* tokens, int32_t* accepted,
                                  int Q, int T, int V, kvd_dtype dt, int32_t* dev_status,
                                  cudaStream_t stream) {
-    const dim3 grid(Q * kVerifyCtas);
-    if (dt == KVD_BF16)
-        return launch_pdl(verify_drafts_kernel<__nv_bfloat16>, grid, dim3(kVerifyThreads), 0,
-                          stream, static_cast<const __nv_bfloat16*>(target),
-                          static_cast<const __nv_bfloat16*>(draft), drafts, u_accept, u_sample,
-                          num_drafts, tokens, accepted, T, V, dev_status);
-    return launch_pdl(verify_drafts_kernel<float>, grid, dim3(kVerifyThreads), 0, stream,
-                      static_cast<const float*>(target), static_cast<const float*>(draft), drafts,
-                      u_accept, u_sample, num_drafts, tokens, accepted, T, V, dev_status);
+    return dt == KVD_BF16
+               ? go_verify<__nv_bfloat16>(target, draft, drafts, u_accept, u_sample, num_drafts,
+                                          tokens, accepted, Q, T, V, dev_status, stream)
+               : go_verify<float>(target, draft, drafts, u_accept, u_sample, num_drafts, tokens,
+                                  accepted, Q, T, V, dev_status, stream);
 }
 
 }  // namespace kvd

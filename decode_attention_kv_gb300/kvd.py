@@ -1052,62 +1052,71 @@ def combine_gathered(parts, R, D, out=None, lse=None, out_dtype=torch.float32):
 
 # ------------------------------------------------------------------ latent caches
 
-def _latent_tensors(fn, dev, *named):
-    """Every (name, tensor) is a contiguous CUDA tensor of device `dev`."""
-    for n, t in named:
-        if not (t.is_cuda and t.is_contiguous()):
-            raise ValueError(f"{fn}: {n} must be a contiguous CUDA tensor")
-        if t.device != dev:
-            raise ValueError(f"{fn}: {n} is on {t.device}, not on {dev}")
+# These calls are made every few microseconds by a decode loop, so each argument
+# is looked at once (device, type, shape, layout) and passed on as an integer.
+
+def _refuse(fn, name, t, dev, dtype, shape):
+    if t.get_device() < 0 or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be a contiguous CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on cuda:{t.get_device()}, not on cuda:{dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+    raise ValueError(f"{fn}: {name} must be {list(shape)}, not {list(t.shape)}")
 
 
-def _latent_int32(fn, dev, name, t, shape):
-    _latent_tensors(fn, dev, (name, t))
-    if t.dtype != torch.int32 or tuple(t.shape) != shape:
-        raise ValueError(f"{fn}: {name} must be int32 {list(shape)}")
+def _arg(fn, name, t, dev, dtype, shape):
+    """The data pointer of a contiguous tensor of this device, type and shape."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or \
+            not t.is_contiguous() or dev < 0:
+        _refuse(fn, name, t, dev, dtype, shape)
+    return t.data_ptr()
 
 
-def _latent_outputs(fn, dev, out, out_shape, dtype, lse, lse_shape):
-    if out is None:
-        out = torch.empty(out_shape, dtype=dtype, device=dev)
-    else:
-        _latent_tensors(fn, dev, ("out", out))
-        if tuple(out.shape) != out_shape or out.dtype != dtype:
-            raise ValueError(f"{fn}: out must be {dtype} {list(out_shape)}")
-    if lse is not None:
-        _latent_tensors(fn, dev, ("lse", lse))
-        if tuple(lse.shape) != lse_shape or lse.dtype != torch.float32:
-            raise ValueError(f"{fn}: lse must be fp32 {list(lse_shape)}")
-    return out
+def _opt(fn, name, t, dev, dtype, shape):
+    return None if t is None else _arg(fn, name, t, dev, dtype, shape)
 
 
-def _latent_call(fn, dev, *args):
-    """One call of the C entry point on the tensors' device and its current stream."""
-    call = getattr(load(), fn)
-    if torch.cuda.current_device() == dev.index:
-        st = call(*args, _stream(dev))
+def _call_on(fn, dev, dev_status, *args):
+    """One call of the C entry point on the tensors' device and its current
+    stream; the status word and the stream are its last arguments."""
+    L = _lib or load()
+    if dev_status is not None:
+        dev_status = _arg(fn, "dev_status", dev_status, dev, torch.int32, dev_status.shape)
+    if torch.cuda.current_device() == dev:
+        st = getattr(L, fn)(*args, dev_status, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = call(*args, _stream(dev))
-    _check(fn, st)
+            st = getattr(L, fn)(*args, dev_status, torch._C._cuda_getCurrentRawStream(dev))
+    if st != OK:
+        _check(fn, st)
 
 
-def _latent_cache(fn, latent_cache, rope_cache, block_tables, seq_offset, Q):
-    dev = latent_cache.device
-    _latent_tensors(fn, dev, ("latent_cache", latent_cache), ("rope_cache", rope_cache))
-    if latent_cache.dim() != 4 or latent_cache.shape[2] != 1 or \
-            tuple(rope_cache.shape[:3]) != tuple(latent_cache.shape[:3]) or rope_cache.dim() != 4:
+def _elem_code(fn, t):
+    if t.dtype is torch.bfloat16:
+        return BF16
+    if t.dtype is torch.float32:
+        return F32
+    raise TypeError(f"{fn}: unsupported dtype {t.dtype} (bf16 or fp32)")
+
+
+def _latent_cache(fn, latent_cache, rope_cache):
+    """Device, sizes and pointers of a latent cache."""
+    dev = latent_cache.get_device()
+    if latent_cache.dim() != 4 or rope_cache.dim() != 4:
         raise ValueError(f"{fn}: caches must be [NB, BS, 1, R] and [NB, BS, 1, P]")
-    if rope_cache.dtype != latent_cache.dtype:
-        raise TypeError(f"{fn}: the caches must share a dtype")
+    NB, BS, one, R = latent_cache.shape
+    P = rope_cache.shape[3]
+    dtype = latent_cache.dtype
+    lp = _arg(fn, "latent_cache", latent_cache, dev, dtype, (NB, BS, 1, R))
+    rp = _arg(fn, "rope_cache", rope_cache, dev, dtype, (NB, BS, 1, P))
+    return dev, NB, BS, R, P, dtype, lp, rp
+
+
+def _columns(fn, block_tables):
     if block_tables.dim() != 2:
         raise ValueError(f"{fn}: block_tables must be int32 [Q, cols]")
-    cols = block_tables.shape[1]
-    _latent_int32(fn, dev, "block_tables", block_tables, (Q, cols))
-    if seq_offset is not None:
-        _latent_int32(fn, dev, "seq_offset", seq_offset, (Q,))
-    NB, BS, _, R = latent_cache.shape
-    return dev, NB, BS, cols, R, rope_cache.shape[3]
+    return block_tables.shape[1]
 
 
 def append_latent(latent_cache, rope_cache, block_tables, seq_offset, latent_new, rope_new,
@@ -1117,20 +1126,17 @@ def append_latent(latent_cache, rope_cache, block_tables, seq_offset, latent_new
     (latent_cache [NB, BS, 1, R], rope_cache [NB, BS, 1, P]; block_tables
     [Q, cols], seq_offset [Q] or None, new_lens [Q + 1] cumsum, pos [Q] int32)."""
     fn = "append_latent"
-    Q = pos.shape[0] if pos.dim() == 1 else -1
-    dev, NB, BS, cols, R, P = _latent_cache(fn, latent_cache, rope_cache, block_tables, seq_offset,
-                                            Q)
-    _latent_tensors(fn, dev, ("latent_new", latent_new), ("rope_new", rope_new))
-    N = latent_new.shape[0]
-    if tuple(latent_new.shape) != (N, R) or tuple(rope_new.shape) != (N, P):
-        raise ValueError(f"{fn}: new rows must be [N, {R}] and [N, {P}]")
-    if not (latent_new.dtype == rope_new.dtype == latent_cache.dtype):
-        raise TypeError(f"{fn}: caches and new rows must share a dtype")
-    _latent_int32(fn, dev, "new_lens", new_lens, (Q + 1,))
-    _latent_int32(fn, dev, "pos", pos, (Q,))
-    _latent_call("kvd_append_latent", dev, _ptr(latent_cache), _ptr(rope_cache), _ptr(latent_new),
-                 _ptr(rope_new), _ptr(block_tables), _ptr(seq_offset), _ptr(new_lens), _ptr(pos),
-                 Q, N, NB, BS, cols, R, P, _dtype_code(latent_cache), _ptr(dev_status))
+    dev, NB, BS, R, P, dtype, lp, rp = _latent_cache(fn, latent_cache, rope_cache)
+    i32 = torch.int32
+    Q, N, cols = pos.numel(), latent_new.shape[0], _columns(fn, block_tables)
+    _call_on("kvd_append_latent", dev, dev_status, lp, rp,
+             _arg(fn, "latent_new", latent_new, dev, dtype, (N, R)),
+             _arg(fn, "rope_new", rope_new, dev, dtype, (N, P)),
+             _arg(fn, "block_tables", block_tables, dev, i32, (Q, cols)),
+             _opt(fn, "seq_offset", seq_offset, dev, i32, (Q,)),
+             _arg(fn, "new_lens", new_lens, dev, i32, (Q + 1,)),
+             _arg(fn, "pos", pos, dev, i32, (Q,)), Q, N, NB, BS, cols, R, P,
+             _elem_code(fn, latent_cache))
 
 
 def attend_latent_workspace_bytes(Q, T, H, BS, cols, R, P, dtype=torch.bfloat16):
@@ -1150,29 +1156,27 @@ def attend_latent(q_latent, q_rope, latent_cache, rope_cache, block_tables, seq_
     [Q, T, H, R]; fills ``lse`` [Q, T, H] fp32 if given.
     """
     fn = "attend_latent"
-    if q_latent.dim() != 4 or q_rope.dim() != 4:
+    dev, NB, BS, R, P, dtype, lp, rp = _latent_cache(fn, latent_cache, rope_cache)
+    if q_latent.dim() != 4:
         raise ValueError(f"{fn}: queries must be [Q, T, H, R] and [Q, T, H, P]")
+    i32 = torch.int32
     Q, T, H, _ = q_latent.shape
-    dev, NB, BS, cols, R, P = _latent_cache(fn, latent_cache, rope_cache, block_tables, seq_offset,
-                                            Q)
-    _latent_tensors(fn, dev, ("q_latent", q_latent), ("q_rope", q_rope))
-    if tuple(q_latent.shape) != (Q, T, H, R) or tuple(q_rope.shape) != (Q, T, H, P):
-        raise ValueError(f"{fn}: queries must be [Q, T, H, {R}] and [Q, T, H, {P}]")
-    if not (q_latent.dtype == q_rope.dtype == latent_cache.dtype):
-        raise TypeError(f"{fn}: queries and caches must share a dtype")
-    _latent_int32(fn, dev, "seq_lens", seq_lens, (Q + 1,))
-    dt = _dtype_code(q_latent)
-    out = _latent_outputs(fn, dev, out, (Q, T, H, R), q_latent.dtype, lse, (Q, T, H))
-    need = load().kvd_attend_latent_workspace_bytes(Q, T, H, BS, cols, R, P, dt)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace is not None:
-        _latent_tensors(fn, dev, ("workspace", workspace))
-    _latent_call("kvd_attend_latent", dev, _ptr(q_latent), _ptr(q_rope), _ptr(latent_cache),
-                 _ptr(rope_cache), _ptr(block_tables), _ptr(seq_lens), _ptr(seq_offset), _ptr(out),
-                 _ptr(lse), Q, T, H, NB, BS, cols, R, P, float(scale), dt, _ptr(workspace),
-                 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                 _ptr(dev_status))
+    cols, dt = _columns(fn, block_tables), _elem_code(fn, latent_cache)
+    args = (_arg(fn, "q_latent", q_latent, dev, dtype, (Q, T, H, R)),
+            _arg(fn, "q_rope", q_rope, dev, dtype, (Q, T, H, P)), lp, rp,
+            _arg(fn, "block_tables", block_tables, dev, i32, (Q, cols)),
+            _arg(fn, "seq_lens", seq_lens, dev, i32, (Q + 1,)),
+            _opt(fn, "seq_offset", seq_offset, dev, i32, (Q,)))
+    if out is None:
+        out = torch.empty_like(q_latent)
+    op = _arg(fn, "out", out, dev, dtype, (Q, T, H, R))
+    zp = _opt(fn, "lse", lse, dev, torch.float32, (Q, T, H))
+    if workspace is None:
+        need = attend_latent_workspace_bytes(Q, T, H, BS, cols, R, P, dtype)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q_latent.device)
+    wp = _arg(fn, "workspace", workspace, dev, workspace.dtype, workspace.shape)
+    _call_on("kvd_attend_latent", dev, dev_status, *args, op, zp, Q, T, H, NB, BS, cols, R, P,
+             scale, dt, wp, workspace.nbytes)
     return out
 
 
@@ -1188,28 +1192,28 @@ def attend_expanded(q, kv, k_rope, q_lens, k_lens, scale=None, causal=True, out=
     [Nq, H, Dv]; fills ``lse`` [Nq, H] fp32 if given.
     """
     fn = "attend_expanded"
-    dev = q.device
-    _latent_tensors(fn, dev, ("q", q), ("kv", kv), ("k_rope", k_rope))
-    if q.dim() != 3 or kv.dim() != 3 or k_rope.dim() != 2 or k_rope.shape[0] != kv.shape[0] or \
-            kv.shape[1] != q.shape[1]:
+    if q.dim() != 3 or kv.dim() != 3 or k_rope.dim() != 2:
         raise ValueError(f"{fn}: q [Nq, H, Dn + P], kv [Nk, H, Dn + Dv], k_rope [Nk, P] required")
+    dev, dtype, i32 = q.get_device(), q.dtype, torch.int32
     Nq, H, Dqk = q.shape
     Nk, P = k_rope.shape
     Dn = Dqk - P
     Dv = kv.shape[2] - Dn
     if Dn < 1 or Dv < 1:
         raise ValueError(f"{fn}: rows of q {Dqk}, kv {kv.shape[2]} and k_rope {P} do not fit")
-    if not (q.dtype == kv.dtype == k_rope.dtype):
-        raise TypeError(f"{fn}: q, kv and k_rope must share a dtype")
-    Q = q_lens.shape[0] - 1 if q_lens.dim() == 1 else -1
-    _latent_int32(fn, dev, "q_lens", q_lens, (Q + 1,))
-    _latent_int32(fn, dev, "k_lens", k_lens, (Q + 1,))
-    if scale is None:
-        scale = 1.0 / math.sqrt(Dqk)
-    out = _latent_outputs(fn, dev, out, (Nq, H, Dv), q.dtype, lse, (Nq, H))
-    _latent_call("kvd_attend_expanded", dev, _ptr(q), _ptr(kv), _ptr(k_rope), _ptr(q_lens),
-                 _ptr(k_lens), _ptr(out), _ptr(lse), Q, Nq, Nk, H, Dn, Dv, P, float(scale),
-                 int(bool(causal)), _dtype_code(q), _ptr(dev_status))
+    Q = q_lens.numel() - 1
+    args = (_arg(fn, "q", q, dev, dtype, (Nq, H, Dqk)),
+            _arg(fn, "kv", kv, dev, dtype, (Nk, H, Dn + Dv)),
+            _arg(fn, "k_rope", k_rope, dev, dtype, (Nk, P)),
+            _arg(fn, "q_lens", q_lens, dev, i32, (Q + 1,)),
+            _arg(fn, "k_lens", k_lens, dev, i32, (Q + 1,)))
+    if out is None:
+        out = torch.empty((Nq, H, Dv), dtype=dtype, device=q.device)
+    op = _arg(fn, "out", out, dev, dtype, (Nq, H, Dv))
+    zp = _opt(fn, "lse", lse, dev, torch.float32, (Nq, H))
+    _call_on("kvd_attend_expanded", dev, dev_status, *args, op, zp, Q, Nq, Nk, H, Dn, Dv, P,
+             1.0 / math.sqrt(Dqk) if scale is None else scale, 1 if causal else 0,
+             _elem_code(fn, q))
     return out
 
 
@@ -1227,36 +1231,25 @@ def verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, n
     and accepted [Q] int32.
     """
     fn = "verify_drafts"
-    dev = target_probs.device
-    _latent_tensors(fn, dev, ("target_probs", target_probs))
     if target_probs.dim() != 3 or target_probs.shape[1] < 1:
         raise ValueError(f"{fn}: target_probs must be [Q, T + 1, V]")
-    Q, T, V = target_probs.shape
-    T -= 1
+    dev, dtype, i32 = target_probs.get_device(), target_probs.dtype, torch.int32
+    Q, T1, V = target_probs.shape
+    T = T1 - 1
+    tp = _arg(fn, "target_probs", target_probs, dev, dtype, (Q, T1, V))
+    dp = xp = up = None
     if T > 0:
-        _latent_tensors(fn, dev, ("draft_probs", draft_probs), ("u_accept", u_accept))
-        if tuple(draft_probs.shape) != (Q, T, V) or draft_probs.dtype != target_probs.dtype:
-            raise ValueError(f"{fn}: draft_probs must be {target_probs.dtype} {[Q, T, V]}")
-        _latent_int32(fn, dev, "draft_tokens", draft_tokens, (Q, T))
-        if tuple(u_accept.shape) != (Q, T) or u_accept.dtype != torch.float32:
-            raise ValueError(f"{fn}: u_accept must be fp32 {[Q, T]}")
-    else:
-        draft_probs = draft_tokens = u_accept = None
-    _latent_tensors(fn, dev, ("u_sample", u_sample))
-    if tuple(u_sample.shape) != (Q,) or u_sample.dtype != torch.float32:
-        raise ValueError(f"{fn}: u_sample must be fp32 {[Q]}")
-    if num_drafts is not None:
-        _latent_int32(fn, dev, "num_drafts", num_drafts, (Q,))
+        dp = _arg(fn, "draft_probs", draft_probs, dev, dtype, (Q, T, V))
+        xp = _arg(fn, "draft_tokens", draft_tokens, dev, i32, (Q, T))
+        up = _arg(fn, "u_accept", u_accept, dev, torch.float32, (Q, T))
+    sp = _arg(fn, "u_sample", u_sample, dev, torch.float32, (Q,))
+    mp = _opt(fn, "num_drafts", num_drafts, dev, i32, (Q,))
     if tokens is None:
-        tokens = torch.empty((Q, T + 1), dtype=torch.int32, device=dev)
-    else:
-        _latent_int32(fn, dev, "tokens", tokens, (Q, T + 1))
+        tokens = torch.empty((Q, T1), dtype=i32, device=target_probs.device)
     if accepted is None:
-        accepted = torch.empty((Q,), dtype=torch.int32, device=dev)
-    else:
-        _latent_int32(fn, dev, "accepted", accepted, (Q,))
-    _latent_call("kvd_verify_drafts", dev, _ptr(target_probs), _ptr(draft_probs),
-                 _ptr(draft_tokens), _ptr(u_accept), _ptr(u_sample), _ptr(num_drafts),
-                 _ptr(tokens), _ptr(accepted), Q, T, V, _dtype_code(target_probs),
-                 _ptr(dev_status))
+        accepted = torch.empty((Q,), dtype=i32, device=target_probs.device)
+    _call_on("kvd_verify_drafts", dev, dev_status, tp, dp, xp, up, sp, mp,
+             _arg(fn, "tokens", tokens, dev, i32, (Q, T1)),
+             _arg(fn, "accepted", accepted, dev, i32, (Q,)), Q, T, V,
+             _elem_code(fn, target_probs))
     return tokens, accepted
