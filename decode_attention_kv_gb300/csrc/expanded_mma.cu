@@ -14,8 +14,9 @@
 // values and the next of keys at 192 + 128 elements a token, and every block is
 // asked for at least one product of 1280 cycles before it is needed.
 //
-// Warps 0-3 and 4-7: softmax of tile 0 and 1, a row a thread.  Warp 8 issues the
-// MMAs, warp 9 the copies.
+// Warps 0-3 and 4-7: softmax of tile 0 and 1, a row a thread.  Warps 8 and 9
+// issue the MMAs of tile 0 and 1: what one spends on waiting and setting up (450
+// cycles a step) the other's products fill.  Warp 10 issues the copies.
 #include "kvd_internal.h"
 #include "latent_common.cuh"
 #include "tcgen05_ptx.cuh"
@@ -27,14 +28,17 @@ constexpr int kRows = 128;               // queries of a tile, keys of a step
 constexpr int kBlock = kRows * 128;      // bytes of 128 rows x 64 bf16
 constexpr int kRing = 8;                 // blocks in flight
 constexpr int kSteps = 4;                // steps with barriers of their own (the ring holds fewer)
-constexpr int kMmaWarp = 8, kCopyWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kMmaWarp = 8, kCopyWarp = 10;
+constexpr int kThreads = 384;  // warp 11 completes the third warpgroup
+// Registers a thread: the softmax holds a row of 128 scores.  2 x 208 + 80 is
+// within the 3 x 168 that three warpgroups start with.
+constexpr int kSoftmaxRegs = 208, kIssueRegs = 80;
 constexpr float kSkip = 8.f;             // log2 units
 constexpr uint32_t kTmemCols = 512;
 
 struct ExpandedShared {
     uint64_t q_full[2], k_full[kSteps], v_full[kSteps], empty[kRing];
-    uint64_t s_full[2], p_full[2], o_full[2], drain;
+    uint64_t s_full[2], p_full[2], o_full[2], turn, drain[2];
     uint32_t tmem;
     int abort;
     int scratch[kFindWords];
@@ -61,6 +65,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return true;
 }
 
+template <int KC, int VC>  // blocks of a step: keys (Dn / 64 + 1), values (Dv / 64)
 __global__ void __launch_bounds__(kThreads, 1)
 expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qmap,
                     const __grid_constant__ CUtensorMap kvmap,
@@ -71,7 +76,7 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
     ExpandedShared& sh = *reinterpret_cast<ExpandedShared*>(sm + L.shared);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x, unit = blockIdx.y;
-    const int KC = L.q_blocks, VC = a.Dv / 64, per = KC + VC;  // blocks of a step
+    constexpr int per = KC + VC;
 
     if (tid == 0) {
         for (int s = 0; s < 2; ++s) {
@@ -84,8 +89,10 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
             mbar_init(&sh.k_full[i], 1);
             mbar_init(&sh.v_full[i], 1);
         }
-        for (int i = 0; i < kRing; ++i) mbar_init(&sh.empty[i], 1);
-        mbar_init(&sh.drain, 1);
+        for (int i = 0; i < kRing; ++i) mbar_init(&sh.empty[i], 2);  // both tiles are done with it
+        mbar_init(&sh.turn, 1);
+        mbar_init(&sh.drain[0], 1);
+        mbar_init(&sh.drain[1], 1);
         sh.abort = 0;
         fence_barrier_init();
     }
@@ -128,6 +135,8 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
     const int nsteps = max(steps[0], steps[1]);
     bool bad = false;
 
+    if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == kCopyWarp) {
         // ------------------------------------------------------------ copies
         // the keys and values are read again by the sequence's other query tiles
@@ -147,27 +156,30 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
                 }
                 return true;
             };
+            auto queries = [&](int s) {
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&sh.q_full[s], KC * kBlock);
+#pragma unroll
+                    for (int c = 0; c < KC; ++c)
+                        tma_g2s_3d(sm + (s * KC + c) * kBlock, &qmap, 0,
+                                   seq.q0 + row0 + s * kRows, qchunk + c, &sh.q_full[s], policy);
+                }
+                __syncwarp();
+            };
             for (int i = 0; i < n && !bad; ++i) {
                 const int row = uniform(seq.k0 + i * kRows);
                 uint64_t* kf = &sh.k_full[i % kSteps];
                 uint64_t* vf = &sh.v_full[i % kSteps];
+                if (i == 0 && steps[0] > 0) queries(0);
                 if (elect_one()) {
-                    if (i == 0) {
-                        for (int s = 0; s < 2; ++s) {
-                            if (steps[s] == 0) continue;
-                            mbar_arrive_expect_tx(&sh.q_full[s], KC * kBlock);
-                            for (int c = 0; c < KC; ++c)
-                                tma_g2s_3d(sm + (s * KC + c) * kBlock, &qmap, 0,
-                                           seq.q0 + row0 + s * kRows, qchunk + c, &sh.q_full[s],
-                                           policy);
-                        }
-                    }
                     mbar_arrive_expect_tx(kf, KC * kBlock);
                     mbar_arrive_expect_tx(vf, VC * kBlock);
                 }
                 __syncwarp();
                 for (int c = 0; c + 1 < KC && !bad; ++c) bad = !block(&kvmap, row, kchunk + c, kf);
                 if (!bad) bad = !block(&ropemap, row, 0, kf);
+                // behind the first keys: tile 1 starts half a step later
+                if (i == 0 && steps[1] > 0) queries(1);
                 for (int c = 0; c < VC && !bad; ++c)
                     bad = !block(&kvmap, row, kchunk + KC - 1 + c, vf);
             }
@@ -179,98 +191,102 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
                 }
             }
         }
-    } else if (warp == kMmaWarp) {
+    } else if (warp < kCopyWarp) {
         // ------------------------------------------------------------ MMA issue
+        // (What an MMA is issued with goes through uniform(), see latent_mma.cu.)
+        const int s = uniform(warp - kMmaWarp);
         const uint32_t sdesc = mma_desc(kRows, kRows), odesc = mma_desc(kRows, 64, kBMn);
         const uint32_t base = uniform(smem_u32(sm)), tm = uniform(tmem);
-        const int n0 = uniform(steps[0]), n1 = uniform(steps[1]), n = uniform(nsteps);
-        // Scores of query tile s over key tile i; the last of the two tiles that
-        // uses the keys frees their blocks.
-        auto scores = [&](int s, int i) {
-            const uint32_t q_low = uniform(desc_low(base + s * KC * kBlock, 16));
-            const bool last = s == 1 || i >= n1;
-            const int b0 = uniform(i * per % kRing);
+        const uint32_t q_low = uniform(desc_low(base + s * KC * kBlock, 16));
+        const uint32_t td = uniform(tm + s * kRows), to = uniform(tm + 256 + s * kRows);
+        const int n = uniform(nsteps), ns = uniform(steps[s]);
+        // scores of step i; then its blocks are free as far as this tile goes
+        auto scores = [&](int i) {
+            const int b0 = i * per;
+            uint32_t k_low[KC];
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+                k_low[c] = uniform(desc_low(base + L.ring + (b0 + c) % kRing * kBlock, 16));
             if (elect_one()) {
-#pragma unroll 1
-                for (int c = 0; c < KC; ++c) {
-                    const int slot = (b0 + c) % kRing;
-                    const uint32_t k_low = desc_low(base + L.ring + slot * kBlock, 16);
-                    const uint32_t qc = q_low + ((c * kBlock) >> 4);
+#pragma unroll
+                for (int c = 0; c < KC; ++c)
 #pragma unroll
                     for (int z = 0; z < 4; ++z)
-                        mma_ss(tm + s * kRows, desc_of(qc + 2 * z), desc_of(k_low + 2 * z), sdesc,
-                               c > 0 || z > 0);
-                    if (last) mma_commit(&sh.empty[slot]);
-                }
+                        mma_ss(td, desc_of(q_low + ((c * kBlock) >> 4) + 2 * z),
+                               desc_of(k_low[c] + 2 * z), sdesc, c > 0 || z > 0);
                 mma_commit(&sh.s_full[s]);
+#pragma unroll
+                for (int c = 0; c < KC; ++c) mma_commit(&sh.empty[(b0 + c) % kRing]);
             }
             __syncwarp();
         };
-        auto values = [&](int s, int i, bool final) {
-            const bool last = s == 1 || i >= n1;
-            const int b0 = uniform((i * per + KC) % kRing);
+        if (ns > 0) {
+            // tile 1 starts half a step behind tile 0, so that one's products and the
+            // other's softmax take turns from the first step on
+            if (s == 1 && n > 0 && steps[0] > 0) bad = !warp_wait(&sh.turn, 0, abort_flag);
+            bad = bad || !warp_wait(&sh.q_full[s], 0, abort_flag) ||
+                  !warp_wait(&sh.k_full[0], 0, abort_flag);
+            tc_fence_after();
+            if (!bad) scores(0);
+        }
+        for (int i = 0; i < ns && !bad; ++i) {
+            const uint32_t keep = uniform((int)(i > 0));
+            const int b0 = i * per + KC;
+            uint32_t v_low[VC];
+#pragma unroll
+            for (int c = 0; c < VC; ++c)
+                v_low[c] = uniform(desc_low(base + L.ring + (b0 + c) % kRing * kBlock, 16));
+            if (!warp_wait(&sh.v_full[i % kSteps], (i / kSteps) & 1, abort_flag) ||
+                !warp_wait(&sh.p_full[s], i & 1, abort_flag)) {
+                bad = true;
+                break;
+            }
+            tc_fence_after();
             if (elect_one()) {
-#pragma unroll 1
-                for (int c = 0; c < VC; ++c) {
-                    const int slot = (b0 + c) % kRing;
-                    const uint32_t v_low = desc_low(base + L.ring + slot * kBlock, 16);
+#pragma unroll
+                for (int c = 0; c < VC; ++c)
 #pragma unroll
                     for (int z = 0; z < 8; ++z)
-                        mma_ts(tm + 256 + s * kRows + 64 * c, tm + s * kRows + 8 * z,
-                               desc_of(v_low + ((z * 2048) >> 4)), odesc, i > 0 || z > 0);
-                    if (last) mma_commit(&sh.empty[slot]);
-                }
-                if (final) mma_commit(&sh.o_full[s]);
+                        mma_ts(to + 64 * c, td + 8 * z, desc_of(v_low[c] + ((z * 2048) >> 4)),
+                               odesc, z > 0 || keep);
+#pragma unroll
+                for (int c = 0; c < VC; ++c) mma_commit(&sh.empty[(b0 + c) % kRing]);
+                if (i + 1 == ns) mma_commit(&sh.o_full[s]);
+                if (s == 0 && i == 0) mbar_arrive(&sh.turn);
             }
             __syncwarp();
-        };
-        if (n > 0) {
-            bad = !warp_wait(&sh.k_full[0], 0, abort_flag);
-            if (!bad && n0 > 0) {
-                bad = !warp_wait(&sh.q_full[0], 0, abort_flag);
-                tc_fence_after();
-                if (!bad) scores(0, 0);
-            }
-            if (!bad && n1 > 0) {
-                bad = !warp_wait(&sh.q_full[1], 0, abort_flag);
-                tc_fence_after();
-                if (!bad) scores(1, 0);
-            }
-            for (int i = 0; i < n && !bad; ++i) {
-#pragma unroll 1
-                for (int s = 0; s < 2 && !bad; ++s) {
-                    const int ns = s == 0 ? n0 : n1;
-                    if (i >= ns) continue;
-                    if (!warp_wait(&sh.p_full[s], i & 1, abort_flag) ||
-                        !warp_wait(&sh.v_full[i % kSteps], (i / kSteps) & 1, abort_flag)) {
-                        bad = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    values(s, i, i + 1 == ns);
-                    if (i + 1 < ns) {
-                        if (!warp_wait(&sh.k_full[(i + 1) % kSteps], ((i + 1) / kSteps) & 1,
-                                       abort_flag)) {
-                            bad = true;
-                            break;
-                        }
-                        tc_fence_after();
-                        scores(s, i + 1);
-                    }
+            if (i + 1 < ns) {
+                if (!warp_wait(&sh.k_full[(i + 1) % kSteps], ((i + 1) / kSteps) & 1, abort_flag)) {
+                    bad = true;
+                    break;
                 }
-            }
-            if (bad) {
-                if (lane == 0) sh.abort = 1;
-                __syncwarp();
-                if (elect_one()) mma_commit(&sh.drain);
-                __syncwarp();
-                const unsigned long long since = global_timer_ns();
-                while (!mbar_try_wait(&sh.drain, 0) && global_timer_ns() - since < kWaitLimitNs) {
-                }
+                tc_fence_after();
+                scores(i + 1);
             }
         }
+        // steps that only the other tile takes
+        for (int i = ns; i < n && !bad; ++i) {
+            if (!warp_wait(&sh.v_full[i % kSteps], (i / kSteps) & 1, abort_flag)) {
+                bad = true;
+                break;
+            }
+            if (elect_one())
+                for (int c = 0; c < per; ++c) mbar_arrive(&sh.empty[(i * per + c) % kRing]);
+            __syncwarp();
+        }
+        if (bad) {
+            if (lane == 0) sh.abort = 1;
+            __syncwarp();
+            if (elect_one()) mma_commit(&sh.drain[s]);
+            __syncwarp();
+            const unsigned long long since = global_timer_ns();
+            while (!mbar_try_wait(&sh.drain[s], 0) && global_timer_ns() - since < kWaitLimitNs) {
+            }
+        }
+    }
     } else {
         // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int s = warp >> 2;
         const int row = row0 + s * kRows + 32 * (warp & 3) + lane;  // in the sequence
         const bool live = some && row < seq.nq;
@@ -292,23 +308,27 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
             tc_fence_after();
             const bool masked = all_see < (i + 1) * kRows - 1;
             const int lim = last - i * kRows;  // keys 0 .. lim of the tile
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float x[kRows];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float x[32];
-                tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(x));
-                tmem_wait_ld();
-                if (flip) {
+            for (int c = 0; c < 4; ++c)
+                tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(x + 32 * c));
+            tmem_wait_ld();
+            if (flip) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = -x[e];
-                }
-                if (masked) {
+                for (int e = 0; e < kRows; ++e) x[e] = -x[e];
+            }
+            if (masked) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * c + e > lim) x[e] = -INFINITY;
-                }
+                for (int e = 0; e < kRows; ++e)
+                    if (e > lim) x[e] = -INFINITY;
+            }
+            float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], x[e]);
+            for (int e = 4; e < kRows; e += 8) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    mx[z] = e + 4 + z < kRows ? fmaxf(mx[z], fmaxf(x[e + z], x[e + 4 + z]))
+                                              : fmaxf(mx[z], x[e + z]);
             }
             const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * qs);
             if (i == 0) m = mn;
@@ -317,44 +337,33 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
                 const float fac = need ? exp2f(m - mn) : 1.f;
                 if (need) m = mn;
                 l *= fac;
-                for (int c = 0; c < a.Dv; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(to + c, o);
+                for (int c = 0; c < a.Dv; c += 16) {
+                    float o[16];
+                    tmem_ld16(to + c, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = __float_as_uint(__uint_as_float(o[e]) * fac);
-                    tmem_st32(to + c, o);
+                    for (int e = 0; e < 16; ++e) o[e] *= fac;
+                    tmem_st16(to + c, o);
                 }
             }
             const float base = m == -INFINITY ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 q2 = make_float2(qs, qs), b2 = make_float2(-base, -base);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                float x[32];
-                tmem_ld32(ts + 32 * c, reinterpret_cast<uint32_t*>(x));
-                tmem_wait_ld();
-                if (flip) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = -x[e];
-                }
-                if (masked) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * c + e > lim) x[e] = -INFINITY;
-                }
+                // over scores that have been read: 16 columns hold 32 weights
                 float p[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    const float e0 = fast_exp2(fmaf(x[e], qs, -base));
-                    const float e1 = fast_exp2(fmaf(x[e + 1], qs, -base));
-                    sum[(e >> 1) & 3] += e0 + e1;
-                    p[e >> 1] = __uint_as_float(pack_bf16(e0, e1));
+                    const float2 y =
+                        ffma2(make_float2(x[32 * c + e], x[32 * c + e + 1]), q2, b2);
+                    const float2 z = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                    sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], z);
+                    p[e >> 1] = __uint_as_float(pack_bf16(z.x, z.y));
                 }
-                // over scores that have been read: 16 columns hold 32 weights
                 tmem_st16(ts + 16 * c, p);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             const int valid = seq.nk - i * kRows;
             if (valid < kRows) {
                 // rows behind the sequence's keys: a weight of zero does not keep
@@ -412,6 +421,18 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
     if (warp == kMmaWarp) tmem_free(tmem, kTmemCols);
 }
 
+template <int KC, int VC>
+cudaError_t go_expanded(const ExpandedArgs& a, const CUtensorMap& qmap, const CUtensorMap& kvmap,
+                        const CUtensorMap& ropemap, cudaStream_t stream) {
+    const ExpandedLayout L(a.Dn);
+    const cudaError_t e = cudaFuncSetAttribute(
+        expanded_mma_kernel<KC, VC>, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+    if (e != cudaSuccess) return e;
+    const int units = (a.Nq + 2 * kRows - 1) / (2 * kRows) + a.Q;
+    return launch_pdl(expanded_mma_kernel<KC, VC>, dim3(a.H, units), dim3(kThreads), L.total,
+                      stream, a, qmap, kvmap, ropemap);
+}
+
 }  // namespace
 
 cudaError_t launch_expanded_mma(const ExpandedArgs& a, cudaStream_t stream) {
@@ -426,14 +447,10 @@ cudaError_t launch_expanded_mma(const ExpandedArgs& a, cudaStream_t stream) {
         e = a.Nk > 0 ? encode_rows(&kvmap, kv, kw, kw, nk, kRows, 1)
                      : encode_rows(&kvmap, kv, 64, 64, nk, kRows, 1);
     if (e == cudaSuccess) e = encode_rows(&ropemap, rope, a.P, a.P, nk, kRows, 1);
-    const ExpandedLayout L(a.Dn);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(expanded_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 L.total);
     if (e != cudaSuccess) return e;
-    const int units = (a.Nq + 2 * kRows - 1) / (2 * kRows) + a.Q;
-    return launch_pdl(expanded_mma_kernel, dim3(a.H, units), dim3(kThreads), L.total, stream, a,
-                      qmap, kvmap, ropemap);
+    auto go = a.Dn == 128 ? (a.Dv == 128 ? go_expanded<3, 2> : go_expanded<3, 1>)
+                          : (a.Dv == 128 ? go_expanded<2, 2> : go_expanded<2, 1>);
+    return go(a, qmap, kvmap, ropemap, stream);
 }
 
 }  // namespace kvd
