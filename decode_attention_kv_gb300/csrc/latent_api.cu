@@ -54,7 +54,9 @@ kvd_status latent_plan(const char* fn, int Q, int T, int H, int BS, int cols, in
     if ((long long)T * H > 65535) return fail(KVD_ERR_UNSUPPORTED, "%s: T*H > 65535", fn);
     if ((long long)cols * BS >= (1ll << 31)) return fail(KVD_ERR_UNSUPPORTED, "%s: cols*BS >= 2^31", fn);
     const bool mma = dt == KVD_BF16;
-    const int rows = T * H, most = mma ? 64 : 16, ctas = mma ? kLatentSMs : 2 * kLatentSMs;
+    // fp32: two CTAs an SM, above R = 256 one (shared memory)
+    const int rows = T * H, most = mma ? 64 : 16,
+              ctas = mma || R > 256 ? kLatentSMs : 2 * kLatentSMs;
     pl->groups = (rows + most - 1) / most;
     pl->rpg = (rows + pl->groups - 1) / pl->groups;
     pl->workers = pl->groups < ctas ? ctas / pl->groups : 1;
@@ -163,7 +165,7 @@ kvd_status kvd_attend_latent(const void* q_latent, const void* q_rope, const voi
     a.part_lse = reinterpret_cast<float*>(ws + pl.off_lse);
     a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
     cudaError_t e = dtype == KVD_BF16 ? launch_latent_mma(a, (cudaStream_t)stream)
-                                      : launch_latent_simt(a, dtype, (cudaStream_t)stream);
+                                      : launch_latent_simt(a, (cudaStream_t)stream);
     if (e == cudaSuccess) e = launch_latent_combine(a, dtype, (cudaStream_t)stream);
     return launched(fn, e);
 }
@@ -209,7 +211,7 @@ kvd_status kvd_attend_expanded(const void* q, const void* kv, const void* k_rope
     a.qscale = scale * kLog2e;
     a.causal = causal != 0;
     return launched(fn, dtype == KVD_BF16 ? launch_expanded_mma(a, (cudaStream_t)stream)
-                                          : launch_expanded_simt(a, dtype, (cudaStream_t)stream));
+                                          : launch_expanded_simt(a, (cudaStream_t)stream));
 }
 
 kvd_status kvd_verify_drafts(const void* target_probs, const void* draft_probs,

@@ -166,7 +166,7 @@ __device__ __forceinline__ int used_workers(const LatentArgs& a, int tot) {
 // Merges the partial rows of sequences that several workers share.
 cudaError_t launch_latent_combine(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream);
 cudaError_t launch_latent_mma(const LatentArgs& a, cudaStream_t stream);
-cudaError_t launch_latent_simt(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream);
+cudaError_t launch_latent_simt(const LatentArgs& a, cudaStream_t stream);
 
 struct ExpandedArgs {
     const void* q;       // [Nq, H, Dn + P]
@@ -208,7 +208,7 @@ __device__ __forceinline__ PackedSeq packed_seq(const ExpandedArgs& a, int b) {
 }
 
 cudaError_t launch_expanded_mma(const ExpandedArgs& a, cudaStream_t stream);
-cudaError_t launch_expanded_simt(const ExpandedArgs& a, kvd_dtype dt, cudaStream_t stream);
+cudaError_t launch_expanded_simt(const ExpandedArgs& a, cudaStream_t stream);
 
 cudaError_t launch_append_latent(void* latent, void* rope, const void* latent_new,
                                  const void* rope_new, const int32_t* block_tables,

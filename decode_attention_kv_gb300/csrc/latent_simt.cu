@@ -1,72 +1,95 @@
-// latent_simt.cu -- attention over latent caches on CUDA cores.
+// latent_simt.cu -- attention over latent caches and expanded rows in fp32, on
+// CUDA cores, and the merge of partial rows.
 //
-// One tile is 16 query rows x 32 keys, both in fp32 shared memory.  Scores:
-// 4 slices of the inner dimension x 64 threads, each 4 rows x 2 keys, so six
-// 16-byte shared loads feed 32 fused multiply-adds.  Softmax: 16 threads a row
-// keep the running max and sum.  Values: a thread owns 4 dims x RPT rows.
+// One tile is 16 query rows x 32 keys in shared memory; the next tile's keys
+// arrive by cp.async meanwhile (two buffers).  Scores: 4 slices of the inner
+// dimension x 64 threads, each 4 rows x 2 keys, so six 16-byte shared loads feed
+// 16 packed multiply-adds (32 products).  Softmax: 16 threads a row keep the
+// running max and sum.  Values: a thread owns 4 dims x RPT rows.
 #include "kvd_internal.h"
 #include "latent_common.cuh"
+#include "tcgen05_ptx.cuh"  // bar_sync
 
 namespace kvd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a group: one tile of keys at a time
+constexpr int kGroups = 2;     // groups of a CTA of the expanded form, every other tile each
 constexpr int kRows = 16;   // query rows per tile
 constexpr int kKeys = 32;   // keys per tile
+
+// Row strides of the scores [slice, row, key] and of the weights [key, row]: no
+// bank conflicts where 16 threads read a row's scores, two-way where they write
+// its weights (8-way both at strides of 32 and 16).
+constexpr int kSs = kKeys + 1, kPs = kRows + 4;
 
 // Shared memory of one CTA, in floats.
 struct SimtLayout {
     int qs, q, k, v, s, p, total;  // qs: padded row stride of q and k
-    int vs;                        // row stride of v
-    __host__ __device__ SimtLayout(int D, int Dv, bool own_v) {
+    int ks, vs;                    // floats of a key buffer, row stride of v
+    int vb;                        // floats of a value buffer (0: the keys are the values)
+    int group;                     // floats of a group (k, v, s, p; group 0's are given)
+    __host__ __device__ SimtLayout(int D, int Dv, bool own_v, int groups) {
         qs = D + 4;
+        ks = kKeys * qs;
+        vs = own_v ? Dv : qs;
+        vb = own_v ? kKeys * Dv : 0;
         q = 0;
         k = q + kRows * qs;
-        vs = own_v ? Dv : qs;
-        v = own_v ? k + kKeys * qs : k;
-        s = k + kKeys * qs + (own_v ? kKeys * Dv : 0);
-        p = s + 4 * kKeys * kRows;
-        total = p + kKeys * kRows + 2 * kRows;
+        v = k + 2 * ks;
+        s = v + 2 * vb;
+        p = s + 4 * kRows * kSs;
+        group = p + kKeys * kPs + kRows - k;
+        total = k + groups * group;
     }
 };
 
-template <typename Elem>
-__device__ __forceinline__ float4 load4(const Elem* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-    return *reinterpret_cast<const float4*>(p);
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool some) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(some ? 16 : 0)
+                 : "memory");
 }
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    const float2 a = bf16x2_to_float2(w.x), b = bf16x2_to_float2(w.y);
-    return make_float4(a.x, a.y, b.x, b.y);
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the newest N groups
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A row of `n` floats (a multiple of 4), by one warp.
+__device__ __forceinline__ void copy_row(float* dst, const float* src, int n, bool some) {
+    for (int c = 4 * (threadIdx.x & 31); c < n; c += 128) copy16(dst + c, src + c, some);
 }
 
 // Running state of one tile of rows, advanced one tile of keys at a time.
 template <int RPT>
 struct RowState {
-    float4 acc[RPT];
+    float2 acc[RPT][2];
     float m, l;  // of softmax row tid / 16
 
     __device__ void clear() {
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < RPT; ++i) acc[i][0] = acc[i][1] = make_float2(0.f, 0.f);
         m = -INFINITY;
         l = 0.f;
     }
 
-    // last: the newest key (index in the tile) that softmax row tid / 16 sees.
-    // valid: one bit per key of the tile.
-    __device__ void step(float* sm, const SimtLayout& L, int D, int Dv, float qscale, int last,
+    // kt, vt: the tile's keys and values.  last: the newest key (index in the
+    // tile) that softmax row tid / 16 sees.  valid: one bit per key of the tile.
+    // sm: the group's shared memory; q: the queries; tid: the thread of the group;
+    // bar: its barrier.
+    __device__ void step(float* sm, const SimtLayout& L, const float* queries, const float* keys,
+                         const float* vals, int tid, int bar, int D, int Dv, float qscale, int last,
                          uint32_t valid) {
-        const int tid = threadIdx.x;
         {
             const int slice = tid >> 6, u = tid & 63, rt = u >> 4, kt = u & 15;
             const int per = D / 4;  // D is a multiple of 64
-            const float* q = sm + L.q + 4 * rt * L.qs + slice * per;
-            const float* k = sm + L.k + kt * L.qs + slice * per;
-            float s[4][2] = {};
+            const float* q = queries + 4 * rt * L.qs + slice * per;
+            const float* k = keys + kt * L.qs + slice * per;
+            float2 s[4][2] = {};
+#pragma unroll 2
             for (int j = 0; j < per; j += 4) {
                 float4 kx[2];
 #pragma unroll
@@ -77,17 +100,18 @@ struct RowState {
                     const float4 qx = *reinterpret_cast<const float4*>(q + r * L.qs + j);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        s[r][i] = fmaf(qx.x, kx[i].x,
-                                       fmaf(qx.y, kx[i].y,
-                                            fmaf(qx.z, kx[i].z, fmaf(qx.w, kx[i].w, s[r][i]))));
+                        s[r][i] = ffma2(make_float2(qx.x, qx.y), make_float2(kx[i].x, kx[i].y),
+                                        ffma2(make_float2(qx.z, qx.w),
+                                              make_float2(kx[i].z, kx[i].w), s[r][i]));
                 }
             }
+            float* to = sm + L.s + (slice * kRows + 4 * rt) * kSs + kt;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<float4*>(sm + L.s + (slice * kKeys + kt + 16 * i) * kRows + 4 * rt) =
-                    make_float4(s[0][i], s[1][i], s[2][i], s[3][i]);
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) to[r * kSs + 16 * i] = s[r][i].x + s[r][i].y;
         }
-        __syncthreads();
+        bar_sync(bar, kThreads);
         {
             const int row = tid >> 4, c = tid & 15;
             float x[2];
@@ -96,7 +120,7 @@ struct RowState {
                 const int key = c + 16 * i;
                 float s = 0.f;
 #pragma unroll
-                for (int z = 0; z < 4; ++z) s += sm[L.s + (z * kKeys + key) * kRows + row];
+                for (int z = 0; z < 4; ++z) s += sm[L.s + (z * kRows + row) * kSs + key];
                 x[i] = (key <= last && ((valid >> key) & 1u)) ? s * qscale : -INFINITY;
             }
             float mx = fmaxf(x[0], x[1]);
@@ -110,52 +134,68 @@ struct RowState {
             for (int i = 0; i < 2; ++i) {
                 const float p = exp2f(x[i] - base);
                 sum += p;
-                sm[L.p + (c + 16 * i) * kRows + row] = p;
+                sm[L.p + (c + 16 * i) * kPs + row] = p;
             }
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             l = l * corr + sum;
             m = mn;
-            if (c == 0) sm[L.p + kKeys * kRows + row] = corr;
+            if (c == 0) sm[L.p + kKeys * kPs + row] = corr;
         }
-        __syncthreads();
+        bar_sync(bar, kThreads);
         {
             const int dgs = Dv / 4, dg = tid % dgs, rg = tid / dgs;
             if (rg < kRows / RPT) {
-                const float* corr = sm + L.p + kKeys * kRows + rg * RPT;
+                const float* corr = sm + L.p + kKeys * kPs + rg * RPT;
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
-                    acc[i].x *= corr[i];
-                    acc[i].y *= corr[i];
-                    acc[i].z *= corr[i];
-                    acc[i].w *= corr[i];
+                    const float2 c = make_float2(corr[i], corr[i]);
+                    acc[i][0] = fmul2(acc[i][0], c);
+                    acc[i][1] = fmul2(acc[i][1], c);
                 }
-                const float* v = sm + L.v + 4 * dg;
+                const float* v = vals + 4 * dg;
                 const float* p = sm + L.p + rg * RPT;
+#pragma unroll 4
                 for (int k = 0; k < kKeys; ++k) {
                     const float4 x = *reinterpret_cast<const float4*>(v + k * L.vs);
+                    float w[RPT];
+                    if constexpr (RPT % 4 == 0) {
+#pragma unroll
+                        for (int i = 0; i < RPT; i += 4)
+                            *reinterpret_cast<float4*>(w + i) =
+                                *reinterpret_cast<const float4*>(p + k * kPs + i);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < RPT; ++i) w[i] = p[k * kPs + i];
+                    }
 #pragma unroll
                     for (int i = 0; i < RPT; ++i) {
-                        const float w = p[k * kRows + i];
-                        acc[i].x = fmaf(w, x.x, acc[i].x);
-                        acc[i].y = fmaf(w, x.y, acc[i].y);
-                        acc[i].z = fmaf(w, x.z, acc[i].z);
-                        acc[i].w = fmaf(w, x.w, acc[i].w);
+                        const float2 ww = make_float2(w[i], w[i]);
+                        acc[i][0] = ffma2(ww, make_float2(x.x, x.y), acc[i][0]);
+                        acc[i][1] = ffma2(ww, make_float2(x.z, x.w), acc[i][1]);
                     }
                 }
             }
         }
-        __syncthreads();
+        bar_sync(bar, kThreads);
     }
 
-    // Leaves every row's sum and max in shared memory: sm[s + row], sm[s + 16 + row].
-    __device__ void publish(float* sm, const SimtLayout& L) {
-        const int tid = threadIdx.x;
+    // Leaves every row's sum and max in the group's shared memory: sm[s + row],
+    // sm[s + 16 + row].  Called by the whole CTA.
+    __device__ void publish(float* sm, const SimtLayout& L, int tid) {
         if ((tid & 15) == 0) {
             sm[L.s + (tid >> 4)] = l;
             sm[L.s + kRows + (tid >> 4)] = m;
         }
         __syncthreads();
+    }
+
+    // This thread's 4 dims of its row i, divided by the row's sum.
+    __device__ float4 result(const float* sm, const SimtLayout& L, int r, int i) const {
+        const float sum = sm[L.s + r];
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        return make_float4(acc[i][0].x * inv, acc[i][0].y * inv, acc[i][1].x * inv,
+                           acc[i][1].y * inv);
     }
 };
 
@@ -163,18 +203,19 @@ __device__ __forceinline__ float lse2_of(float m, float l) {
     return l > 0.f ? m + log2f(l) : (l == 0.f ? -INFINITY : NAN);
 }
 
-template <typename Elem, int RPT>
+template <int RPT>
 __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs a) {
     extern __shared__ __align__(16) float sm[];
     __shared__ int scratch[kFindWords];
-    __shared__ long long rows_of[kKeys];
     pdl_launch_dependents();
     pdl_wait();
-    const int tid = threadIdx.x, g = blockIdx.x, w = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x, w = blockIdx.y;
     const int D = a.R + a.P;
-    const SimtLayout L(D, a.R, false);
+    const SimtLayout L(D, a.R, false, 1);
+    const float* latent = static_cast<const float*>(a.latent);
+    const float* rope = static_cast<const float*>(a.rope);
     int W = 1;
-    Found f = block_find<kThreads>(
+    const Found f = block_find<kThreads>(
         a.Q, scratch,
         [&](int tot) {
             W = used_workers(a, tot);
@@ -196,52 +237,57 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
         // the run's part of the sequence's places: `lead` of them, then its tiles
         const int first = max(0, t - before - a.lead), end = min(nt, t1 - before - a.lead);
         if (end <= first) break;  // the run ends before the first tile
-        // the group's queries
-        for (int i = tid; i < kRows * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = 4 * (i % (D / 4));
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < nrows) {
-                const size_t row = (size_t)b * a.rows + row0 + r;
-                x = c < a.R ? load4(static_cast<const Elem*>(a.q_latent) + row * a.R + c)
-                            : load4(static_cast<const Elem*>(a.q_rope) + row * a.P + (c - a.R));
+        // Starts the copies of tile k into buffer `buf` and returns its valid keys
+        // (lane: the key); a warp brings every eighth of them.
+        auto fetch = [&](int k, int buf) {
+            const int key = k * kKeys + lane;
+            long long row = -1;
+            if (key < seq.n) {
+                const int phys = a.block_tables[(size_t)b * a.cols + seq.col0 + key / a.BS];
+                if (phys >= 0 && phys < a.NB)
+                    row = (long long)phys * a.BS + key % a.BS;
+                else if (warp == 0)
+                    report(a.dev_status, KVD_DEV_BLOCK_RANGE);
             }
-            *reinterpret_cast<float4*>(sm + L.q + r * L.qs + c) = x;
+#pragma unroll
+            for (int i = 0; i < kKeys / 8; ++i) {
+                const int r = warp + 8 * i;
+                const long long from = __shfl_sync(0xffffffffu, row, r);
+                float* to = sm + L.k + buf * L.ks + r * L.qs;
+                const size_t at = from < 0 ? 0 : (size_t)from;
+                copy_row(to, latent + at * a.R, a.R, from >= 0);
+                copy_row(to + a.R, rope + at * a.P, a.P, from >= 0);
+            }
+            return __ballot_sync(0xffffffffu, row >= 0);
+        };
+        // the group's queries, with the first tile
+#pragma unroll
+        for (int i = 0; i < kRows / 8; ++i) {
+            const int r = warp + 8 * i;
+            const size_t row = (size_t)b * a.rows + row0 + min(r, nrows - 1);
+            copy_row(sm + L.q + r * L.qs, static_cast<const float*>(a.q_latent) + row * a.R, a.R,
+                     r < nrows);
+            copy_row(sm + L.q + r * L.qs + a.R, static_cast<const float*>(a.q_rope) + row * a.P,
+                     a.P, r < nrows);
         }
+        uint32_t valid = fetch(first, 0);
+        copies_commit();
         st.clear();
         const int srow = tid >> 4;
         // newest key the softmax row sees
         const int last = srow < nrows ? seq.n - a.T + (row0 + srow) / a.H : -1;
         for (int k = first; k < end; ++k) {
-            if (tid < kKeys) {
-                const int key = k * kKeys + tid;
-                long long row = -1;
-                if (key < seq.n) {
-                    const long long phys =
-                        a.block_tables[(size_t)b * a.cols + seq.col0 + key / a.BS];
-                    if (phys < 0 || phys >= a.NB) {
-                        report(a.dev_status, KVD_DEV_BLOCK_RANGE);
-                    } else {
-                        row = phys * a.BS + key % a.BS;
-                    }
-                }
-                rows_of[tid] = row;
-                const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0);
-                if (tid == 0) scratch[34] = (int)valid;
-            }
+            const int buf = (k - first) & 1;
+            uint32_t next = 0;
+            if (k + 1 < end) next = fetch(k + 1, buf ^ 1);
+            copies_commit();
+            copies_wait<1>();
             __syncthreads();
-            for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
-                const int r = i / (D / 4), c = 4 * (i % (D / 4));
-                const long long row = rows_of[r];
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (row >= 0)
-                    x = c < a.R ? load4(static_cast<const Elem*>(a.latent) + row * a.R + c)
-                                : load4(static_cast<const Elem*>(a.rope) + row * a.P + (c - a.R));
-                *reinterpret_cast<float4*>(sm + L.k + r * L.qs + c) = x;
-            }
-            __syncthreads();
-            st.step(sm, L, D, a.R, a.qscale, last - k * kKeys, (uint32_t)scratch[34]);
+            const float* keys = sm + L.k + buf * L.ks;
+            st.step(sm, L, sm + L.q, keys, keys, tid, 1, D, a.R, a.qscale, last - k * kKeys, valid);
+            valid = next;
         }
-        st.publish(sm, L);
+        st.publish(sm, L, tid);
         const bool whole = first == 0 && end == nt;
         const size_t slot = ((size_t)w * a.groups + g) * 2 + (t == t0 ? 0 : 1);
         const int dgs = a.R / 4, dg = tid % dgs, rg = tid / dgs;
@@ -249,16 +295,11 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
                 const int r = rg * RPT + i;
-                if (r >= nrows) break;
-                const float sum = sm[L.s + r];
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                const float4 x = make_float4(st.acc[i].x * inv, st.acc[i].y * inv,
-                                             st.acc[i].z * inv, st.acc[i].w * inv);
-                if (whole) {
+                if (r < nrows) {
                     const size_t row = (size_t)b * a.rows + row0 + r;
-                    ElemTraits<Elem>::store4(a.out, row * a.R + 4 * dg, x);
-                } else {
-                    *reinterpret_cast<float4*>(a.part_o + (slot * a.rpg + r) * a.R + 4 * dg) = x;
+                    float* to = whole ? static_cast<float*>(a.out) + row * a.R
+                                      : a.part_o + (slot * a.rpg + r) * a.R;
+                    *reinterpret_cast<float4*>(to + 4 * dg) = st.result(sm, L, r, i);
                 }
             }
         }
@@ -278,16 +319,19 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
     }
 }
 
-template <typename Elem, int RPT>
-__global__ void __launch_bounds__(kThreads) expanded_simt_kernel(const ExpandedArgs a) {
-    extern __shared__ __align__(16) float sm[];
+template <int RPT>
+__global__ void __launch_bounds__(kGroups * kThreads) expanded_simt_kernel(const ExpandedArgs a) {
+    extern __shared__ __align__(16) float smem[];
     __shared__ int scratch[kFindWords];
     pdl_launch_dependents();
     pdl_wait();
-    const int tid = threadIdx.x, h = blockIdx.y, unit = blockIdx.x;
+    // tid, warp: of the group
+    const int group = threadIdx.x / kThreads, tid = threadIdx.x % kThreads, warp = tid >> 5;
+    const int h = blockIdx.y, unit = blockIdx.x;
     const int D = a.Dn + a.P;
-    const SimtLayout L(D, a.Dv, true);
-    const Found f = block_find<kThreads>(
+    const SimtLayout L(D, a.Dv, true, kGroups);
+    float* sm = smem + group * L.group;
+    const Found f = block_find<kGroups * kThreads>(
         a.Q, scratch, [&](int) { return unit; },
         [&](int b) {
             const PackedSeq s = packed_seq(a, b);
@@ -296,64 +340,102 @@ __global__ void __launch_bounds__(kThreads) expanded_simt_kernel(const ExpandedA
         });
     if (f.item >= a.Q) return;
     const PackedSeq seq = packed_seq(a, f.item);
-    const int row0 = (unit - f.before) * kRows, nrows = min(kRows, seq.nq - row0);
-    const Elem* kv = static_cast<const Elem*>(a.kv);
-    for (int i = tid; i < kRows * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), c = 4 * (i % (D / 4));
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < nrows)
-            x = load4(static_cast<const Elem*>(a.q) +
-                      ((size_t)(seq.q0 + row0 + r) * a.H + h) * D + c);
-        *reinterpret_cast<float4*>(sm + L.q + r * L.qs + c) = x;
-    }
-    RowState<RPT> st;
-    st.clear();
+    // the last rows of a sequence first: under the causal mask they see most keys
+    const int units = (seq.nq + kRows - 1) / kRows;
+    const int row0 = (units - 1 - (unit - f.before)) * kRows, nrows = min(kRows, seq.nq - row0);
+    const float* kv = static_cast<const float*>(a.kv);
+    const float* rope = static_cast<const float*>(a.k_rope);
     const int shift = a.causal ? seq.nk - seq.nq : seq.nk - 1;
     const int srow = tid >> 4;
     const int last = srow < nrows ? (a.causal ? row0 + srow + shift : shift) : -1;
     const int nkeys = a.causal ? min(seq.nk, row0 + nrows + shift) : seq.nk;
-    for (int k0 = 0; k0 < nkeys; k0 += kKeys) {
-        const int n = min(kKeys, nkeys - k0);
-        __syncthreads();
-        for (int i = tid; i < kKeys * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = 4 * (i % (D / 4));
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < n) {
-                const size_t key = (size_t)seq.k0 + k0 + r;
-                x = c < a.Dn ? load4(kv + (key * a.H + h) * (a.Dn + a.Dv) + c)
-                             : load4(static_cast<const Elem*>(a.k_rope) + key * a.P + (c - a.Dn));
-            }
-            *reinterpret_cast<float4*>(sm + L.k + r * L.qs + c) = x;
+    // Starts the copies of the keys from k0 on into buffer `buf`: a warp every
+    // eighth key, a lane 16 bytes of each part of it (parts are at most 128 floats).
+    const int lane = tid & 31, c4 = 4 * lane;
+    const size_t stride = (size_t)a.H * (a.Dn + a.Dv);
+    const float* kv_lane = kv + ((size_t)seq.k0 * a.H + h) * (a.Dn + a.Dv) + c4;
+    const float* rope_lane = rope + (size_t)seq.k0 * a.P + c4;
+    auto fetch = [&](int k0, int buf) {
+        float* kd = sm + L.k + buf * L.ks + warp * L.qs + c4;
+        float* vd = sm + L.v + buf * L.vb + warp * L.vs + c4;
+#pragma unroll
+        for (int i = 0; i < kKeys / 8; ++i) {
+            const int r = k0 + warp + 8 * i;
+            const bool some = r < nkeys;
+            const float* row = kv_lane + (some ? r : 0) * stride;
+            if (c4 < a.Dn) copy16(kd + 8 * i * L.qs, row, some);
+            if (c4 < a.P)
+                copy16(kd + 8 * i * L.qs + a.Dn, rope_lane + (size_t)(some ? r : 0) * a.P, some);
+            if (c4 < a.Dv) copy16(vd + 8 * i * L.vs, row + a.Dn, some);
         }
-        for (int i = tid; i < kKeys * (a.Dv / 4); i += kThreads) {
-            const int r = i / (a.Dv / 4), c = 4 * (i % (a.Dv / 4));
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < n)
-                x = load4(kv + (((size_t)seq.k0 + k0 + r) * a.H + h) * (a.Dn + a.Dv) + a.Dn + c);
-            *reinterpret_cast<float4*>(sm + L.v + r * L.vs + c) = x;
-        }
-        __syncthreads();
-        st.step(sm, L, D, a.Dv, a.qscale, last - k0, n == 32 ? ~0u : (1u << n) - 1u);
+    };
+    for (int r = threadIdx.x >> 5; r < kRows; r += kGroups * kThreads / 32)
+        copy_row(smem + L.q + r * L.qs,
+                 static_cast<const float*>(a.q) +
+                     ((size_t)(seq.q0 + row0 + min(r, nrows - 1)) * a.H + h) * D,
+                 D, r < nrows);
+    constexpr int kStride = kGroups * kKeys;
+    const int first = group * kKeys;
+    if (first < nkeys) fetch(first, 0);
+    copies_commit();
+    copies_wait<0>();
+    __syncthreads();
+    RowState<RPT> st;
+    st.clear();
+    for (int k0 = first; k0 < nkeys; k0 += kStride) {
+        const int buf = (k0 / kStride) & 1, n = min(kKeys, nkeys - k0);
+        if (k0 + kStride < nkeys) fetch(k0 + kStride, buf ^ 1);
+        copies_commit();
+        copies_wait<1>();
+        bar_sync(1 + group, kThreads);
+        st.step(sm, L, smem + L.q, sm + L.k + buf * L.ks, sm + L.v + buf * L.vb, tid, 1 + group, D,
+                a.Dv, a.qscale, last - k0, n == 32 ? ~0u : (1u << n) - 1u);
+    }
+    copies_wait<0>();
+    __syncthreads();
+    // the groups' rows by their maxima: the second leaves its own where its keys were
+    const int dgs = a.Dv / 4, dg = tid % dgs, rg = tid / dgs;
+    float4* other = reinterpret_cast<float4*>(smem + L.group + L.k);
+    st.publish(sm, L, tid);
+    if (group == 1 && rg < kRows / RPT) {
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+            other[(rg * RPT + i) * dgs + dg] = make_float4(st.acc[i][0].x, st.acc[i][0].y,
+                                                           st.acc[i][1].x, st.acc[i][1].y);
     }
     __syncthreads();
-    st.publish(sm, L);
-    const int dgs = a.Dv / 4, dg = tid % dgs, rg = tid / dgs;
+    if (group == 1) return;
+    const float* sum0 = smem + L.s;
+    const float* sum1 = smem + L.group + L.s;
+    auto merged = [&](int r, float& c0, float& c1, float& m) {
+        const float m0 = sum0[kRows + r], m1 = sum1[kRows + r];
+        m = fmaxf(m0, m1);
+        const float base = m == -INFINITY ? 0.f : m;
+        c0 = exp2f(m0 - base);
+        c1 = exp2f(m1 - base);
+        return sum0[r] * c0 + sum1[r] * c1;
+    };
+    float c0, c1, m;
     if (rg < kRows / RPT) {
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
             const int r = rg * RPT + i;
-            if (r >= nrows) break;
-            const float sum = sm[L.s + r];
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            ElemTraits<Elem>::store4(
-                a.out, ((size_t)(seq.q0 + row0 + r) * a.H + h) * a.Dv + 4 * dg,
-                make_float4(st.acc[i].x * inv, st.acc[i].y * inv, st.acc[i].z * inv,
-                            st.acc[i].w * inv));
+            if (r < nrows) {
+                const float l = merged(r, c0, c1, m), inv = l == 0.f ? 0.f : 1.f / l;
+                const float4 o = other[r * dgs + dg];
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out) +
+                                           ((size_t)(seq.q0 + row0 + r) * a.H + h) * a.Dv + 4 * dg) =
+                    make_float4((st.acc[i][0].x * c0 + o.x * c1) * inv,
+                                (st.acc[i][0].y * c0 + o.y * c1) * inv,
+                                (st.acc[i][1].x * c0 + o.z * c1) * inv,
+                                (st.acc[i][1].y * c0 + o.w * c1) * inv);
+            }
         }
     }
-    if (tid < nrows && a.lse_out)
-        a.lse_out[(size_t)(seq.q0 + row0 + tid) * a.H + h] =
-            lse2_of(sm[L.s + kRows + tid], sm[L.s + tid]) * kLn2;
+    if (tid < nrows && a.lse_out) {
+        const float l = merged(tid, c0, c1, m);
+        a.lse_out[(size_t)(seq.q0 + row0 + tid) * a.H + h] = lse2_of(m, l) * kLn2;
+    }
 }
 
 // One warp per (row, 128 dims): the workers' partial rows by log-sum-exp.
@@ -423,49 +505,39 @@ __global__ void __launch_bounds__(128) latent_combine_kernel(const LatentArgs a)
     if (d == 0 && a.lse_out) a.lse_out[at] = lse2_of(base, l) * kLn2;
 }
 
-template <typename Elem, int RPT>
+template <int RPT>
 cudaError_t go_latent(const LatentArgs& a, cudaStream_t stream) {
-    const SimtLayout L(a.R + a.P, a.R, false);
+    const SimtLayout L(a.R + a.P, a.R, false, 1);
     const int smem = L.total * 4;
-    cudaError_t e = cudaFuncSetAttribute(latent_simt_kernel<Elem, RPT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(
+        latent_simt_kernel<RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(latent_simt_kernel<Elem, RPT>, dim3(a.groups, a.workers), dim3(kThreads),
-                      smem, stream, a);
-}
-
-template <typename Elem, int RPT>
-cudaError_t go_expanded(const ExpandedArgs& a, cudaStream_t stream) {
-    const SimtLayout L(a.Dn + a.P, a.Dv, true);
-    const int smem = L.total * 4;
-    cudaError_t e = cudaFuncSetAttribute(expanded_simt_kernel<Elem, RPT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const int units = (a.Nq + kRows - 1) / kRows + a.Q;
-    return launch_pdl(expanded_simt_kernel<Elem, RPT>, dim3(units, a.H), dim3(kThreads), smem,
+    return launch_pdl(latent_simt_kernel<RPT>, dim3(a.groups, a.workers), dim3(kThreads), smem,
                       stream, a);
 }
 
-template <typename Elem>
-cudaError_t go(const LatentArgs& a, cudaStream_t stream) {
-    if (a.R > 256) return go_latent<Elem, 8>(a, stream);
-    if (a.R > 128) return go_latent<Elem, 4>(a, stream);
-    return go_latent<Elem, 2>(a, stream);
-}
-
-template <typename Elem>
-cudaError_t go(const ExpandedArgs& a, cudaStream_t stream) {
-    return a.Dv == 128 ? go_expanded<Elem, 2>(a, stream) : go_expanded<Elem, 1>(a, stream);
+template <int RPT>
+cudaError_t go_expanded(const ExpandedArgs& a, cudaStream_t stream) {
+    const SimtLayout L(a.Dn + a.P, a.Dv, true, kGroups);
+    const int smem = L.total * 4;
+    const cudaError_t e = cudaFuncSetAttribute(
+        expanded_simt_kernel<RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int units = (a.Nq + kRows - 1) / kRows + a.Q;
+    return launch_pdl(expanded_simt_kernel<RPT>, dim3(units, a.H), dim3(kGroups * kThreads), smem,
+                      stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_simt(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream) {
-    return dt == KVD_BF16 ? go<__nv_bfloat16>(a, stream) : go<float>(a, stream);
+cudaError_t launch_latent_simt(const LatentArgs& a, cudaStream_t stream) {
+    if (a.R > 256) return go_latent<8>(a, stream);
+    if (a.R > 128) return go_latent<4>(a, stream);
+    return go_latent<2>(a, stream);
 }
 
-cudaError_t launch_expanded_simt(const ExpandedArgs& a, kvd_dtype dt, cudaStream_t stream) {
-    return dt == KVD_BF16 ? go<__nv_bfloat16>(a, stream) : go<float>(a, stream);
+cudaError_t launch_expanded_simt(const ExpandedArgs& a, cudaStream_t stream) {
+    return a.Dv == 128 ? go_expanded<2>(a, stream) : go_expanded<1>(a, stream);
 }
 
 cudaError_t launch_latent_combine(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream) {
