@@ -82,7 +82,7 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sh.q_full[s], 1);
             mbar_init(&sh.s_full[s], 1);
-            mbar_init(&sh.p_full[s], kRows);
+            mbar_init(&sh.p_full[s], kRows / 32);
             mbar_init(&sh.o_full[s], 1);
         }
         for (int i = 0; i < kSteps; ++i) {
@@ -378,7 +378,8 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&sh.p_full[s]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[s]);  // one arrival a warp
         }
         if (ns > 0 && !bad && !mbar_wait(&sh.o_full[s], 0, abort_flag)) bad = true;
         if (__any_sync(0xffffffffu, bad)) {

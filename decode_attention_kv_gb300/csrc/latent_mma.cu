@@ -191,9 +191,9 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
         }
         mbar_init(&sh.s_full[0], 2);
         mbar_init(&sh.s_full[1], 2);
-        mbar_init(&sh.s_free[0], kSoftmax);
-        mbar_init(&sh.s_free[1], kSoftmax);
-        mbar_init(&sh.p_full, kSoftmax);
+        mbar_init(&sh.s_free[0], kSoftmax / 32);
+        mbar_init(&sh.s_free[1], kSoftmax / 32);
+        mbar_init(&sh.p_full, kSoftmax / 32);
         mbar_init(&sh.pv_done, 1);
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_free, 1);
@@ -454,8 +454,9 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                 tc_fence_after();
                 const uint32_t v_low = uniform(desc_low(kv + st * stage_bytes, kChunk));
                 if (elect_one()) {
-#pragma unroll 1
-                    for (int j = 0; j < pairs; ++j) {
+#pragma unroll
+                    for (int j = 0; j < kMaxPairs; ++j) {
+                        if (j >= pairs) break;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             mma_ss(tm + j * N, desc_of(v_low + ((2 * j * kChunk + i * 2048) >> 4)),
@@ -500,6 +501,8 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                 m[h] = -INFINITY;
                 l[h] = 0.f;
             }
+            // newest key that every row of the warp sees
+            const int all_see = __reduce_min_sync(0xffffffffu, min(last[0], last[1]));
             for (int k = s.first; k < s.end; ++k, ++it) {
                 if (!mbar_wait(&sh.s_full[it & 1], (it >> 1) & 1, abort_flag)) bad = true;
                 __syncwarp();
@@ -513,22 +516,21 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                     tmem_wait_ld();
                     tc_fence_before();
                 }
-                mbar_arrive(&sh.s_free[it & 1]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.s_free[it & 1]);  // one arrival a warp
                 if (busy) {
                     if (flip) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = -x[i];
                     }
-                    unsigned long long sees[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int lim = last[h] - k * KT;  // keys 0 .. lim of the tile
-                        sees[h] = valid & (lim >= 63 ? ~0ull : lim < 0 ? 0ull : (2ull << lim) - 1ull);
-                    }
-                    if (!__all_sync(0xffffffffu, (sees[0] & sees[1]) == ~0ull)) {
+                    if (valid != ~0ull || k * KT + 63 > all_see) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const unsigned long long z = sees[h] >> (2 * quad);
+                            const int lim = last[h] - k * KT;  // keys 0 .. lim of the tile
+                            const unsigned long long z =
+                                (valid & (lim >= 63 ? ~0ull
+                                          : lim < 0 ? 0ull
+                                                    : (2ull << lim) - 1ull)) >> (2 * quad);
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 if (!((z >> (8 * (i >> 1) + (i & 1))) & 1ull))
@@ -623,7 +625,8 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                 }
                 fence_async_smem();
                 tc_fence_before();
-                mbar_arrive(&sh.p_full);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full);
                 if (++st == L.stages) {
                     st = 0;
                     par ^= 1;
