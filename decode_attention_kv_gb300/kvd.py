@@ -1169,7 +1169,9 @@ def attend_latent(q_latent, q_rope, latent_cache, rope_cache, block_tables, seq_
             _opt(fn, "seq_offset", seq_offset, dev, i32, (Q,)))
     if out is None:
         out = torch.empty_like(q_latent)
-    op = _arg(fn, "out", out, dev, dtype, (Q, T, H, R))
+        op = out.data_ptr()
+    else:
+        op = _arg(fn, "out", out, dev, dtype, (Q, T, H, R))
     zp = _opt(fn, "lse", lse, dev, torch.float32, (Q, T, H))
     if workspace is None:
         need = attend_latent_workspace_bytes(Q, T, H, BS, cols, R, P, dtype)
@@ -1209,7 +1211,9 @@ def attend_expanded(q, kv, k_rope, q_lens, k_lens, scale=None, causal=True, out=
             _arg(fn, "k_lens", k_lens, dev, i32, (Q + 1,)))
     if out is None:
         out = torch.empty((Nq, H, Dv), dtype=dtype, device=q.device)
-    op = _arg(fn, "out", out, dev, dtype, (Nq, H, Dv))
+        op = out.data_ptr()
+    else:
+        op = _arg(fn, "out", out, dev, dtype, (Nq, H, Dv))
     zp = _opt(fn, "lse", lse, dev, torch.float32, (Nq, H))
     _call_on("kvd_attend_expanded", dev, dev_status, *args, op, zp, Q, Nq, Nk, H, Dn, Dv, P,
              1.0 / math.sqrt(Dqk) if scale is None else scale, 1 if causal else 0,
