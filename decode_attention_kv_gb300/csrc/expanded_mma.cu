@@ -200,13 +200,14 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
         const uint32_t q_low = uniform(desc_low(base + s * KC * kBlock, 16));
         const uint32_t td = uniform(tm + s * kRows), to = uniform(tm + 256 + s * kRows);
         const int n = uniform(nsteps), ns = uniform(steps[s]);
-        // scores of step i; then its blocks are free as far as this tile goes
-        auto scores = [&](int i) {
-            const int b0 = i * per;
-            uint32_t k_low[KC];
+        uint32_t k_low[KC];  // the key blocks of the next scores
+        auto keys_of = [&](int i) {
 #pragma unroll
             for (int c = 0; c < KC; ++c)
-                k_low[c] = uniform(desc_low(base + L.ring + (b0 + c) % kRing * kBlock, 16));
+                k_low[c] = uniform(desc_low(base + L.ring + (i * per + c) % kRing * kBlock, 16));
+        };
+        // scores of step i; then its blocks are free as far as this tile goes
+        auto scores = [&](int i) {
             if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < KC; ++c)
@@ -216,7 +217,7 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
                                desc_of(k_low[c] + 2 * z), sdesc, c > 0 || z > 0);
                 mma_commit(&sh.s_full[s]);
 #pragma unroll
-                for (int c = 0; c < KC; ++c) mma_commit(&sh.empty[(b0 + c) % kRing]);
+                for (int c = 0; c < KC; ++c) mma_commit(&sh.empty[(i * per + c) % kRing]);
             }
             __syncwarp();
         };
@@ -227,6 +228,7 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
             bad = bad || !warp_wait(&sh.q_full[s], 0, abort_flag) ||
                   !warp_wait(&sh.k_full[0], 0, abort_flag);
             tc_fence_after();
+            keys_of(0);
             if (!bad) scores(0);
         }
         for (int i = 0; i < ns && !bad; ++i) {
@@ -236,8 +238,17 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
 #pragma unroll
             for (int c = 0; c < VC; ++c)
                 v_low[c] = uniform(desc_low(base + L.ring + (b0 + c) % kRing * kBlock, 16));
-            if (!warp_wait(&sh.v_full[i % kSteps], (i / kSteps) & 1, abort_flag) ||
-                !warp_wait(&sh.p_full[s], i & 1, abort_flag)) {
+            keys_of(i + 1);
+            // looked at while the softmax still runs; not waited for before the values,
+            // whose blocks the keys' copies may need
+            uint64_t* kf = &sh.k_full[(i + 1) % kSteps];
+            const uint32_t kpar = ((i + 1) / kSteps) & 1;
+            if (!warp_wait(&sh.v_full[i % kSteps], (i / kSteps) & 1, abort_flag)) {
+                bad = true;
+                break;
+            }
+            const bool keys = i + 1 < ns && __all_sync(0xffffffffu, mbar_test(kf, kpar));
+            if (!warp_wait(&sh.p_full[s], i & 1, abort_flag)) {
                 bad = true;
                 break;
             }
@@ -256,7 +267,7 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
             }
             __syncwarp();
             if (i + 1 < ns) {
-                if (!warp_wait(&sh.k_full[(i + 1) % kSteps], ((i + 1) / kSteps) & 1, abort_flag)) {
+                if (!keys && !warp_wait(kf, kpar, abort_flag)) {
                     bad = true;
                     break;
                 }
