@@ -62,7 +62,8 @@ kvd_status latent_plan(const char* fn, int Q, int T, int H, int BS, int cols, in
     pl->workers = pl->groups < ctas ? ctas / pl->groups : 1;
     pl->min_tiles = mma ? 2 : 1;
     pl->lead = mma ? 2 : 1;
-    const size_t slots = (size_t)pl->workers * pl->groups * 2;
+    // a single worker shares no sequence: no partial rows
+    const size_t slots = pl->workers > 1 ? (size_t)pl->workers * pl->groups * 2 : 0;
     pl->off_lse = round256((size_t)(Q < 1 ? 1 : Q) * sizeof(int4));
     pl->off_o = pl->off_lse + round256(slots * pl->rpg * 4);
     pl->bytes = pl->off_o + slots * pl->rpg * R * 4;

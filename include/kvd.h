@@ -650,7 +650,7 @@ kvd_status kvd_combine_gathered(const float* parts, void* out, float* lse_out, i
  *   latent_new [N, R], rope_new [N, P] of `dtype`, packed
  *   new_lens [Q + 1] int32, cumsum starting at 0;  pos [Q] int32 (device)
  *   block_tables [Q, cols] int32;  seq_offset [Q] int32 or NULL (zeros)
- * A byte copy.  Rows at and behind new_lens[Q] are not read.  Device-detected
+ * A byte copy.  Rows at and behind new_lens[Q] go nowhere.  Device-detected
  * errors skip the row (nothing written): new_lens not starting at 0,
  * decreasing or past N (KVD_DEV_SEQLENS), pos[q] < 0 (KVD_DEV_POS_RANGE),
  * seq_offset negative or not a multiple of BS (KVD_DEV_SEQ_OFFSET), table
