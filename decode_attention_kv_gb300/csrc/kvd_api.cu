@@ -383,22 +383,6 @@ namespace kvd {
 void set_last_error(const char* msg) {
     snprintf(g_last_error, sizeof g_last_error, "%s", msg);
 }
-
-cudaError_t encode_rows(CUtensorMap* map, const void* base, long long width, long long stride,
-                        long long rows, int box_rows, int box_chunks) {
-    const cudaError_t e = get_encoder();
-    if (e != cudaSuccess) return e;
-    if (!g_encode) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {64u, (cuuint64_t)rows, (cuuint64_t)(width / 64)};
-    const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, 128u};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    const CUresult r =
-        g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
-                 box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
 }  // namespace kvd
 
 // ===================================================================== C ABI

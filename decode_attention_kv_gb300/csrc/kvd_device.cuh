@@ -136,14 +136,6 @@ __device__ __forceinline__ void tma_g2s_3d(void* dst, const CUtensorMap* map, in
         : "memory");
 }
 
-// The same box into L2 only.
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(c2)
-                 : "memory");
-}
-
 // 2-D tiled tensor copy global -> shared through a tensor map.
 __device__ __forceinline__ void tma_g2s_2d(void* dst, const CUtensorMap* map, int c0, int c1,
                                            uint64_t* bar, uint64_t policy) {
@@ -179,13 +171,6 @@ __device__ __forceinline__ uint64_t policy_evict_first() {
     return p;
 }
 
-// L2 policy for data that other CTAs read again.
-__device__ __forceinline__ uint64_t policy_evict_normal() {
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-
 // ------------------------------------------------------------ packed fp32x2
 
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
@@ -201,15 +186,6 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
 __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
     unsigned long long d;
     asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(d)
-        : "l"(*reinterpret_cast<unsigned long long*>(&a)),
-          "l"(*reinterpret_cast<unsigned long long*>(&b)));
-    return *reinterpret_cast<float2*>(&d);
-}
-
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;"
         : "=l"(d)
         : "l"(*reinterpret_cast<unsigned long long*>(&a)),
           "l"(*reinterpret_cast<unsigned long long*>(&b)));

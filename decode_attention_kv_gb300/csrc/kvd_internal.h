@@ -53,13 +53,6 @@ inline bool small_uses_mma(kvd_dtype dt, int G) { (void)G; return dt == KVD_BF16
 // Sets the message kvd_last_error() returns on this thread.
 void set_last_error(const char* msg);
 
-// Tensor map over `rows` bf16 rows of `stride` elements, of which the first
-// `width` (a multiple of 64) are mapped: (64, rows, width / 64).  A box is
-// box_chunks blocks of box_rows consecutive rows x 64 elements (128 bytes, under
-// the 128-byte swizzle), one block behind the other.
-cudaError_t encode_rows(CUtensorMap* map, const void* base, long long width, long long stride,
-                        long long rows, int box_rows, int box_chunks);
-
 // part_o [R, S, D] / part_lse [R, S]; or, with gathered_stride > 0, split s's
 // rows at part_o + s * gathered_stride ([R, D]) and its log-sum-exps at
 // part_lse + s * gathered_stride ([R]).

@@ -17,7 +17,7 @@
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, a row a thread.  Warps 8 and 9
 // issue the MMAs of tile 0 and 1: what one spends on waiting and setting up (450
 // cycles a step) the other's products fill.  Warp 10 issues the copies.
-#include "kvd_internal.h"
+#include "../kvd_internal.h"
 #include "latent_common.cuh"
 #include "tcgen05_ptx.cuh"
 

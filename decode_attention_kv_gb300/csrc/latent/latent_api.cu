@@ -1,10 +1,13 @@
 // latent_api.cu -- the C ABI of the latent-cache operators: argument checks,
 // plans and launches.  Allocates nothing, never synchronises; every launch
 // goes to the caller's stream.
+#include <cudaTypedefs.h>
+
 #include <cstdarg>
 #include <cstdio>
+#include <mutex>
 
-#include "kvd_internal.h"
+#include "../kvd_internal.h"
 #include "latent_common.cuh"
 
 using namespace kvd;
@@ -70,7 +73,38 @@ kvd_status latent_plan(const char* fn, int Q, int T, int H, int BS, int cols, in
     return KVD_OK;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+cudaError_t g_encode_err = cudaSuccess;
+
 }  // namespace
+
+namespace kvd {
+
+cudaError_t encode_rows(CUtensorMap* map, const void* base, long long width, long long stride,
+                        long long rows, int box_rows, int box_chunks) {
+    std::call_once(g_encode_once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        g_encode_err = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                        cudaEnableDefault, &q);
+        if (g_encode_err == cudaSuccess && q != cudaDriverEntryPointSuccess)
+            g_encode_err = cudaErrorNotSupported;
+        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    if (g_encode_err != cudaSuccess) return g_encode_err;
+    const cuuint64_t dims[3] = {64u, (cuuint64_t)rows, (cuuint64_t)(width / 64)};
+    const cuuint64_t strides[2] = {(cuuint64_t)stride * 2, 128u};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)box_rows, (cuuint32_t)box_chunks};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    const CUresult r =
+        g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                 box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace kvd
 
 extern "C" {
 

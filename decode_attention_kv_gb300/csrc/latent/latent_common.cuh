@@ -13,7 +13,7 @@
 // spends on starting and finishing it.
 #pragma once
 
-#include "kvd_device.cuh"
+#include "../kvd_device.cuh"
 
 namespace kvd {
 
@@ -162,6 +162,13 @@ __device__ __forceinline__ int worker_of(int tile, int tot, int W) {
 __device__ __forceinline__ int used_workers(const LatentArgs& a, int tot) {
     return max(1, min(a.workers, (tot + a.min_tiles - 1) / a.min_tiles));
 }
+
+// Tensor map over `rows` bf16 rows of `stride` elements, of which the first
+// `width` (a multiple of 64) are mapped: (64, rows, width / 64).  A box is
+// box_chunks blocks of box_rows consecutive rows x 64 elements (128 bytes, under
+// the 128-byte swizzle), one block behind the other.
+cudaError_t encode_rows(CUtensorMap* map, const void* base, long long width, long long stride,
+                        long long rows, int box_rows, int box_chunks);
 
 // Merges the partial rows of sequences that several workers share.
 cudaError_t launch_latent_combine(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream);

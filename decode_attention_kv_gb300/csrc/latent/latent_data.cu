@@ -2,7 +2,7 @@
 // tokens: the two latent-decode operators that are bound by memory alone.
 #include <cooperative_groups.h>
 
-#include "kvd_internal.h"
+#include "../kvd_internal.h"
 #include "latent_common.cuh"
 
 namespace kvd {

@@ -15,7 +15,7 @@
 // Warp 10: of the queries.
 // The running output is rescaled only when some row's maximum rose by more
 // than 8 (log2 units), as in the decode kernel: weights stay below 2^8.
-#include "kvd_internal.h"
+#include "../kvd_internal.h"
 #include "latent_common.cuh"
 #include "tcgen05_ptx.cuh"
 

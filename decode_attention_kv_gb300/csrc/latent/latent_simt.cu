@@ -6,7 +6,7 @@
 // dimension x 64 threads, each 4 rows x 2 keys, so six 16-byte shared loads feed
 // 16 packed multiply-adds (32 products).  Softmax: 16 threads a row keep the
 // running max and sum.  Values: a thread owns 4 dims x RPT rows.
-#include "kvd_internal.h"
+#include "../kvd_internal.h"
 #include "latent_common.cuh"
 #include "tcgen05_ptx.cuh"  // bar_sync
 

@@ -1,13 +1,40 @@
 // tcgen05_ptx.cuh -- fifth-generation tensor core primitives: tensor memory
 // allocation, matrix descriptors, bf16 MMA issue, commit, tensor memory loads
-// and stores.
+// and stores; and the copy, barrier and packed-arithmetic helpers that only the
+// latent-cache kernels use.
 #pragma once
 
 #include <stdint.h>
 
-#include "kvd_device.cuh"
+#include "../kvd_device.cuh"
 
 namespace kvd {
+
+// ------------------------------------------------------------ copies, arithmetic
+
+// The box of tma_g2s_3d into L2 only.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+// L2 policy for data that other CTAs read again.
+__device__ __forceinline__ uint64_t policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)),
+          "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
+}
 
 // ------------------------------------------------------------ tensor memory
 
