@@ -35,7 +35,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kSkip = 8.f;             // log2 units
 
 struct MmaShared {
-    uint64_t full[kMaxStages][2];  // the first (pairs + 1) / 2 pairs, the rest
+    uint64_t full[kMaxStages][kMaxPairs];
     uint64_t empty[kMaxStages][kMaxPairs];
     uint64_t s_full[2], s_free[2];
     uint64_t p_full, pv_done, q_full, q_free, drain[2];
@@ -140,19 +140,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     return true;
 }
 
-// Scores of the pairs [j0, j1) of a tile's chunks, added to D.
-__device__ __forceinline__ void score_pairs(uint32_t d, uint32_t q_low, uint32_t k_low,
-                                            uint32_t desc, int j0, int j1) {
-#pragma unroll 1
-    for (int j = j0; j < j1; ++j) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t off = ((2 * j + (i >> 2)) * kChunk + (i & 3) * 32) >> 4;
-            mma_ss(d, desc_of(q_low + off), desc_of(k_low + off), desc, true);
-        }
-    }
-}
-
 // A wait ran out: tells the others and waits for this warp's own MMAs.
 __device__ __forceinline__ void drain(uint64_t* bar, int* abort_flag) {
     *reinterpret_cast<volatile int*>(abort_flag) = 1;
@@ -181,13 +168,13 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
     const int row0 = g * a.rpg, nrows = min(a.rpg, a.rows - row0);
     const int N = (a.rpg + 15) / 16 * 16;  // rows of the MMA
     const uint32_t stage_bytes = L.chunks * kChunk;
-    const int front = (pairs + 1) / 2;  // pairs of the first half of a tile's copies
 
     if (tid == 0) {
         for (int s = 0; s < L.stages; ++s) {
-            for (int j = 0; j < pairs; ++j) mbar_init(&sh.empty[s][j], 1);
-            mbar_init(&sh.full[s][0], front);
-            mbar_init(&sh.full[s][1], pairs - front + (pairs == front));
+            for (int j = 0; j < pairs; ++j) {
+                mbar_init(&sh.full[s][j], 1);
+                mbar_init(&sh.empty[s][j], 1);
+            }
         }
         mbar_init(&sh.s_full[0], 2);
         mbar_init(&sh.s_full[1], 2);
@@ -317,7 +304,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                     if (lane == 0) sh.valid[it % kValid] = valid;
                     __syncwarp();
                 }
-                uint64_t* full = &sh.full[st][j >= front];
+                uint64_t* full = &sh.full[st][j];
                 if (it >= L.stages) {
                     // the stage is still in use: meanwhile the tile comes to L2
 #pragma unroll
@@ -372,7 +359,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
             if (lane == 0) sh.abort = 1;
             const unsigned long long since = global_timer_ns();
             for (int i = max(0, it - L.stages); i < it; ++i)
-                while (!mbar_try_wait(&sh.full[i % L.stages][j >= front],
+                while (!mbar_try_wait(&sh.full[i % L.stages][j],
                                       (i / L.stages) & 1) &&
                        global_timer_ns() - since < kWaitLimitNs) {
                 }
@@ -395,39 +382,42 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
             for (int k = 0; k < tiles && !bad; ++k, ++it) {
                 const uint32_t d = tm + 64 * (it & 1);
                 if (it > 1) bad = !warp_wait(&sh.s_free[it & 1], ((it >> 1) - 1) & 1, abort_flag);
-                // in two halves: the first runs while the second arrives
+                // pair by pair, as they arrive
                 const uint32_t q_low = uniform(desc_low(q, 16));
                 const uint32_t k_low = uniform(desc_low(kv + st * stage_bytes, 16));
-                if (bad || !warp_wait(&sh.full[st][0], par, abort_flag)) {
-                    bad = true;
-                    break;
-                }
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t rope = (2 * pairs * kChunk) >> 4;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma_ss(d, desc_of(q_low + rope + 2 * i), desc_of(k_low + rope + 2 * i), desc,
-                               i > 0);
-                    score_pairs(d, q_low, k_low, desc, 0, front);
-                    // the copying warps' writes (which this warp has waited for) are
-                    // ordered before the softmax's reads by an arrival of its own
-                    mbar_arrive(&sh.s_full[it & 1]);
-                }
-                __syncwarp();
-                if (front < pairs) {
-                    if (!warp_wait(&sh.full[st][1], par, abort_flag)) {
+                for (int j = 0; j < kMaxPairs; ++j) {
+                    if (j >= pairs || bad) break;
+                    if (!warp_wait(&sh.full[st][j], par, abort_flag)) {
                         bad = true;
                         break;
                     }
                     tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t off = ((2 * j + (i >> 2)) * kChunk + (i & 3) * 32) >> 4;
+                            mma_ss(d, desc_of(q_low + off), desc_of(k_low + off), desc,
+                                   i > 0 || j > 0);
+                        }
+                        if (j == 0) {
+                            const uint32_t rope = (2 * pairs * kChunk) >> 4;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma_ss(d, desc_of(q_low + rope + 2 * i),
+                                       desc_of(k_low + rope + 2 * i), desc, true);
+                            // the copying warps' writes (which this warp has waited
+                            // for) are ordered before the softmax's reads by an
+                            // arrival of its own
+                            mbar_arrive(&sh.s_full[it & 1]);
+                        }
+                        if (j + 1 == pairs) {
+                            mma_commit(&sh.s_full[it & 1]);
+                            if (k + 1 == tiles) mma_commit(&sh.q_free);
+                        }
+                    }
+                    __syncwarp();
                 }
-                if (elect_one()) {
-                    score_pairs(d, q_low, k_low, desc, front, pairs);
-                    mma_commit(&sh.s_full[it & 1]);
-                    if (k + 1 == tiles) mma_commit(&sh.q_free);
-                }
-                __syncwarp();
                 if (++st == L.stages) {
                     st = 0;
                     par ^= 1;
@@ -447,12 +437,12 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
             const Segment s = segment(a, walk, KT);
             const int tiles = uniform(s.end - s.first);
             for (int k = 0; k < tiles && !bad; ++k, ++it) {
+                const uint32_t v_low = uniform(desc_low(kv + st * stage_bytes, kChunk));
                 if (!warp_wait(&sh.p_full, it & 1, abort_flag)) {
                     bad = true;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t v_low = uniform(desc_low(kv + st * stage_bytes, kChunk));
                 if (elect_one()) {
 #pragma unroll
                     for (int j = 0; j < kMaxPairs; ++j) {
