@@ -2,7 +2,9 @@
 
 Each translation unit compiles in parallel into ``_build/`` and is linked
 into ``decode_attention_kv_gb300/libkvd.so`` (CUDA runtime linked
-statically).  Rebuilds only when a source or header is newer than the library.
+statically).  The host binding of the latent calls (csrc/binding, against the
+installed torch) compiles beside them into ``_latent_binding.so``.  Rebuilds
+only when a source or header is newer than the libraries.
 """
 from __future__ import annotations
 
@@ -17,6 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvd.so")
+BINDING_SRC = os.path.join(CSRC, "binding", "latent_binding.cpp")
+BINDING = os.path.join(PKG, "_latent_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]
@@ -36,14 +40,38 @@ def sources():
 
 def _inputs():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(CSRC, "*", "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "kvd.h"), __file__]
+        os.path.join(CSRC, "*", "*.cuh")) + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "kvd.h"), __file__]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def build_binding() -> str:
+    """Compile the host binding of the latent calls; returns its path."""
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in inc:
+        cmd += ["-isystem", d]
+    cmd += [BINDING_SRC, "-o", tmp, "-L" + os.path.join(base, "lib"), "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None,
@@ -66,8 +94,10 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None,
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

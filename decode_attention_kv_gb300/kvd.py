@@ -1052,71 +1052,26 @@ def combine_gathered(parts, R, D, out=None, lse=None, out_dtype=torch.float32):
 
 # ------------------------------------------------------------------ latent caches
 
-# These calls are made every few microseconds by a decode loop, so each argument
-# is looked at once (device, type, shape, layout) and passed on as an integer.
-
-def _refuse(fn, name, t, dev, dtype, shape):
-    if t.get_device() < 0 or not t.is_contiguous():
-        raise ValueError(f"{fn}: {name} must be a contiguous CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{fn}: {name} is on cuda:{t.get_device()}, not on cuda:{dev}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
-    raise ValueError(f"{fn}: {name} must be {list(shape)}, not {list(t.shape)}")
+# These calls are made every few microseconds by a decode loop: their argument
+# checks and the call itself are in the _latent_binding extension.
+_binding = None
 
 
-def _arg(fn, name, t, dev, dtype, shape):
-    """The data pointer of a contiguous tensor of this device, type and shape."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or \
-            not t.is_contiguous() or dev < 0:
-        _refuse(fn, name, t, dev, dtype, shape)
-    return t.data_ptr()
-
-
-def _opt(fn, name, t, dev, dtype, shape):
-    return None if t is None else _arg(fn, name, t, dev, dtype, shape)
-
-
-def _call_on(fn, dev, dev_status, *args):
-    """One call of the C entry point on the tensors' device and its current
-    stream; the status word and the stream are its last arguments."""
-    L = _lib or load()
-    if dev_status is not None:
-        dev_status = _arg(fn, "dev_status", dev_status, dev, torch.int32, dev_status.shape)
-    if torch.cuda.current_device() == dev:
-        st = getattr(L, fn)(*args, dev_status, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with torch.cuda.device(dev):
-            st = getattr(L, fn)(*args, dev_status, torch._C._cuda_getCurrentRawStream(dev))
-    if st != OK:
-        _check(fn, st)
-
-
-def _elem_code(fn, t):
-    if t.dtype is torch.bfloat16:
-        return BF16
-    if t.dtype is torch.float32:
-        return F32
-    raise TypeError(f"{fn}: unsupported dtype {t.dtype} (bf16 or fp32)")
-
-
-def _latent_cache(fn, latent_cache, rope_cache):
-    """Device, sizes and pointers of a latent cache."""
-    dev = latent_cache.get_device()
-    if latent_cache.dim() != 4 or rope_cache.dim() != 4:
-        raise ValueError(f"{fn}: caches must be [NB, BS, 1, R] and [NB, BS, 1, P]")
-    NB, BS, one, R = latent_cache.shape
-    P = rope_cache.shape[3]
-    dtype = latent_cache.dtype
-    lp = _arg(fn, "latent_cache", latent_cache, dev, dtype, (NB, BS, 1, R))
-    rp = _arg(fn, "rope_cache", rope_cache, dev, dtype, (NB, BS, 1, P))
-    return dev, NB, BS, R, P, dtype, lp, rp
-
-
-def _columns(fn, block_tables):
-    if block_tables.dim() != 2:
-        raise ValueError(f"{fn}: block_tables must be int32 [Q, cols]")
-    return block_tables.shape[1]
+def _bind():
+    """The extension, bound to the loaded library."""
+    global _binding
+    if _binding is None:
+        L = load()
+        try:
+            from . import _latent_binding as m
+        except ImportError as e:
+            raise RuntimeError("_latent_binding.so not found or not loadable: build it first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        m.bind(_check, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "kvd_append_latent", "kvd_attend_latent_workspace_bytes", "kvd_attend_latent",
+            "kvd_attend_expanded", "kvd_verify_drafts")))
+        _binding = m
+    return _binding
 
 
 def append_latent(latent_cache, rope_cache, block_tables, seq_offset, latent_new, rope_new,
@@ -1125,18 +1080,8 @@ def append_latent(latent_cache, rope_cache, block_tables, seq_offset, latent_new
     [N, P] becomes token pos[q] + i of sequence q in the paged latent cache
     (latent_cache [NB, BS, 1, R], rope_cache [NB, BS, 1, P]; block_tables
     [Q, cols], seq_offset [Q] or None, new_lens [Q + 1] cumsum, pos [Q] int32)."""
-    fn = "append_latent"
-    dev, NB, BS, R, P, dtype, lp, rp = _latent_cache(fn, latent_cache, rope_cache)
-    i32 = torch.int32
-    Q, N, cols = pos.numel(), latent_new.shape[0], _columns(fn, block_tables)
-    _call_on("kvd_append_latent", dev, dev_status, lp, rp,
-             _arg(fn, "latent_new", latent_new, dev, dtype, (N, R)),
-             _arg(fn, "rope_new", rope_new, dev, dtype, (N, P)),
-             _arg(fn, "block_tables", block_tables, dev, i32, (Q, cols)),
-             _opt(fn, "seq_offset", seq_offset, dev, i32, (Q,)),
-             _arg(fn, "new_lens", new_lens, dev, i32, (Q + 1,)),
-             _arg(fn, "pos", pos, dev, i32, (Q,)), Q, N, NB, BS, cols, R, P,
-             _elem_code(fn, latent_cache))
+    (_binding or _bind()).append_latent(latent_cache, rope_cache, block_tables, seq_offset,
+                                        latent_new, rope_new, new_lens, pos, dev_status)
 
 
 def attend_latent_workspace_bytes(Q, T, H, BS, cols, R, P, dtype=torch.bfloat16):
@@ -1155,31 +1100,9 @@ def attend_latent(q_latent, q_rope, latent_cache, rope_cache, block_tables, seq_
     that of the attention before the projections were absorbed.  Returns out
     [Q, T, H, R]; fills ``lse`` [Q, T, H] fp32 if given.
     """
-    fn = "attend_latent"
-    dev, NB, BS, R, P, dtype, lp, rp = _latent_cache(fn, latent_cache, rope_cache)
-    if q_latent.dim() != 4:
-        raise ValueError(f"{fn}: queries must be [Q, T, H, R] and [Q, T, H, P]")
-    i32 = torch.int32
-    Q, T, H, _ = q_latent.shape
-    cols, dt = _columns(fn, block_tables), _elem_code(fn, latent_cache)
-    args = (_arg(fn, "q_latent", q_latent, dev, dtype, (Q, T, H, R)),
-            _arg(fn, "q_rope", q_rope, dev, dtype, (Q, T, H, P)), lp, rp,
-            _arg(fn, "block_tables", block_tables, dev, i32, (Q, cols)),
-            _arg(fn, "seq_lens", seq_lens, dev, i32, (Q + 1,)),
-            _opt(fn, "seq_offset", seq_offset, dev, i32, (Q,)))
-    if out is None:
-        out = torch.empty_like(q_latent)
-        op = out.data_ptr()
-    else:
-        op = _arg(fn, "out", out, dev, dtype, (Q, T, H, R))
-    zp = _opt(fn, "lse", lse, dev, torch.float32, (Q, T, H))
-    if workspace is None:
-        need = attend_latent_workspace_bytes(Q, T, H, BS, cols, R, P, dtype)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_latent.device)
-    wp = _arg(fn, "workspace", workspace, dev, workspace.dtype, workspace.shape)
-    _call_on("kvd_attend_latent", dev, dev_status, *args, op, zp, Q, T, H, NB, BS, cols, R, P,
-             scale, dt, wp, workspace.nbytes)
-    return out
+    return (_binding or _bind()).attend_latent(q_latent, q_rope, latent_cache, rope_cache,
+                                               block_tables, seq_lens, scale, seq_offset, out, lse,
+                                               workspace, dev_status)
 
 
 def attend_expanded(q, kv, k_rope, q_lens, k_lens, scale=None, causal=True, out=None, lse=None,
@@ -1193,32 +1116,10 @@ def attend_expanded(q, kv, k_rope, q_lens, k_lens, scale=None, causal=True, out=
     sees them all).  ``scale`` defaults to 1/sqrt(Dn + P).  Returns out
     [Nq, H, Dv]; fills ``lse`` [Nq, H] fp32 if given.
     """
-    fn = "attend_expanded"
-    if q.dim() != 3 or kv.dim() != 3 or k_rope.dim() != 2:
-        raise ValueError(f"{fn}: q [Nq, H, Dn + P], kv [Nk, H, Dn + Dv], k_rope [Nk, P] required")
-    dev, dtype, i32 = q.get_device(), q.dtype, torch.int32
-    Nq, H, Dqk = q.shape
-    Nk, P = k_rope.shape
-    Dn = Dqk - P
-    Dv = kv.shape[2] - Dn
-    if Dn < 1 or Dv < 1:
-        raise ValueError(f"{fn}: rows of q {Dqk}, kv {kv.shape[2]} and k_rope {P} do not fit")
-    Q = q_lens.numel() - 1
-    args = (_arg(fn, "q", q, dev, dtype, (Nq, H, Dqk)),
-            _arg(fn, "kv", kv, dev, dtype, (Nk, H, Dn + Dv)),
-            _arg(fn, "k_rope", k_rope, dev, dtype, (Nk, P)),
-            _arg(fn, "q_lens", q_lens, dev, i32, (Q + 1,)),
-            _arg(fn, "k_lens", k_lens, dev, i32, (Q + 1,)))
-    if out is None:
-        out = torch.empty((Nq, H, Dv), dtype=dtype, device=q.device)
-        op = out.data_ptr()
-    else:
-        op = _arg(fn, "out", out, dev, dtype, (Nq, H, Dv))
-    zp = _opt(fn, "lse", lse, dev, torch.float32, (Nq, H))
-    _call_on("kvd_attend_expanded", dev, dev_status, *args, op, zp, Q, Nq, Nk, H, Dn, Dv, P,
-             1.0 / math.sqrt(Dqk) if scale is None else scale, 1 if causal else 0,
-             _elem_code(fn, q))
-    return out
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    return (_binding or _bind()).attend_expanded(q, kv, k_rope, q_lens, k_lens, scale, causal, out,
+                                                 lse, dev_status)
 
 
 # ------------------------------------------------------------------ drafted tokens
@@ -1234,26 +1135,5 @@ def verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, n
     Returns tokens [Q, T + 1] int32 (accepted drafts, the new token, then -1)
     and accepted [Q] int32.
     """
-    fn = "verify_drafts"
-    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
-        raise ValueError(f"{fn}: target_probs must be [Q, T + 1, V]")
-    dev, dtype, i32 = target_probs.get_device(), target_probs.dtype, torch.int32
-    Q, T1, V = target_probs.shape
-    T = T1 - 1
-    tp = _arg(fn, "target_probs", target_probs, dev, dtype, (Q, T1, V))
-    dp = xp = up = None
-    if T > 0:
-        dp = _arg(fn, "draft_probs", draft_probs, dev, dtype, (Q, T, V))
-        xp = _arg(fn, "draft_tokens", draft_tokens, dev, i32, (Q, T))
-        up = _arg(fn, "u_accept", u_accept, dev, torch.float32, (Q, T))
-    sp = _arg(fn, "u_sample", u_sample, dev, torch.float32, (Q,))
-    mp = _opt(fn, "num_drafts", num_drafts, dev, i32, (Q,))
-    if tokens is None:
-        tokens = torch.empty((Q, T1), dtype=i32, device=target_probs.device)
-    if accepted is None:
-        accepted = torch.empty((Q,), dtype=i32, device=target_probs.device)
-    _call_on("kvd_verify_drafts", dev, dev_status, tp, dp, xp, up, sp, mp,
-             _arg(fn, "tokens", tokens, dev, i32, (Q, T1)),
-             _arg(fn, "accepted", accepted, dev, i32, (Q,)), Q, T, V,
-             _elem_code(fn, target_probs))
-    return tokens, accepted
+    return (_binding or _bind()).verify_drafts(target_probs, draft_probs, draft_tokens, u_accept,
+                                               u_sample, num_drafts, tokens, accepted, dev_status)
