@@ -438,9 +438,16 @@ __global__ void __launch_bounds__(kGroups * kThreads) expanded_simt_kernel(const
     }
 }
 
-// One warp per (row, 128 dims): the workers' partial rows by log-sum-exp.
-template <typename Out>
-__global__ void __launch_bounds__(128) latent_combine_kernel(const LatentArgs a) {
+// A CTA a row: the workers' partial rows by log-sum-exp.  R / 128 warps share the
+// dims, and as many sets of them as fit share the workers (every other one, every
+// fourth ..): with one warp for 65 partial rows of 128 dims the merge of a short
+// fp32 call took longer than its attention.  Few rows take 8 warps each (kWide);
+// many take one set of warps, no shared memory and few registers, so that CTAs fit
+// beside the attention and wait there for its end (2048 rows of 512: 92 us with the
+// attention, 99 at 8 warps; 48 rows of 256: 23 us and 16).
+template <typename Out, bool kWide>
+__global__ void __launch_bounds__(kWide ? 256 : 128) latent_combine_kernel(const LatentArgs a) {
+    constexpr int kMergeWarps = kWide ? 8 : 4, kBatch = kWide ? 8 : 4;
     pdl_launch_dependents();
     pdl_wait();
     const int b = blockIdx.y;
@@ -450,16 +457,17 @@ __global__ void __launch_bounds__(128) latent_combine_kernel(const LatentArgs a)
     // a launch that gave up on a wait may have left no division behind
     if (w0 < 0 || w1 < w0 || w1 >= a.workers || (meta.z & ~1)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int cols = a.R / 128, sets = kWide ? kMergeWarps / cols : 1, set = warp / cols;
+    if (!kWide && set > 0) return;
     const int row = blockIdx.x, g = row / a.rpg, r = row % a.rpg;
-    const int d = 128 * warp + 4 * lane;
-    if (128 * warp >= a.R) return;
-    // a lane a worker: its log-sum-exp, then its weight; 32 workers at a time
-    // against a running maximum
+    const int d = 128 * (warp % cols) + 4 * lane;
     const float* base_o = a.part_o + d;
     float M = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int wb = w0; wb <= w1; wb += 32) {
-        const int w = wb + lane, n = min(32, w1 - wb + 1);
+    // a lane a worker: its log-sum-exp, then its weight; up to 32 workers of the set
+    // at a time against a running maximum
+    for (int wb = w0 + set; set < sets && wb <= w1; wb += 32 * sets) {
+        const int w = wb + lane * sets, n = min(32, (w1 - wb) / sets + 1);
         const int slot = (w * a.groups + g) * 2 + (w == w0 ? meta.z : 0);
         const float z = w <= w1 ? a.part_lse[(size_t)slot * a.rpg + r] : -INFINITY;
         float top = z;
@@ -474,11 +482,11 @@ __global__ void __launch_bounds__(128) latent_combine_kernel(const LatentArgs a)
         acc.y *= corr;
         acc.z *= corr;
         acc.w *= corr;
-        for (int i0 = 0; i0 < n; i0 += 8) {
-            float4 x[8];
-            float f[8];
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+            float4 x[kBatch];
+            float f[kBatch];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kBatch; ++i) {
                 const int from = min(i0 + i, n - 1);
                 const int sl = __shfl_sync(0xffffffffu, slot, from);
                 f[i] = __shfl_sync(0xffffffffu, e, from);
@@ -488,13 +496,37 @@ __global__ void __launch_bounds__(128) latent_combine_kernel(const LatentArgs a)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < kBatch; ++i) {
                 l += f[i];
                 acc.x = fmaf(f[i], x[i].x, acc.x);
                 acc.y = fmaf(f[i], x[i].y, acc.y);
                 acc.z = fmaf(f[i], x[i].z, acc.z);
                 acc.w = fmaf(f[i], x[i].w, acc.w);
             }
+        }
+    }
+    if constexpr (kWide) {
+        __shared__ float4 part[kMergeWarps][32];
+        __shared__ float part_m[kMergeWarps], part_l[kMergeWarps];
+        part[warp][lane] = acc;
+        if (lane == 0) {
+            part_m[warp] = M;
+            part_l[warp] = l;
+        }
+        __syncthreads();
+        if (set != 0) return;
+        for (int k = 1; k < sets; ++k) M = fmaxf(M, part_m[warp + k * cols]);
+        const float top = M == -INFINITY ? 0.f : M;
+        l = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < sets; ++k) {
+            const float c = exp2f(part_m[warp + k * cols] - top);
+            const float4 x = part[warp + k * cols][lane];
+            l = fmaf(c, part_l[warp + k * cols], l);
+            acc.x = fmaf(c, x.x, acc.x);
+            acc.y = fmaf(c, x.y, acc.y);
+            acc.z = fmaf(c, x.z, acc.z);
+            acc.w = fmaf(c, x.w, acc.w);
         }
     }
     const float base = M == -INFINITY ? 0.f : M;
@@ -540,11 +572,16 @@ cudaError_t launch_expanded_simt(const ExpandedArgs& a, cudaStream_t stream) {
     return a.Dv == 128 ? go_expanded<2>(a, stream) : go_expanded<1>(a, stream);
 }
 
-cudaError_t launch_latent_combine(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream) {
+template <typename Out>
+static cudaError_t go_combine(const LatentArgs& a, cudaStream_t stream) {
     const dim3 grid(a.rows, a.Q);
-    return dt == KVD_BF16
-               ? launch_pdl(latent_combine_kernel<__nv_bfloat16>, grid, dim3(128), 0, stream, a)
-               : launch_pdl(latent_combine_kernel<float>, grid, dim3(128), 0, stream, a);
+    if ((long long)a.rows * a.Q <= 2 * kLatentSMs)
+        return launch_pdl(latent_combine_kernel<Out, true>, grid, dim3(256), 0, stream, a);
+    return launch_pdl(latent_combine_kernel<Out, false>, grid, dim3(128), 0, stream, a);
+}
+
+cudaError_t launch_latent_combine(const LatentArgs& a, kvd_dtype dt, cudaStream_t stream) {
+    return dt == KVD_BF16 ? go_combine<__nv_bfloat16>(a, stream) : go_combine<float>(a, stream);
 }
 
 }  // namespace kvd
