@@ -14,6 +14,11 @@
 // values and the next of keys at 192 + 128 elements a token, and every block is
 // asked for at least one product of 1280 cycles before it is needed.
 //
+// What bounds it: the chain of a step (softmax 1160 cycles, hand-overs, products
+// 1500) is 3300 cycles against 2616 of MMA time for both tiles: 1580 TFLOP/s at one
+// sequence of 8192 x 16 heads, 1290 at four of 1024 to 4096 x 32 heads (329 us),
+// where starting and ending a unit counts.
+//
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, a row a thread.  Warps 8 and 9
 // issue the MMAs of tile 0 and 1: what one spends on waiting and setting up (450
 // cycles a step) the other's products fill.  Warp 10 issues the copies.

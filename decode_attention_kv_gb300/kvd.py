@@ -1,7 +1,8 @@
 """Thin ctypes binding of libkvd (argument marshalling only).
 
 Every function passes torch tensors' device pointers and sizes straight to the
-C entry point of the same name (``kvd_<name>``) on the current CUDA stream.
+C entry point of the same name (``kvd_<name>``) on the current CUDA stream (the
+latent calls through the _latent_binding extension).
 All computation happens in libkvd's kernels; there is no other code path: if
 the library is not built, or a call fails, an exception is raised.
 """
