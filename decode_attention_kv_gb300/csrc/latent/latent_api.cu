@@ -40,7 +40,7 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // How kvd_attend_latent divides a call (a function of the sizes only).
 struct LatentPlan {
-    int groups, rpg, workers, min_tiles, lead;
+    int groups, rpg, workers, min_shift, lead;
     size_t off_lse, off_o, bytes;
 };
 
@@ -63,7 +63,7 @@ kvd_status latent_plan(const char* fn, int Q, int T, int H, int BS, int cols, in
     pl->groups = (rows + most - 1) / most;
     pl->rpg = (rows + pl->groups - 1) / pl->groups;
     pl->workers = pl->groups < ctas ? ctas / pl->groups : 1;
-    pl->min_tiles = mma ? 2 : 1;
+    pl->min_shift = mma ? 1 : 0;
     pl->lead = mma ? 2 : 1;
     // a single worker shares no sequence: no partial rows
     const size_t slots = pl->workers > 1 ? (size_t)pl->workers * pl->groups * 2 : 0;
@@ -194,7 +194,9 @@ kvd_status kvd_attend_latent(const void* q_latent, const void* q_rope, const voi
     a.groups = pl.groups;
     a.rpg = pl.rpg;
     a.workers = pl.workers;
-    a.min_tiles = pl.min_tiles;
+    a.min_shift = pl.min_shift;
+    a.by_page = FastDiv(BS);
+    a.by_head = FastDiv(H);
     a.lead = pl.lead;
     a.meta = reinterpret_cast<int4*>(ws);
     a.part_lse = reinterpret_cast<float*>(ws + pl.off_lse);

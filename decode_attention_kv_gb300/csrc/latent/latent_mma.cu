@@ -72,7 +72,7 @@ struct MmaLayout {
 // The tiles of one worker, sequence by sequence.
 struct Walk {
     int t, t1, b, before;
-    int tot, W;
+    Runs runs;
     __device__ bool more() const { return t < t1; }
 };
 
@@ -83,10 +83,10 @@ struct Segment {
     int end;
 };
 
-__device__ __forceinline__ Segment segment(const LatentArgs& a, const Walk& k, int KT) {
+__device__ __forceinline__ Segment segment(const LatentArgs& a, const Walk& k, FastDiv by_tile) {
     Segment s;
     s.seq = latent_seq(a, k.b);
-    s.nt = max(1, (s.seq.n + KT - 1) / KT);
+    s.nt = max(1, by_tile.up(s.seq.n));
     // the run's part of the sequence's places: `lead` of them, then its tiles
     s.first = max(0, k.t - k.before - a.lead);
     s.end = min(s.nt, k.t1 - k.before - a.lead);
@@ -159,7 +159,7 @@ __device__ __forceinline__ void drain(uint64_t* bar, int* abort_flag) {
 }
 
 __global__ void __maxnreg__(144)
-latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ CUtensorMap lmap,
+latent_mma_kernel(const LatentArgs a, const int piece, const FastDiv by_tile, const __grid_constant__ CUtensorMap lmap,
                   const __grid_constant__ CUtensorMap rmap,
                   const __grid_constant__ CUtensorMap qlmap,
                   const __grid_constant__ CUtensorMap qrmap) {
@@ -210,24 +210,24 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
     volatile int* abort_flag = &sh.abort;
 
     Walk walk;
-    walk.W = 1;
+    uint32_t refused = 0;
     const Found f = block_find<kThreads>(
         a.Q, sh.scratch,
         [&](int tot) {
-            walk.W = used_workers(a, tot);
-            return w < walk.W ? run_start(w, tot, walk.W) : tot;
+            walk.runs = Runs(tot, used_workers(a, tot));
+            return w < walk.runs.W ? walk.runs.start(w) : tot;
         },
         [&](int b) {
             const SeqInfo s = latent_seq(a, b);
-            if (s.bad && g == 0 && w == 0) report(a.dev_status, s.bad);
-            return a.lead + max(1, (s.n + KT - 1) / KT);
+            refused |= s.bad;
+            return a.lead + max(1, by_tile.up(s.n));
         });
+    if (refused && g == 0 && w == 0) report(a.dev_status, refused);
     const bool some = f.item < a.Q;
     walk.b = f.item;
     walk.before = f.before;
-    walk.tot = f.total;
-    walk.t = some ? run_start(w, f.total, walk.W) : 0;
-    walk.t1 = some ? run_start(w + 1, f.total, walk.W) : 0;
+    walk.t = some ? walk.runs.start(w) : 0;
+    walk.t1 = some ? walk.runs.start(w + 1) : 0;
     if (walk.t1 <= walk.before + a.lead) walk.t = walk.t1;  // no tile of its first sequence
     const int t0 = walk.t;
     bool bad = false;
@@ -239,7 +239,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
         const uint64_t policy = policy_evict_first();
         int seg = 0;
         while (walk.more() && !bad) {
-            const Segment s = segment(a, walk, KT);
+            const Segment s = segment(a, walk, by_tile);
             const int row = uniform(walk.b * a.rows + row0);
             if (seg > 0 && !warp_wait(&sh.q_free, (seg - 1) & 1, abort_flag)) {
                 bad = true;
@@ -278,7 +278,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
         int it = 0, st = 0, par = 1;
         if (j >= pairs) walk.t = walk.t1;
         while (walk.more() && !bad) {
-            const Segment s = segment(a, walk, KT);
+            const Segment s = segment(a, walk, by_tile);
             for (int k = s.first; k < s.end; ++k, ++it) {
                 unsigned long long valid = 0;
                 int src[2];  // first row of this lane's pieces in the cache, or -1
@@ -288,12 +288,13 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                     const int key = k * KT + p * piece;
                     src[u] = -1;
                     if (p < pieces && key < s.seq.n) {
+                        const int page = a.by_page(key);
                         const int phys = __ldg(a.block_tables + (size_t)walk.b * a.cols +
-                                               s.seq.col0 + key / a.BS);
+                                               s.seq.col0 + page);
                         if (phys < 0 || phys >= a.NB) {
                             report(a.dev_status, KVD_DEV_BLOCK_RANGE);
                         } else {
-                            src[u] = phys * a.BS + key % a.BS;
+                            src[u] = phys * a.BS + key - page * a.BS;
                             const int n = min(piece, s.seq.n - key);
                             valid |= (n == 64 ? ~0ull : (1ull << n) - 1ull) << (p * piece);
                         }
@@ -382,7 +383,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
         const uint32_t tm = uniform(tmem) + 256;
         int it = 0, st = 0, par = 0, seg = 0;
         while (uniform((int)walk.more()) && !bad) {
-            const Segment s = segment(a, walk, KT);
+            const Segment s = segment(a, walk, by_tile);
             const int tiles = uniform(s.end - s.first);
             bad = !warp_wait(&sh.q_full, seg & 1, abort_flag);
             for (int k = 0; k < tiles && !bad; ++k, ++it) {
@@ -440,7 +441,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
         const uint32_t p_low = uniform(desc_low(smem_u32(sm + L.p), 16));
         int it = 0, st = 0;
         while (uniform((int)walk.more()) && !bad) {
-            const Segment s = segment(a, walk, KT);
+            const Segment s = segment(a, walk, by_tile);
             const int tiles = uniform(s.end - s.first);
             for (int k = 0; k < tiles && !bad; ++k, ++it) {
                 const uint32_t v_low = uniform(desc_low(kv + st * stage_bytes, kChunk));
@@ -488,12 +489,13 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
         int it = 0, st = 0;
         uint32_t par = 0;
         while (walk.more()) {
-            const Segment s = segment(a, walk, KT);
+            const Segment s = segment(a, walk, by_tile);
             int last[2];  // newest key that the row sees
             float m[2], l[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                last[h] = rows[h] < nrows ? s.seq.n - a.T + (row0 + rows[h]) / a.H : 0x3fffffff;
+                last[h] = rows[h] < nrows ? s.seq.n - a.T + a.by_head(row0 + rows[h])
+                                         : 0x3fffffff;
                 m[h] = -INFINITY;
                 l[h] = 0.f;
             }
@@ -653,7 +655,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const __grid_constant__ C
                 }
             }
             if (g == 0 && tid == 0 && s.first == 0)
-                a.meta[b] = make_int4(w, worker_of(before + a.lead + s.nt - 1, walk.tot, walk.W),
+                a.meta[b] = make_int4(w, walk.runs.worker_of(before + a.lead + s.nt - 1),
                                       head ? 0 : 1, 0);
             if (it > 0 && !mbar_wait(&sh.pv_done, (it - 1) & 1, abort_flag)) bad = true;
             __syncwarp();
@@ -708,7 +710,7 @@ cudaError_t launch_latent_mma(const LatentArgs& a, cudaStream_t stream) {
                              L.total);
     if (e != cudaSuccess) return e;
     return launch_pdl(latent_mma_kernel, dim3(a.groups, a.workers), dim3(kThreads), L.total, stream,
-                      a, piece, lmap, rmap, qlmap, qrmap);
+                      a, piece, FastDiv(kTile / piece * piece), lmap, rmap, qlmap, qrmap);
 }
 
 }  // namespace kvd

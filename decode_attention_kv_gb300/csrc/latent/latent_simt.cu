@@ -214,20 +214,22 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
     const SimtLayout L(D, a.R, false, 1);
     const float* latent = static_cast<const float*>(a.latent);
     const float* rope = static_cast<const float*>(a.rope);
-    int W = 1;
+    Runs runs;
+    uint32_t refused = 0;
     const Found f = block_find<kThreads>(
         a.Q, scratch,
         [&](int tot) {
-            W = used_workers(a, tot);
-            return w < W ? run_start(w, tot, W) : tot;
+            runs = Runs(tot, used_workers(a, tot));
+            return w < runs.W ? runs.start(w) : tot;
         },
         [&](int b) {
             const SeqInfo s = latent_seq(a, b);
-            if (s.bad && g == 0 && w == 0) report(a.dev_status, s.bad);
+            refused |= s.bad;
             return a.lead + max(1, (s.n + kKeys - 1) / kKeys);
         });
+    if (refused && g == 0 && w == 0) report(a.dev_status, refused);
     if (f.item >= a.Q) return;
-    const int t0 = run_start(w, f.total, W), t1 = run_start(w + 1, f.total, W);
+    const int t0 = runs.start(w), t1 = runs.start(w + 1);
     const int row0 = g * a.rpg, nrows = min(a.rpg, a.rows - row0);
     int b = f.item, before = f.before;
     RowState<RPT> st;
@@ -243,9 +245,10 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
             const int key = k * kKeys + lane;
             long long row = -1;
             if (key < seq.n) {
-                const int phys = a.block_tables[(size_t)b * a.cols + seq.col0 + key / a.BS];
+                const int page = a.by_page(key);
+                const int phys = a.block_tables[(size_t)b * a.cols + seq.col0 + page];
                 if (phys >= 0 && phys < a.NB)
-                    row = (long long)phys * a.BS + key % a.BS;
+                    row = (long long)phys * a.BS + key - page * a.BS;
                 else if (warp == 0)
                     report(a.dev_status, KVD_DEV_BLOCK_RANGE);
             }
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
         st.clear();
         const int srow = tid >> 4;
         // newest key the softmax row sees
-        const int last = srow < nrows ? seq.n - a.T + (row0 + srow) / a.H : -1;
+        const int last = srow < nrows ? seq.n - a.T + a.by_head(row0 + srow) : -1;
         for (int k = first; k < end; ++k) {
             const int buf = (k - first) & 1;
             uint32_t next = 0;
@@ -311,7 +314,7 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
                 a.lse_out[(size_t)b * a.rows + row0 + tid] = z * kLn2;
         }
         if (g == 0 && tid == 0 && first == 0)
-            a.meta[b] = make_int4(w, worker_of(before + a.lead + nt - 1, f.total, W),
+            a.meta[b] = make_int4(w, runs.worker_of(before + a.lead + nt - 1),
                                   t == t0 ? 0 : 1, 0);
         __syncthreads();
         before += a.lead + nt;
