@@ -116,7 +116,7 @@ __device__ __forceinline__ void store_rows(uint32_t tm, int pairs, int N, int nr
             f[i + 3] = x.w;
         }
         const int n = min(16, nrows - c);
-#pragma unroll 1
+#pragma unroll 2
         for (int j = 0; j < pairs; ++j) {
             float o[16];
             tmem_ld16(tm + j * N + c, o);

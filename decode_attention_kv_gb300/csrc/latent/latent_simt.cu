@@ -473,6 +473,18 @@ __global__ void __launch_bounds__(kWide ? 256 : 128) latent_combine_kernel(const
         const int w = wb + lane * sets, n = min(32, (w1 - wb) / sets + 1);
         const int slot = (w * a.groups + g) * 2 + (w == w0 ? meta.z : 0);
         const float z = w <= w1 ? a.part_lse[(size_t)slot * a.rpg + r] : -INFINITY;
+        // the first rows are on their way before the weights are known
+        float4 x[kBatch];
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int sl = __shfl_sync(0xffffffffu, slot, min(i0 + i, n - 1));
+                x[i] = i0 + i < n ? *reinterpret_cast<const float4*>(
+                                        base_o + ((size_t)sl * a.rpg + r) * a.R)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        };
+        load(0);
         float top = z;
 #pragma unroll
         for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
@@ -486,17 +498,12 @@ __global__ void __launch_bounds__(kWide ? 256 : 128) latent_combine_kernel(const
         acc.z *= corr;
         acc.w *= corr;
         for (int i0 = 0; i0 < n; i0 += kBatch) {
-            float4 x[kBatch];
             float f[kBatch];
+            if (i0 > 0) load(i0);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const int from = min(i0 + i, n - 1);
-                const int sl = __shfl_sync(0xffffffffu, slot, from);
-                f[i] = __shfl_sync(0xffffffffu, e, from);
+                f[i] = __shfl_sync(0xffffffffu, e, min(i0 + i, n - 1));
                 if (i0 + i >= n) f[i] = 0.f;
-                x[i] = i0 + i < n ? *reinterpret_cast<const float4*>(
-                                        base_o + ((size_t)sl * a.rpg + r) * a.R)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
