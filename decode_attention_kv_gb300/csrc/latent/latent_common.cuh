@@ -102,38 +102,35 @@ template <int THREADS, typename Total, typename Count>
 __device__ __forceinline__ Found block_find(int Q, int* scratch, Total target_of, Count count) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (Q <= kFindWarp) {
-        // item 32 i + lane is the lane's i-th: 32 items cost one memory latency, as many
-        // as there are cost one too (the counts do not depend on one another)
         constexpr int kPer = kFindWarp / 32;
-        int c[kPer], inc[kPer], total = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) c[i] = 32 * i + lane < Q ? count(32 * i + lane) : 0;
+        int c[kPer], sum = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            inc[i] = c[i];
-            if (32 * i >= Q) continue;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, inc[i], d);
-                if (lane >= d) inc[i] += o;
-            }
-            inc[i] += total;
-            total = __shfl_sync(0xffffffffu, inc[i], 31);
+            const int b = lane * kPer + i;
+            c[i] = b < Q ? count(b) : 0;
+            sum += c[i];
         }
+        int inc = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        const int total = __shfl_sync(0xffffffffu, inc, 31);
         const int target = target_of(total);
-        int item = Q, at = 0;
+        int at = inc - sum, item = lane * kPer;
+        const bool mine = target >= at && target < inc;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (32 * i >= Q) continue;
-            const uint32_t who = __ballot_sync(
-                0xffffffffu, target >= inc[i] - c[i] && target < inc[i]);
-            if (who) {
-                const int src = __ffs(who) - 1;
-                item = 32 * i + src;
-                at = __shfl_sync(0xffffffffu, inc[i] - c[i], src);
+        for (int i = 0; i + 1 < kPer; ++i)
+            if (mine && target >= at + c[i] && item == lane * kPer + i) {
+                at += c[i];
+                ++item;
             }
-        }
-        return Found{item, at, total};
+        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        const int src = who ? __ffs(who) - 1 : 0;
+        item = __shfl_sync(0xffffffffu, item, src);
+        at = __shfl_sync(0xffffffffu, at, src);
+        return Found{who ? item : Q, at, total};
     }
     const int per = (Q + THREADS - 1) / THREADS;
     const int lo = min(tid * per, Q), hi = min(lo + per, Q);
@@ -172,6 +169,47 @@ __device__ __forceinline__ Found block_find(int Q, int* scratch, Total target_of
     Found f{scratch[32], scratch[33], total};
     __syncthreads();
     return f;
+}
+
+// The same with item 32 i + lane as the lane's i-th, so that all counts cost one
+// memory latency.  (kvd_attend_latent: 64 sequences 66.0 -> 63.8 us with the cheaper
+// divisions, 8 sequences 15.8 -> 13.9.  kvd_attend_expanded, whose softmax has no
+// registers left, lost 1 % to it.)
+template <int THREADS, typename Total, typename Count>
+__device__ __forceinline__ Found block_find_strided(int Q, int* scratch, Total target_of,
+                                                    Count count) {
+    if (Q > kFindWarp) return block_find<THREADS>(Q, scratch, target_of, count);
+    const int lane = threadIdx.x & 31;
+    constexpr int kPer = kFindWarp / 32;
+    int c[kPer], inc[kPer], total = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) c[i] = 32 * i + lane < Q ? count(32 * i + lane) : 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        inc[i] = c[i];
+        if (32 * i >= Q) continue;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc[i], d);
+            if (lane >= d) inc[i] += o;
+        }
+        inc[i] += total;
+        total = __shfl_sync(0xffffffffu, inc[i], 31);
+    }
+    const int target = target_of(total);
+    int item = Q, at = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (32 * i >= Q) continue;
+        const uint32_t who =
+            __ballot_sync(0xffffffffu, target >= inc[i] - c[i] && target < inc[i]);
+        if (who) {
+            const int src = __ffs(who) - 1;
+            item = 32 * i + src;
+            at = __shfl_sync(0xffffffffu, inc[i] - c[i], src);
+        }
+    }
+    return Found{item, at, total};
 }
 
 // `tot` tiles over W workers: worker w's run is [start(w), start(w + 1)), and the

@@ -211,7 +211,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const FastDiv by_tile, co
 
     Walk walk;
     uint32_t refused = 0;
-    const Found f = block_find<kThreads>(
+    const Found f = block_find_strided<kThreads>(
         a.Q, sh.scratch,
         [&](int tot) {
             walk.runs = Runs(tot, used_workers(a, tot));

@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) latent_simt_kernel(const LatentArgs 
     const float* rope = static_cast<const float*>(a.rope);
     Runs runs;
     uint32_t refused = 0;
-    const Found f = block_find<kThreads>(
+    const Found f = block_find_strided<kThreads>(
         a.Q, scratch,
         [&](int tot) {
             runs = Runs(tot, used_workers(a, tot));
