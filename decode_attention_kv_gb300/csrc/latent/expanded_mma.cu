@@ -1,7 +1,7 @@
 // expanded_mma.cu -- kvd_attend_expanded in bf16 on the tensor cores.
 //
-// A CTA holds two tiles of 128 queries of one head and walks the keys 128 at a
-// time: S_s = Q_s . K^T and O_s += P_s . V for s = 0, 1 in turn, so that one
+// A CTA holds two tiles of 128 queries of one head (one where there are few) and
+// walks the keys 128 at a time: S_s = Q_s . K^T and O_s += P_s . V for s = 0, 1 in turn, so that one
 // tile's softmax runs while the tensor cores work on the other.  Tensor memory
 // is full: two score tiles and two outputs of 128 columns; the weights replace
 // the scores they came from and are the A operand from there.  MMAs of one
@@ -120,18 +120,19 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
         [&](int b) {
             const PackedSeq s = packed_seq(a, b);
             if (s.bad && h == 0 && unit == 0) report(a.dev_status, s.bad);
-            return (s.nq + 2 * kRows - 1) / (2 * kRows);
+            return (s.nq + (1 << a.span_log) - 1) >> a.span_log;
         });
     const bool some = f.item < a.Q;
     const PackedSeq seq = some ? packed_seq(a, f.item) : PackedSeq{0, 0, 0, 0, 0u};
     // the last unit of a sequence first: under the causal mask it sees most keys
-    const int units = (seq.nq + 2 * kRows - 1) / (2 * kRows);
-    const int row0 = some ? (units - 1 - (unit - f.before)) * 2 * kRows : 0;
+    const int units = (seq.nq + (1 << a.span_log) - 1) >> a.span_log;
+    const int row0 = some ? (units - 1 - (unit - f.before)) << a.span_log : 0;
+    const int behind = min(seq.nq, row0 + (1 << a.span_log));  // the first row that is not its
     const int shift = seq.nk - seq.nq;  // query i sees the keys 0 .. i + shift
     int steps[2];                       // key tiles that each query tile sees
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        const int first = row0 + s * kRows, rows = min(kRows, seq.nq - first);
+        const int first = row0 + s * kRows, rows = min(kRows, behind - first);
         const int keys = rows <= 0 ? 0
                          : a.causal ? max(0, min(seq.nk, first + rows + shift))
                                     : seq.nk;
@@ -305,7 +306,7 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         const int s = warp >> 2;
         const int row = row0 + s * kRows + 32 * (warp & 3) + lane;  // in the sequence
-        const bool live = some && row < seq.nq;
+        const bool live = some && row < behind;
         const uint32_t quarter = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + s * kRows + quarter, to = tmem + 256 + s * kRows + quarter;
         const int last = !live ? -1 : a.causal ? min(seq.nk - 1, row + shift) : seq.nk - 1;
@@ -445,14 +446,19 @@ cudaError_t go_expanded(const ExpandedArgs& a, const CUtensorMap& qmap, const CU
     const cudaError_t e = cudaFuncSetAttribute(
         expanded_mma_kernel<KC, VC>, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
     if (e != cudaSuccess) return e;
-    const int units = (a.Nq + 2 * kRows - 1) / (2 * kRows) + a.Q;
+    const int units = ((a.Nq - 1) >> a.span_log) + 1 + a.Q;
     return launch_pdl(expanded_mma_kernel<KC, VC>, dim3(a.H, units), dim3(kThreads), L.total,
                       stream, a, qmap, kvmap, ropemap);
 }
 
 }  // namespace
 
-cudaError_t launch_expanded_mma(const ExpandedArgs& a, cudaStream_t stream) {
+cudaError_t launch_expanded_mma(const ExpandedArgs& args, cudaStream_t stream) {
+    ExpandedArgs a = args;
+    // One query tile a CTA where all CTAs still run at once: the tensor cores wait, but
+    // a step is over sooner (300 x 8 heads 10.8 -> 9.4 us, 1024 x 16 20.1 -> 17.0, 2048 x
+    // 8 32.3 -> 28.5; but 4 x 512 x 16, 256 CTAs of work, 16.4 -> 21.5).
+    a.span_log = (long long)a.H * ((a.Nq - 1) / kRows + 1 + a.Q) <= kLatentSMs ? 7 : 8;
     CUtensorMap qmap, kvmap, ropemap;
     const long long qw = (long long)a.H * (a.Dn + a.P), kw = (long long)a.H * (a.Dn + a.Dv);
     cudaError_t e = encode_rows(&qmap, a.q, qw, qw, a.Nq, kRows, 1);

@@ -262,6 +262,7 @@ struct ExpandedArgs {
     int Q, Nq, Nk, H, Dn, Dv, P;
     float qscale;        // scale * log2(e)
     int causal;
+    int span_log;        // log2 of the queries that a CTA of the bf16 kernel takes
 };
 
 // Queries and keys of one sequence.  A bad pair of q_lens leaves no queries, a

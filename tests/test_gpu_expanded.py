@@ -98,6 +98,14 @@ def test_shapes(kvd, shape, dtype, causal):
     Packed(*shape, dtype, seed=len(shape[0]), causal=causal).same(kvd, "shape")
 
 
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("shape", SHAPES[2:], ids=lambda s: f"{len(s[0])}x{max(s[0])}D{s[3]}.{s[4]}")
+def test_more_heads_than_fit_at_once(kvd, shape, causal):
+    """The same lengths with 152 heads: more CTAs than SMs."""
+    nq, nk, _, Dn, Dv = shape
+    Packed(nq, nk, 152, Dn, Dv, BF, seed=7, causal=causal).same(kvd, "heads")
+
+
 def test_many_sequences(kvd):
     nq = [(i * 29) % 70 for i in range(300)]
     Packed(nq, [n + (n * 13) % 40 for n in nq], 2, 128, 128, BF, seed=3).same(kvd, "many")
