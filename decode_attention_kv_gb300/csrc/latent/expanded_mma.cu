@@ -406,6 +406,8 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
         __syncwarp();
         if (!bad) {
             tc_fence_after();
+            // a scale of NaN (the weights above do without it): every query that sees a key
+            if (a.qscale != a.qscale && l != 0.f) l = a.qscale;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t at = (size_t)(seq.q0 + (live ? row : 0)) * a.H + h;
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * a.Dv;

@@ -645,6 +645,8 @@ latent_mma_kernel(const LatentArgs a, const int piece, const FastDiv by_tile, co
             for (int h = 0; h < 2; ++h) {
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
                 l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+                // a scale of NaN (the weights above do without it): every query that sees a key
+                if (a.qscale != a.qscale && l[h] != 0.f) l[h] = a.qscale;
                 if (quad == 0) sh.factor[rows[h]] = l[h] == 0.f ? 0.f : 1.f / l[h];
                 if (quad == 0 && rows[h] < nrows) {
                     const float z = l[h] > 0.f ? m[h] + log2f(l[h]) : (l[h] == 0.f ? -INFINITY : NAN);
