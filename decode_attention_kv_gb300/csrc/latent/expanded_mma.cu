@@ -313,7 +313,7 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
         // newest key that every row of the warp sees
         const int all_see = __reduce_min_sync(0xffffffffu, live ? last : 0x3fffffff);
         const bool flip = a.qscale < 0.f;
-        const float qs = fmaxf(fabsf(a.qscale), 1e-30f);
+        const float qs = fmaxf(fabsf(a.qscale), kTinyScale);
         const int ns = steps[s];
         float m = -INFINITY, l = 0.f;
         for (int i = 0; i < ns; ++i) {

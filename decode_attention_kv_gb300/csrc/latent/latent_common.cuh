@@ -60,6 +60,10 @@ struct LatentArgs {
     float* part_o;          // [workers * groups * 2, rpg, R], normalised
 };
 
+// What the bf16 kernels take for a scale of zero, so that a masked score of -inf stays
+// one: the smallest number, which makes any finite product less than 2^-21.
+constexpr float kTinyScale = 1.4e-45f;
+
 // A sequence's keys: count (0 if the sequence is refused), first table column.
 struct SeqInfo {
     int n;

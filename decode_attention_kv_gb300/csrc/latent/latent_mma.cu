@@ -478,10 +478,9 @@ latent_mma_kernel(const LatentArgs a, const int piece, const FastDiv by_tile, co
         const int rows[2] = {16 * warp + (lane >> 2), 16 * warp + (lane >> 2) + 8};
         const bool busy = 16 * warp < nrows;  // the warp has rows at all
         // The largest score is the largest product where the scale is positive;
-        // products change sign where it is negative, and a scale of zero is a very
-        // small one.
+        // products change sign where it is negative.
         const bool flip = a.qscale < 0.f;
-        const float qs = fmaxf(fabsf(a.qscale), 1e-30f);
+        const float qs = fmaxf(fabsf(a.qscale), kTinyScale);
         // where this lane's row of a group of four 8 x 8 weight tiles goes
         const int prow = 16 * warp + 8 * ((lane >> 3) & 1) + (lane & 7);
         const uint32_t p_row = smem_u32(sm + L.p) + prow * 128;

@@ -59,3 +59,37 @@ def test_nan_in_the_expanded_form(kvd, dtype, causal):
                       else torch.full((a,), b > 0, device="cuda") for a, b in zip(nq, nk)])
     sees = sees[:, None].expand(-1, 2)
     same(out[:sum(nq)], lse[:sum(nq)], sees, ~sees)
+
+
+# Products of 1e34 and more: a scale of zero still gives the mean of what a
+# query sees, and one of 1e-34 ordinary scores.  The kernels' bounds hold as
+# they are, with one addition at scale zero: the bf16 kernels take the
+# smallest number of fp32 (2^-149) in its place, so that a score of up to 2^127
+# is off by 2^-22, a weight by a factor of 1 + 2^-21, an lse by 2^-22.
+HUGE = 2.0 ** 56
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-34, -1e-34], ids=["0", "-0", "+", "-"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_small_scales(kvd, dtype, scale):
+    c = ref.LatentCase([300, 64, 1], 2, 4, 128, 16, dtype, seed=5)
+    c.ql, c.qr = c.ql * HUGE, c.qr * HUGE
+    c.latent, c.rope = c.latent * HUGE, c.rope * HUGE
+    c.rows = [(x * HUGE, y * HUGE) for x, y in c.rows]
+    c.scale = scale
+    out, lse = attend(kvd, c, scale)
+    o, z, A, d = c.reference()
+    ref.check("latent", out, lse, o, z, A, d + (2.0 ** -22 if scale == 0 else 0), 300, dtype)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-34, -1e-34], ids=["0", "+", "-"])
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_small_scales_in_the_expanded_form(kvd, dtype, scale):
+    c = Packed([130, 7], [200, 9], 2, 128, 64, dtype, seed=6)
+    c.q, c.kv, c.kr = c.q * HUGE, c.kv * HUGE, c.kr * HUGE
+    c.scale = scale
+    out, lse, bits = c.call(kvd)
+    assert bits == 0
+    o, z, A, d = c.reference()
+    ref.check("expanded", out[:137], lse[:137], o, z, A, d + (2.0 ** -22 if scale == 0 else 0), 200,
+              dtype)
