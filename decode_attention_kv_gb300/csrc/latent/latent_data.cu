@@ -103,16 +103,23 @@ append_latent_kernel(unsigned char* __restrict__ latent, unsigned char* __restri
 //
 // A sum must decide the same token as one in 64 bits, and 64-bit additions run
 // at a small fraction of the fp32 rate here: the difference p - q is taken
-// exactly as two fp32 words and the sums of a share are held in two (Knuth's
-// two-sum), about 2^-48 relative; only the shares' sums are added in 64 bits, by
-// one warp (a 64-bit addition holds an SM's unit for 16 cycles a warp: with all
-// warps at it these few sums took longer than the row).
+// exactly as two fp32 words and the sums of 64 elements a lane are held in two
+// (Knuth's two-sum; the second word's own rounding leaves about 2^-47 relative, at
+// worst 2^-36); these are added in 64 bits, those of a CTA's warps by one warp (a
+// 64-bit addition holds an SM's unit for 16 cycles a warp: with all warps at it
+// every few elements they took longer than the row).
 // 64 rows of 128000 fp32: 18.4 us, 3.6 TB/s, 21 instructions an element; one row of
 // 32000: 6.9 us, a chain of five memory latencies and two barriers.
 constexpr int kVerifyMaxCtas = 8;
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyBatch = 16;  // elements a lane loads at once
+// Elements of a warp between two additions in 64 bits: 64 a lane, so that the second
+// word, which is a plain fp32 sum, stays right to about 2^-47 of the sum; over the 1024
+// that a lane takes of a row of 2^22 it was right to 2^-37 (ones with thirds of 2^-25
+// behind them).  The steps that join the lanes cost 1 to 3 % of a long row (96 of 200000:
+// fp32 36.1 -> 36.6 us, bf16 34.9 -> 35.9) and nothing of a short one.
+constexpr int kVerifyFold = 4 * 32 * kVerifyBatch;
 
 __device__ __forceinline__ float as_prob(float x) { return x; }
 __device__ __forceinline__ float as_prob(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -157,9 +164,9 @@ __device__ __forceinline__ float2 weight(float p, float q) {
     return make_float2(some ? d : 0.f, some && d < INFINITY ? e : 0.f);
 }
 
-// This warp's sum over [lo, hi), in lane 0 at least.
+// This warp's sum over [lo, hi) in every lane, as two words.
 template <typename Elem, int VEC, bool kRest>
-__device__ __forceinline__ double share_sum(const Elem* p, const Elem* q, int lo, int hi) {
+__device__ __forceinline__ float2 fold_sum(const Elem* p, const Elem* q, int lo, int hi) {
     float s = 0.f, c = 0.f;
     for (int i0 = lo; i0 < hi; i0 += 32 * kVerifyBatch) {
         float a[kVerifyBatch], b[kVerifyBatch] = {};
@@ -181,7 +188,19 @@ __device__ __forceinline__ double share_sum(const Elem* p, const Elem* q, int lo
         s = two_sum(s, so, e);
         c += s < INFINITY ? e + co : 0.f;
     }
-    return (double)s + (s < INFINITY ? (double)c : 0.0);
+    return make_float2(s, c);
+}
+
+// This warp's sum over [lo, hi) in every lane.
+template <typename Elem, int VEC, bool kRest>
+__device__ __forceinline__ double share_sum(const Elem* p, const Elem* q, int lo, int hi) {
+    auto fold = [&](int i0) {
+        const float2 x = fold_sum<Elem, VEC, kRest>(p, q, i0, min(i0 + kVerifyFold, hi));
+        return (double)x.x + (x.x < INFINITY ? (double)x.y : 0.0);
+    };
+    double sum = fold(lo);
+    for (int i0 = lo + kVerifyFold; i0 < hi; i0 += kVerifyFold) sum += fold(i0);
+    return sum;
 }
 
 // Running sums of the first n (at most 32) values, lane by lane.
