@@ -117,8 +117,7 @@ constexpr int kVerifyBatch = 16;  // elements a lane loads at once
 // Elements of a warp between two additions in 64 bits: 64 a lane, so that the second
 // word, which is a plain fp32 sum, stays right to about 2^-47 of the sum; over the 1024
 // that a lane takes of a row of 2^22 it was right to 2^-37 (ones with thirds of 2^-25
-// behind them).  The steps that join the lanes cost 1 to 3 % of a long row (96 of 200000:
-// fp32 36.1 -> 36.6 us, bf16 34.9 -> 35.9) and nothing of a short one.
+// behind them).  Rows of 200000 take as long either way (96 of them 36.0 us).
 constexpr int kVerifyFold = 4 * 32 * kVerifyBatch;
 
 __device__ __forceinline__ float as_prob(float x) { return x; }
@@ -161,10 +160,11 @@ __device__ __forceinline__ float2 weight(float p, float q) {
     float e;
     const float d = two_sum(p, -q, e);
     const bool some = d > 0.f;  // d = 0 only where p = q
-    return make_float2(some ? d : 0.f, some && d < INFINITY ? e : 0.f);
+    return make_float2(some ? d : 0.f, some ? e : 0.f);
 }
 
-// This warp's sum over [lo, hi) in every lane, as two words.
+// This warp's sum over [lo, hi) in every lane, as two words; infinite where fp32 does
+// not reach.
 template <typename Elem, int VEC, bool kRest>
 __device__ __forceinline__ float2 fold_sum(const Elem* p, const Elem* q, int lo, int hi) {
     float s = 0.f, c = 0.f;
@@ -180,23 +180,41 @@ __device__ __forceinline__ float2 fold_sum(const Elem* p, const Elem* q, int lo,
             c += e + w.y;
         }
     }
-    if (!(s < INFINITY)) c = 0.f;
 #pragma unroll
     for (int k = 16; k; k >>= 1) {
         float e;
         const float so = __shfl_xor_sync(0xffffffffu, s, k), co = __shfl_xor_sync(0xffffffffu, c, k);
         s = two_sum(s, so, e);
-        c += s < INFINITY ? e + co : 0.f;
+        c += e + co;
     }
     return make_float2(s, c);
+}
+
+// The weight max(p - q, 0) in 64 bits; NaN counts as zero.
+template <bool kRest>
+__device__ __forceinline__ double weight64(float p, float q) {
+    const double d = kRest ? (double)p - (double)q : (double)p;
+    return d > 0.0 ? d : 0.0;
+}
+
+// This warp's sum over [lo, hi) in every lane, in 64 bits: for weights near the largest
+// fp32 number, or above it, or infinite.  (Not inlined: registers.)
+template <typename Elem, bool kRest>
+__device__ __noinline__ double wide_sum(const Elem* p, const Elem* q, int lo, int hi) {
+    double s = 0.0;
+    for (int i = lo + (int)(threadIdx.x & 31); i < hi; i += 32)
+        s += weight64<kRest>(as_prob(p[i]), kRest ? as_prob(q[i]) : 0.f);
+    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    return s;
 }
 
 // This warp's sum over [lo, hi) in every lane.
 template <typename Elem, int VEC, bool kRest>
 __device__ __forceinline__ double share_sum(const Elem* p, const Elem* q, int lo, int hi) {
     auto fold = [&](int i0) {
-        const float2 x = fold_sum<Elem, VEC, kRest>(p, q, i0, min(i0 + kVerifyFold, hi));
-        return (double)x.x + (x.x < INFINITY ? (double)x.y : 0.0);
+        const int end = min(i0 + kVerifyFold, hi);
+        const float2 x = fold_sum<Elem, VEC, kRest>(p, q, i0, end);
+        return x.x < INFINITY ? (double)x.x + (double)x.y : wide_sum<Elem, kRest>(p, q, i0, end);
     };
     double sum = fold(lo);
     for (int i0 = lo + kVerifyFold; i0 < hi; i0 += kVerifyFold) sum += fold(i0);
@@ -233,9 +251,8 @@ __device__ __forceinline__ int find(const Elem* p, const Elem* q, int lo, int hi
     const int lane = threadIdx.x & 31;
     for (int i0 = lo; i0 < hi; i0 += 32) {
         const int i = i0 + lane;
-        const float2 x = weight<kRest>(i < hi ? as_prob(p[i]) : 0.f,
-                                       kRest && i < hi ? as_prob(q[i]) : 0.f);
-        const double w = (double)x.x + (double)x.y;
+        const double w = weight64<kRest>(i < hi ? as_prob(p[i]) : 0.f,
+                                         kRest && i < hi ? as_prob(q[i]) : 0.f);
         double cum = w;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {

@@ -1,12 +1,16 @@
 """Sums of kvd_verify_drafts that fp32 alone cannot hold: long rows whose small
-weights do not add up exactly."""
+weights do not add up exactly, and weights whose sum is above the largest fp32."""
 from fractions import Fraction
 
 import numpy as np
 import pytest
 import torch
 
+from test_gpu_verify import expect
+
 pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
 
 
 @pytest.fixture(scope="module")
@@ -55,3 +59,39 @@ def test_long_rows(kvd, V):
     p = torch.from_numpy(np.stack(rows)).cuda()[:, None]
     tokens, _ = kvd.verify_drafts(p, None, None, None, torch.full((2,), 0.5, device="cuda"))
     assert tokens[:, 0].tolist() == [half, half - 1]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V", [40, 1000, 50257, 200000])
+def test_sums_above_the_largest_fp32(kvd, V, dtype):
+    """Weights need not be normalised: finite ones count whatever their sum.  A
+    difference p - q may be above the largest fp32 by itself."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    p = torch.rand((6, 2, V), generator=g, device="cuda") * 3e38
+    p = torch.where(torch.rand((6, 2, V), generator=g, device="cuda") < 0.3, 0.0, p).to(dtype)
+    q = (torch.rand((6, 1, V), generator=g, device="cuda") * 3e38).to(dtype)
+    q[3:] = -q[3:]
+    x = torch.zeros((6, 1), dtype=torch.int32, device="cuda")
+    p[:, 0, 0], q[:, 0, 0] = 0.0, 1.0             # the draft is always rejected
+    u = torch.full((6, 1), 0.5, device="cuda")
+    us = torch.tensor([0.0, 0.37, 0.999], device="cuda").repeat(2)
+    status = kvd.status_tensor()
+    tokens, acc = kvd.verify_drafts(p, q, x, u, us, dev_status=status)
+    want, n = expect(p, q, x, u, us, [1] * 6)
+    assert int(status.item()) == 0
+    assert torch.equal(tokens.cpu(), want) and torch.equal(acc.cpu(), n)
+    rows = p[:, :1].contiguous()
+    tokens, _ = kvd.verify_drafts(rows, None, None, None, us, dev_status=status)
+    want, _ = expect(rows, None, torch.zeros((6, 0), dtype=torch.int32), None, us, [0] * 6)
+    assert int(status.item()) == 0 and torch.equal(tokens.cpu(), want)
+
+
+def test_infinite_weights_are_refused(kvd):
+    """One infinite weight among finite ones whose sum is above the largest fp32."""
+    p = torch.full((3, 1, 5000), 1e36, device="cuda")
+    p[1, 0, 4321] = float("inf")
+    status = kvd.status_tensor()
+    tokens, _ = kvd.verify_drafts(p, None, None, None, torch.full((3,), 0.5, device="cuda"),
+                                  dev_status=status)
+    assert int(status.item()) == kvd.DEV_PROBS
+    assert tokens[:, 0].tolist() == [2500, -1, 2500]
