@@ -115,15 +115,10 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
     const uint32_t tmem = sh.tmem;
     volatile int* abort_flag = &sh.abort;
 
-    const Found f = block_find<kThreads>(
-        a.Q, sh.scratch, [&](int) { return unit; },
-        [&](int b) {
-            const PackedSeq s = packed_seq(a, b);
-            if (s.bad && h == 0 && unit == 0) report(a.dev_status, s.bad);
-            return (s.nq + (1 << a.span_log) - 1) >> a.span_log;
-        });
+    const Found f =
+        packed_find<kThreads>(a, sh.scratch, unit, a.span_log, h == 0 && unit == 0);
     const bool some = f.item < a.Q;
-    const PackedSeq seq = some ? packed_seq(a, f.item) : PackedSeq{0, 0, 0, 0, 0u};
+    const PackedSeq seq = some ? packed_seq(a, f.item) : PackedSeq{0, 0, 0, 0, 0u, false};
     // the last unit of a sequence first: under the causal mask it sees most keys
     const int units = (seq.nq + (1 << a.span_log) - 1) >> a.span_log;
     const int row0 = some ? (units - 1 - (unit - f.before)) << a.span_log : 0;

@@ -270,16 +270,18 @@ struct ExpandedArgs {
 };
 
 // Queries and keys of one sequence.  A bad pair of q_lens leaves no queries, a
-// bad pair of k_lens no keys.
+// bad pair of k_lens no keys.  falls: q_lens decreases here.
 struct PackedSeq {
     int q0, nq, k0, nk;
     uint32_t bad;
+    bool falls;
 };
 
 __device__ __forceinline__ PackedSeq packed_seq(const ExpandedArgs& a, int b) {
-    PackedSeq s{0, 0, 0, 0, 0u};
+    PackedSeq s{0, 0, 0, 0, 0u, false};
     const int q0 = a.q_lens[b], q1 = a.q_lens[b + 1], k0 = a.k_lens[b], k1 = a.k_lens[b + 1];
-    if ((b == 0 && q0 != 0) || q0 < 0 || q1 < q0 || q1 > a.Nq) {
+    s.falls = q1 < q0;
+    if ((b == 0 && q0 != 0) || q0 < 0 || s.falls || q1 > a.Nq) {
         s.bad = KVD_DEV_SEQLENS;
     } else {
         s.q0 = q0;
@@ -292,6 +294,42 @@ __device__ __forceinline__ PackedSeq packed_seq(const ExpandedArgs& a, int b) {
         s.nk = k1 - k0;
     }
     return s;
+}
+
+// The sequence of a CTA's unit in the line of all units of 2^span_log queries, by the
+// whole block.  The grid has units for Nq queries, one sequence each; a q_lens that
+// decreases would give queries to several.  So sequences have queries only up to the
+// first pair that does; the second search is for such a q_lens alone.  `tell`: the CTA
+// that reports bad pairs.
+template <int THREADS>
+__device__ __forceinline__ Found packed_find(const ExpandedArgs& a, int* scratch, int unit,
+                                             int span_log, bool tell) {
+    int end = a.Q;
+    Found f;
+    for (bool again = true; again;) {
+        int fall = a.Q;
+        f = block_find<THREADS>(
+            a.Q, scratch, [&](int) { return unit; },
+            [&](int b) {
+                const PackedSeq s = packed_seq(a, b);
+                if (s.bad && tell) report(a.dev_status, s.bad);
+                if (s.falls) fall = min(fall, b);
+                return b < end ? (s.nq + (1 << span_log) - 1) >> span_log : 0;
+            });
+        if (a.Q <= kFindWarp) {
+            fall = __reduce_min_sync(0xffffffffu, fall);
+        } else if (__syncthreads_or(fall < end)) {
+            if (threadIdx.x == 0) scratch[0] = a.Q;
+            __syncthreads();
+            if (fall < a.Q) atomicMin(scratch, fall);
+            __syncthreads();
+            fall = scratch[0];
+            __syncthreads();
+        }
+        again = fall < end;
+        end = min(end, fall);
+    }
+    return f;
 }
 
 cudaError_t launch_expanded_mma(const ExpandedArgs& a, cudaStream_t stream);

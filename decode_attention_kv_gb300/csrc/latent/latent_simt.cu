@@ -15,7 +15,7 @@ namespace {
 
 constexpr int kThreads = 256;  // of a group: one tile of keys at a time
 constexpr int kGroups = 2;     // groups of a CTA of the expanded form, every other tile each
-constexpr int kRows = 16;   // query rows per tile
+constexpr int kRowsLog = 4, kRows = 1 << kRowsLog;  // query rows per tile
 constexpr int kKeys = 32;   // keys per tile
 
 // Row strides of the scores [slice, row, key] and of the weights [key, row]: no
@@ -334,13 +334,7 @@ __global__ void __launch_bounds__(kGroups * kThreads) expanded_simt_kernel(const
     const int D = a.Dn + a.P;
     const SimtLayout L(D, a.Dv, true, kGroups);
     float* sm = smem + group * L.group;
-    const Found f = block_find<kGroups * kThreads>(
-        a.Q, scratch, [&](int) { return unit; },
-        [&](int b) {
-            const PackedSeq s = packed_seq(a, b);
-            if (s.bad && h == 0 && unit == 0) report(a.dev_status, s.bad);
-            return (s.nq + kRows - 1) / kRows;
-        });
+    const Found f = packed_find<kGroups * kThreads>(a, scratch, unit, kRowsLog, h == 0 && unit == 0);
     if (f.item >= a.Q) return;
     const PackedSeq seq = packed_seq(a, f.item);
     // the last rows of a sequence first: under the causal mask they see most keys

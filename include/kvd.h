@@ -717,8 +717,9 @@ kvd_status kvd_attend_latent(const void* q_latent, const void* q_rope, const voi
  * The keys and values of a sequence must be finite (one that is not may reach
  * queries of its sequence that come before it).
  * Device-detected errors: a bad pair of k_lens (not starting at 0, decreasing,
- * past Nk) makes the sequence's keys empty, a bad pair of q_lens skips its
- * queries; both set KVD_DEV_SEQLENS.
+ * past Nk) makes the sequence's keys empty; a bad pair of q_lens skips its
+ * queries, a decreasing one those of all sequences behind it too (rows that are
+ * not computed are left as they were); both set KVD_DEV_SEQLENS.
  * Supported: Dn, Dv in {64, 128}, P = 64.  Needs no workspace.
  */
 kvd_status kvd_attend_expanded(const void* q, const void* kv, const void* k_rope,
