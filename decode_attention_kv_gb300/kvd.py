@@ -9,11 +9,14 @@ the library is not built, or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
 
 import torch
+
+from . import _build
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libkvd.so")
@@ -1059,15 +1062,17 @@ _binding = None
 
 
 def _bind():
-    """The extension, bound to the loaded library."""
+    """The extension that was compiled for this torch, bound to the loaded library."""
     global _binding
     if _binding is None:
         L = load()
+        path = _build.binding_path()
         try:
-            from . import _latent_binding as m
+            spec = importlib.util.spec_from_file_location(__package__ + "._latent_binding", path)
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
         except ImportError as e:
-            raise RuntimeError("_latent_binding.so not found or not loadable: build it first "
-                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+            raise RuntimeError(f"{path} not found or not loadable: {_build.binding_error()}") from e
         m.bind(_check, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "kvd_append_latent", "kvd_attend_latent_workspace_bytes", "kvd_attend_latent",
             "kvd_attend_expanded", "kvd_verify_drafts")))
