@@ -3,7 +3,8 @@
 Each translation unit compiles in parallel into ``_build/`` and is linked
 into ``decode_attention_kv_gb300/libkvd.so`` (CUDA runtime linked
 statically).  The host binding of the latent calls (csrc/binding) compiles
-beside them against the installed torch.  libkvd.so needs nvcc only: where the binding does not compile, the
+beside them against the installed torch, into a file named for that torch and
+this Python.  libkvd.so needs nvcc only: where the binding does not compile, the
 build goes on without it and the latent calls raise what stopped it.  Rebuilds
 only when a source or header is newer than the libraries.
 """
@@ -53,7 +54,11 @@ def _newer(lib, inputs) -> bool:
 
 
 def binding_path() -> str:
-    return os.path.join(PKG, "_latent_binding.so")
+    """The binding's file for the installed torch and this Python: tensors are read
+    through torch's own types, whose layout goes with its version and C++ ABI."""
+    import torch
+    return os.path.join(PKG, "_latent_binding.torch-{}.abi{}.{}.so".format(
+        torch.__version__, int(torch._C._GLIBCXX_USE_CXX11_ABI), sysconfig.get_config_var("SOABI")))
 
 
 def up_to_date() -> bool:
@@ -62,7 +67,7 @@ def up_to_date() -> bool:
 
 
 def binding_up_to_date() -> bool:
-    """So is the binding."""
+    """So is the binding, and it was compiled against the installed torch."""
     return _newer(binding_path(), [BINDING_SRC, os.path.join(ROOT, "include", "kvd.h"), __file__])
 
 

@@ -3,6 +3,7 @@ latent call says where the binding is missing (no GPU needed)."""
 import os
 
 import pytest
+import torch
 
 from decode_attention_kv_gb300 import _build, kvd
 
@@ -45,6 +46,21 @@ def test_the_library_links_without_the_binding(elsewhere, capsys):
 def test_no_binding_at_all(elsewhere):
     with pytest.raises(RuntimeError, match="build it first"):
         kvd.attend_latent(*[None] * 7)
+
+
+@pytest.mark.parametrize("change", ["version", "abi", "python"])
+def test_the_binding_goes_with_its_torch_and_python(monkeypatch, change):
+    """Another torch, C++ ABI or Python: the library stays, the binding is built anew."""
+    assert _build.up_to_date() and _build.binding_up_to_date()
+    here = _build.binding_path()
+    if change == "version":
+        monkeypatch.setattr(torch, "__version__", "1.0.0")
+    elif change == "abi":
+        monkeypatch.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)
+    else:
+        monkeypatch.setattr(_build.sysconfig, "get_config_var", lambda name: "cpython-30-none")
+    assert _build.binding_path() != here
+    assert _build.up_to_date() and not _build.binding_up_to_date()
 
 
 def test_sources_of_the_library_and_of_the_binding(monkeypatch):
