@@ -651,11 +651,15 @@ kvd_status kvd_combine_gathered(const float* parts, void* out, float* lse_out, i
  *   new_lens [Q + 1] int32, cumsum starting at 0;  pos [Q] int32 (device)
  *   block_tables [Q, cols] int32;  seq_offset [Q] int32 or NULL (zeros)
  * A byte copy.  Rows at and behind new_lens[Q] go nowhere.  Device-detected
- * errors skip the row (nothing written): new_lens not starting at 0,
- * decreasing or past N (KVD_DEV_SEQLENS), pos[q] < 0 (KVD_DEV_POS_RANGE),
- * seq_offset negative or not a multiple of BS (KVD_DEV_SEQ_OFFSET), table
- * column past cols (KVD_DEV_TABLE_COLS), block id outside [0, NB)
- * (KVD_DEV_BLOCK_RANGE).  Any R and P with rows of whole 16-byte vectors.
+ * errors skip the row (nothing written): new_lens not starting at 0 (every row),
+ * a pair past N (its rows; both KVD_DEV_SEQLENS), pos[q] < 0
+ * (KVD_DEV_POS_RANGE), seq_offset negative or not a multiple of BS
+ * (KVD_DEV_SEQ_OFFSET), table column past cols (KVD_DEV_TABLE_COLS), block id
+ * outside [0, NB) (KVD_DEV_BLOCK_RANGE).  Where new_lens decreases
+ * (KVD_DEV_SEQLENS) the rows below the smallest value that it falls to go where
+ * they belong, the others to one sequence whose pair holds them, or nowhere.
+ * With Q = 0 or N = 0 nothing is launched, and new_lens is not looked at.
+ * Any R and P with rows of whole 16-byte vectors.
  */
 kvd_status kvd_append_latent(void* latent_cache, void* rope_cache, const void* latent_new,
                              const void* rope_new, const int32_t* block_tables,
@@ -719,7 +723,8 @@ kvd_status kvd_attend_latent(const void* q_latent, const void* q_rope, const voi
  * Device-detected errors: a bad pair of k_lens (not starting at 0, decreasing,
  * past Nk) makes the sequence's keys empty; a bad pair of q_lens skips its
  * queries, a decreasing one those of all sequences behind it too (rows that are
- * not computed are left as they were); both set KVD_DEV_SEQLENS.
+ * not computed are left as they were); both set KVD_DEV_SEQLENS.  With Q = 0 or
+ * Nq = 0 nothing is launched, and the lengths are not looked at.
  * Supported: Dn, Dv in {64, 128}, P = 64.  Needs no workspace.
  */
 kvd_status kvd_attend_expanded(const void* q, const void* kv, const void* k_rope,

@@ -64,3 +64,62 @@ def test_expanded_decreasing_among_many(kvd, dtype):
     lens[201] -= 150
     lens[250] -= 1000
     expanded(kvd, lens, c, range(200))
+
+
+# ------------------------------------------------------------------ append
+
+def append(kvd, lens, N):
+    """Appends rows 1, 2, .. N of all ones times their number at token 0 of every
+    sequence, each with pages of its own; returns what every token then holds."""
+    Q, BS, cols, R, P = len(lens) - 1, 4, 8, 64, 8
+    table = torch.arange(Q * cols, dtype=torch.int32).view(Q, cols).cuda()
+    latent, rope = torch.zeros(Q * cols, BS, 1, R).cuda(), torch.zeros(Q * cols, BS, 1, P).cuda()
+    rows = torch.arange(1.0, N + 1, device="cuda")[:, None]
+    status = kvd.status_tensor()
+    kvd.append_latent(latent, rope, table, None, rows.repeat(1, R), rows.repeat(1, P),
+                      torch.tensor(lens, dtype=torch.int32).cuda(),
+                      torch.zeros(Q, dtype=torch.int32).cuda(), status)
+    assert bool((latent == latent[..., :1]).all()) and bool((rope == latent[..., :1]).all())
+    return latent[..., 0].view(Q, cols * BS).long().tolist(), int(status.item())
+
+
+def held(lens, rows):
+    """Tokens of every sequence where `rows` (counted from 0) are written."""
+    want = [[0] * 32 for _ in lens[1:]]
+    for r, b in rows:
+        want[b][r - lens[b]] = r + 1
+    return want
+
+
+def test_append_past_the_rows(kvd):
+    """A sequence whose rows end behind the N given has none of them written."""
+    got, bits = append(kvd, [0, 3, 5, 9], 8)
+    assert bits == kvd.DEV_SEQLENS
+    assert got == held([0, 3, 5, 9], [(0, 0), (1, 0), (2, 0), (3, 1), (4, 1)])
+
+
+def test_append_not_from_zero(kvd):
+    """Nothing is written at all."""
+    got, bits = append(kvd, [1, 3, 5], 8)
+    assert bits == kvd.DEV_SEQLENS and got == held([1, 3, 5], [])
+
+
+@pytest.mark.parametrize("lens", [[0, 2, 1, 6, 9], [0, 5, 3, 3, 8], [0, 4, 8, 6, 7, 8],
+                                  [0, 7, -1, 8], [0, 20, 5, 6]], ids=str)
+def test_append_decreasing(kvd, lens):
+    """Rows below the smallest length that new_lens falls to are written where
+    they belong, the others once at most, to a sequence whose pair holds them."""
+    N = 8
+    got, bits = append(kvd, lens, N)
+    assert bits == kvd.DEV_SEQLENS
+    low = min(b for a, b in zip(lens, lens[1:]) if b < a)
+    holds = [[b for b in range(len(lens) - 1) if 0 <= lens[b] <= r < lens[b + 1] <= N]
+             for r in range(N)]
+    for r in range(N):
+        at = [(b, t) for b, row in enumerate(got) for t, v in enumerate(row) if v == r + 1]
+        assert len(at) <= 1
+        assert all(b in holds[r] and t == r - lens[b] for b, t in at)
+        if r < low:
+            assert len(at) == len(holds[r])
+    written = sum(v != 0 for row in got for v in row)
+    assert written == sum(any(v == r + 1 for row in got for v in row) for r in range(N))
