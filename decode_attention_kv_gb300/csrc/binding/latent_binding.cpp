@@ -121,10 +121,9 @@ struct Call {
         raise(PyExc_TypeError,
               std::string(fn) + ": unsupported dtype " + type_name(t) + " (bf16 or fp32)");
     }
-    float number(int i, const char* name) const {
+    float number(int i) const {
         const double x = PyFloat_AsDouble(args[i]);
         if (x == -1.0 && PyErr_Occurred()) throw Raised{};
-        (void)name;
         return (float)x;
     }
     int small(int64_t x, const char* name) const {
@@ -215,7 +214,7 @@ PyObject* attend_latent(Call& c) {
     const void* rp = c.data(1, "q_rope", k.dtype, {Q, T, H, k.P});
     auto* tables = static_cast<const int32_t*>(c.data(4, "block_tables", kI32, {Q, cols}));
     auto* lens = static_cast<const int32_t*>(c.data(5, "seq_lens", kI32, {Q + 1}));
-    const float scale = c.number(6, "scale");
+    const float scale = c.number(6);
     auto* offset = static_cast<const int32_t*>(c.maybe(7, "seq_offset", kI32, {Q}));
     float* lse = static_cast<float*>(c.maybe(9, "lse", kF32, {Q, T, H}));
     int32_t* status = c.status(11);
@@ -259,7 +258,7 @@ PyObject* attend_expanded(Call& c) {
     const void* rp = c.data(kr, "k_rope", dtype, {Nk, P});
     auto* ql = static_cast<const int32_t*>(c.data(3, "q_lens", kI32, {Q + 1}));
     auto* kl = static_cast<const int32_t*>(c.data(4, "k_lens", kI32, {Q + 1}));
-    const float scale = c.number(5, "scale");
+    const float scale = c.number(5);
     const int causal = PyObject_IsTrue(c.args[6]);
     if (causal < 0) throw Raised{};
     float* lse = static_cast<float*>(c.maybe(8, "lse", kF32, {Nq, H}));

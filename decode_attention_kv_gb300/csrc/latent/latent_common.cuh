@@ -232,10 +232,11 @@ struct Runs {
         return (int)((((long long)tile + 1) * W - 1) / tot);
     }
 };
-// A worker per 2^min_shift tiles, or per tile where that makes kFewWorkers at most:
-// while there are few the merge of their partial rows is cheaper than a second tile
-// (bf16: 1000 tokens 11.8 us instead of 12.7 with 18 workers instead of 9, but 4000
-// tokens 16.1 instead of 15.0 with 66 instead of 33).
+// A worker per 2^min_shift places of the line (the `lead` ones, which hold no tile,
+// counted), but kFewWorkers at least, or one a place where there are fewer: while there
+// are few the merge of their partial rows is cheaper than a second tile (bf16: 1000
+// tokens 11.8 us instead of 12.7 with 18 workers instead of 9, but 4000 tokens 16.1
+// instead of 15.0 with 66 instead of 33).
 constexpr int kFewWorkers = 32;
 __device__ __forceinline__ int used_workers(const LatentArgs& a, int tot) {
     return max(1, min(a.workers,

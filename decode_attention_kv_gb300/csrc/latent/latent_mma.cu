@@ -486,7 +486,6 @@ latent_mma_kernel(const LatentArgs a, const int piece, const FastDiv by_tile, co
         const uint32_t p_row = smem_u32(sm + L.p) + prow * 128;
         const uint32_t p_group = lane >> 4, p_swizzle = lane & 7;
         int it = 0, st = 0;
-        uint32_t par = 0;
         while (walk.more()) {
             const Segment s = segment(a, walk, by_tile);
             int last[2];  // newest key that the row sees
@@ -584,6 +583,8 @@ latent_mma_kernel(const LatentArgs a, const int piece, const FastDiv by_tile, co
                     }
                     tmem_wait_st();
                 }
+                // Weights are rounded to bf16, what the matrix unit takes with bf16 values (each
+                // is off by 2^-8 of itself at most); their sum keeps fp32.
                 uint32_t p[2][8];
                 if (busy) {
 #pragma unroll
@@ -624,10 +625,7 @@ latent_mma_kernel(const LatentArgs a, const int piece, const FastDiv by_tile, co
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p_full);
-                if (++st == L.stages) {
-                    st = 0;
-                    par ^= 1;
-                }
+                if (++st == L.stages) st = 0;
             }
             __syncwarp();
             if (bar_any(1, kSoftmax, bad)) {

@@ -126,19 +126,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const float (&r)[16]) {
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* u) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-        "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
-        "%27, %28, %29, %30, %31};" ::"r"(u[0]),
-        "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
-        "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]),
-        "r"(u[16]), "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]),
-        "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]),
-        "r"(u[30]), "r"(u[31]), "r"(addr)
-        : "memory");
-}
-
 // ------------------------------------------------------------ matrix operands
 // Shared-memory operands are tiles of 128-byte rows under the 128-byte swizzle,
 // groups of eight rows 1024 bytes apart.  With rows along M or N (64 elements
@@ -153,9 +140,6 @@ __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) {
 }
 __device__ __forceinline__ uint64_t desc_of(uint32_t low) {
     return ((uint64_t)kDescHigh << 32) | low;
-}
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
-    return desc_of(desc_low(addr, lead));
 }
 
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N.
