@@ -363,7 +363,8 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                // over scores that have been read: 16 columns hold 32 weights
+                // over scores that have been read: 16 columns hold 32 weights, rounded to
+                // bf16 as the matrix unit takes them (2^-8 of each); their sum keeps fp32
                 float p[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {

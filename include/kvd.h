@@ -685,6 +685,8 @@ kvd_status kvd_append_latent(void* latent_cache, void* rope_cache, const void* l
  * Slots of a page behind the sequence's end may hold anything (inf, NaN).
  * The rows of the sequence itself must be finite: one that is not reaches all
  * T queries of its sequence, also those that come before it.
+ * bf16: scores, maxima and sums are held in fp32, the weights w_k are rounded to
+ * bf16 before they multiply latent_k, and out is rounded once.
  * Device-detected errors as for kvd_attend_paged: KVD_DEV_SEQLENS, SEQ_OFFSET
  * and TABLE_COLS make the sequence empty, KVD_DEV_BLOCK_RANGE drops the
  * block's tokens.
@@ -720,6 +722,8 @@ kvd_status kvd_attend_latent(const void* q_latent, const void* q_rope, const voi
  * of kv and k_rope of other sequences and behind k_lens[Q] may hold anything.
  * The keys and values of a sequence must be finite (one that is not may reach
  * queries of its sequence that come before it).
+ * bf16: as for kvd_attend_latent, the weights are rounded to bf16 before they
+ * multiply the values.
  * Device-detected errors: a bad pair of k_lens (not starting at 0, decreasing,
  * past Nk) makes the sequence's keys empty; a bad pair of q_lens skips its
  * queries, a decreasing one those of all sequences behind it too (rows that are
@@ -751,11 +755,13 @@ kvd_status kvd_attend_expanded(const void* q, const void* kv, const void* k_rope
  *   draft_tokens [Q, T] int32;  u_accept [Q, T], u_sample [Q] float in [0, 1)
  *   num_drafts [Q] int32 or NULL;  tokens [Q, T + 1] int32;  accepted [Q] int32
  * T = 0 (a token without drafts) takes NULL for the drafts' arrays.  The
- * acceptance and the subtraction are exact to 64 bits and the sums are held in
- * two fp32 words or 64 bits.  Device-detected errors: a drafted token outside
- * [0, V) is rejected (KVD_DEV_TOKEN_RANGE); no weight above zero, or a sum
- * that is not finite, gives the token -1 (KVD_DEV_PROBS); num_drafts[q]
- * outside [0, T] gives tokens -1 and accepted 0 (KVD_DEV_POS_RANGE).
+ * acceptance and the differences are exact to 64 bits; a sum is right to about
+ * 2^-47 of itself (two fp32 words for 64 elements of a lane, 64 bits above), so
+ * that only a draw closer than that to a border can differ from one in 64 bits.
+ * Finite weights count whatever their sum.  Device-detected errors: a drafted
+ * token outside [0, V) is rejected (KVD_DEV_TOKEN_RANGE); no weight above zero,
+ * or an infinite one, gives the token -1 (KVD_DEV_PROBS); num_drafts[q] outside
+ * [0, T] gives tokens -1 and accepted 0 (KVD_DEV_POS_RANGE).
  */
 kvd_status kvd_verify_drafts(const void* target_probs, const void* draft_probs,
                              const int32_t* draft_tokens, const float* u_accept,
