@@ -682,9 +682,10 @@ kvd_status kvd_append_latent(void* latent_cache, void* rope_cache, const void* l
  *   q_latent [Q, T, H, R], q_rope [Q, T, H, P] of `dtype`
  *   block_tables, seq_lens, seq_offset as for kvd_attend_paged
  *   out [Q, T, H, R] of `dtype`;  lse_out [Q, T, H] float or NULL
- * Slots of a page behind the sequence's end may hold anything (inf, NaN).
- * The rows of the sequence itself must be finite: one that is not reaches all
- * T queries of its sequence, also those that come before it.
+ * Slots of a page behind the sequence's end, and the rotary values of tokens
+ * behind a query's own, may hold anything (inf, NaN) without reaching it.  The
+ * latent rows of a sequence, which are values too, must be finite: one that is
+ * not reaches all T queries of its sequence, also those that come before it.
  * bf16: scores, maxima and sums are held in fp32, the weights w_k are rounded to
  * bf16 before they multiply latent_k, and out is rounded once.
  * Device-detected errors as for kvd_attend_paged: KVD_DEV_SEQLENS, SEQ_OFFSET
@@ -719,9 +720,9 @@ kvd_status kvd_attend_latent(const void* q_latent, const void* q_rope, const voi
  *   q_lens, k_lens [Q + 1] int32, cumsum starting at 0 (device)
  *   out [Nq, H, Dv] of `dtype`;  lse_out [Nq, H] float or NULL
  * Rows of out and lse_out at and behind q_lens[Q] are left as they were; rows
- * of kv and k_rope of other sequences and behind k_lens[Q] may hold anything.
- * The keys and values of a sequence must be finite (one that is not may reach
- * queries of its sequence that come before it).
+ * of kv and k_rope of other sequences and behind k_lens[Q], and keys that a query
+ * does not see, may hold anything (inf, NaN) without reaching it.  The values of
+ * a sequence must be finite: one that is not may reach queries before it.
  * bf16: as for kvd_attend_latent, the weights are rounded to bf16 before they
  * multiply the values.
  * Device-detected errors: a bad pair of k_lens (not starting at 0, decreasing,
