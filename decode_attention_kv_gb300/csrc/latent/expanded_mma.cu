@@ -117,8 +117,8 @@ expanded_mma_kernel(const ExpandedArgs a, const __grid_constant__ CUtensorMap qm
 
     const Found f =
         packed_find<kThreads>(a, sh.scratch, unit, a.span_log, h == 0 && unit == 0);
-    const bool some = f.item < a.Q;
-    const PackedSeq seq = some ? packed_seq(a, f.item) : PackedSeq{0, 0, 0, 0, 0u, false};
+    const PackedSeq seq = f.item < a.Q ? packed_seq(a, f.item) : PackedSeq{0, 0, 0, 0, 0u, false};
+    const bool some = seq.nq > 0;
     // the last unit of a sequence first: under the causal mask it sees most keys
     const int units = (seq.nq + (1 << a.span_log) - 1) >> a.span_log;
     const int row0 = some ? (units - 1 - (unit - f.before)) << a.span_log : 0;

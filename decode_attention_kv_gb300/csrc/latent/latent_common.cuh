@@ -93,7 +93,8 @@ __device__ __forceinline__ SeqInfo latent_seq(const LatentArgs& a, int b) {
 // count(b) places each (b < Q): item, the places before it, and the total.
 // Every thread gets the result; item = Q if target is behind the line.  Up to
 // kFindWarp items each warp finds it by itself (no barrier), above with the whole
-// block.  `scratch`: kFindWords ints of shared memory.
+// block, a thread's sum of counts ending at kMost.  `scratch`: kFindWords ints of shared
+// memory.
 constexpr int kFindWords = 40;
 constexpr int kFindWarp = 128;
 struct Found {
@@ -102,7 +103,7 @@ struct Found {
     int total;
 };
 
-template <int THREADS, typename Total, typename Count>
+template <int THREADS, int kMost = 0x7fffffff, typename Total, typename Count>
 __device__ __forceinline__ Found block_find(int Q, int* scratch, Total target_of, Count count) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (Q <= kFindWarp) {
@@ -139,7 +140,7 @@ __device__ __forceinline__ Found block_find(int Q, int* scratch, Total target_of
     const int per = (Q + THREADS - 1) / THREADS;
     const int lo = min(tid * per, Q), hi = min(lo + per, Q);
     int sum = 0;
-    for (int b = lo; b < hi; ++b) sum += count(b);
+    for (int b = lo; b < hi; ++b) sum = min(sum + count(b), kMost);
     int inc = sum;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -299,38 +300,21 @@ __device__ __forceinline__ PackedSeq packed_seq(const ExpandedArgs& a, int b) {
 
 // The sequence of a CTA's unit in the line of all units of 2^span_log queries, by the
 // whole block.  The grid has units for Nq queries, one sequence each; a q_lens that
-// decreases would give queries to several.  So sequences have queries only up to the
-// first pair that does; the second search is for such a q_lens alone.  `tell`: the CTA
-// that reports bad pairs.
+// decreases would give queries to several.  A pair that does takes more units than any
+// grid has (2^23 queries in 16s and 2^14 sequences), so that nothing behind it is found,
+// and has no queries itself: a sequence found may have none.  (A second search for such
+// lengths, or a vote on them, cost good calls 1 %.)  `tell`: the CTA that reports.
 template <int THREADS>
 __device__ __forceinline__ Found packed_find(const ExpandedArgs& a, int* scratch, int unit,
                                              int span_log, bool tell) {
-    int end = a.Q;
-    Found f;
-    for (bool again = true; again;) {
-        int fall = a.Q;
-        f = block_find<THREADS>(
-            a.Q, scratch, [&](int) { return unit; },
-            [&](int b) {
-                const PackedSeq s = packed_seq(a, b);
-                if (s.bad && tell) report(a.dev_status, s.bad);
-                if (s.falls) fall = min(fall, b);
-                return b < end ? (s.nq + (1 << span_log) - 1) >> span_log : 0;
-            });
-        if (a.Q <= kFindWarp) {
-            fall = __reduce_min_sync(0xffffffffu, fall);
-        } else if (__syncthreads_or(fall < end)) {
-            if (threadIdx.x == 0) scratch[0] = a.Q;
-            __syncthreads();
-            if (fall < a.Q) atomicMin(scratch, fall);
-            __syncthreads();
-            fall = scratch[0];
-            __syncthreads();
-        }
-        again = fall < end;
-        end = min(end, fall);
-    }
-    return f;
+    constexpr int kBehindAll = 1 << 20;
+    return block_find<THREADS, 2 * kBehindAll>(
+        a.Q, scratch, [&](int) { return unit; },
+        [&](int b) {
+            const PackedSeq s = packed_seq(a, b);
+            if (s.bad && tell) report(a.dev_status, s.bad);
+            return s.falls ? kBehindAll : (s.nq + (1 << span_log) - 1) >> span_log;
+        });
 }
 
 cudaError_t launch_expanded_mma(const ExpandedArgs& a, cudaStream_t stream);

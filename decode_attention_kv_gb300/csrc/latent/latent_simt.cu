@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(kGroups * kThreads) expanded_simt_kernel(const
     const Found f = packed_find<kGroups * kThreads>(a, scratch, unit, kRowsLog, h == 0 && unit == 0);
     if (f.item >= a.Q) return;
     const PackedSeq seq = packed_seq(a, f.item);
+    if (seq.nq == 0) return;
     // the last rows of a sequence first: under the causal mask they see most keys
     const int units = (seq.nq + kRows - 1) / kRows;
     const int row0 = (units - 1 - (unit - f.before)) * kRows, nrows = min(kRows, seq.nq - row0);

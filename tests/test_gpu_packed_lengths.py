@@ -41,6 +41,7 @@ def expanded(kvd, lens, c, sequences):
     ([0, 300, 100, 200, 300], [0]),
     ([0, 5000, 100, 300], []),          # past the queries, then decreasing
     ([0, -4, 100, 300], []),
+    ([0, 100, 5000], [0]),              # past the queries: only that pair is bad
     ([3, 100, 300], [1]),               # not from zero: only that pair is bad
 ], ids=str)
 def test_expanded_decreasing(kvd, lens, sequences, dtype):
@@ -64,6 +65,14 @@ def test_expanded_decreasing_among_many(kvd, dtype):
     lens[201] -= 150
     lens[250] -= 1000
     expanded(kvd, lens, c, range(200))
+
+
+def test_expanded_decreasing_all_along(kvd):
+    """As many falling pairs as there may be sequences: nothing but the first is found."""
+    nq = [3] + [0] * 16383
+    for dtype in (BF, F32):
+        c = Packed(nq, nq, 1, 64, 64, dtype, seed=3)
+        expanded(kvd, ([0, 3] + [2, 3] * 8192)[:16385], c, [0])
 
 
 # ------------------------------------------------------------------ append
