@@ -2,7 +2,7 @@
 // the C entry points: argument checks, outputs, device and stream.  A decode loop
 // makes these calls every few microseconds; with the same checks in Python and 18
 // to 25 arguments converted by ctypes the host took 9.3 us for an append, 16 for a
-// verification, 20 and 26 for the attentions; now 2.9, 6.6, 12 and 15 (their
+// verification, 20 and 26 for the attentions; now 2.8, 5.8, 11 and 13 (their
 // outputs' allocation among it).
 //
 // The entry points come from the library that kvd.py has loaded (bind); errors

@@ -15,9 +15,10 @@
 // asked for at least one product of 1280 cycles before it is needed.
 //
 // What bounds it: the chain of a step (softmax 1160 cycles, hand-overs, products
-// 1500) is 3300 cycles against 2616 of MMA time for both tiles: 1580 TFLOP/s at one
-// sequence of 8192 x 16 heads, 1290 at four of 1024 to 4096 x 32 heads (329 us),
-// where starting and ending a unit counts.
+// 1500) is 3300 cycles against 2616 of MMA time for both tiles: 218 us in a graph, 220
+// as called (1560 TFLOP/s) at one sequence of 8192 x 16 heads; 330 us in a graph over
+// the same inputs, 350 as called over inputs in turn (1220 TFLOP/s) at four of 1024 to
+// 4096 x 32 heads, where starting and ending a unit counts.
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, a row a thread.  Warps 8 and 9
 // issue the MMAs of tile 0 and 1: what one spends on waiting and setting up (450
@@ -454,8 +455,8 @@ cudaError_t go_expanded(const ExpandedArgs& a, const CUtensorMap& qmap, const CU
 cudaError_t launch_expanded_mma(const ExpandedArgs& args, cudaStream_t stream) {
     ExpandedArgs a = args;
     // One query tile a CTA where all CTAs still run at once: the tensor cores wait, but
-    // a step is over sooner (300 x 8 heads 10.8 -> 9.4 us, 1024 x 16 20.1 -> 17.0, 2048 x
-    // 8 32.3 -> 28.5; but 4 x 512 x 16, 256 CTAs of work, 16.4 -> 21.5).
+    // a step is over sooner (in a graph: 300 x 8 heads 10.8 -> 9.4 us, 1024 x 16 20.1 ->
+    // 17.0, 2048 x 8 32.3 -> 28.5; but 4 x 512 x 16, 256 CTAs of work, 16.4 -> 21.5).
     a.span_log = (long long)a.H * ((a.Nq - 1) / kRows + 1 + a.Q) <= kLatentSMs ? 7 : 8;
     CUtensorMap qmap, kvmap, ropemap;
     const long long qw = (long long)a.H * (a.Dn + a.P), kw = (long long)a.H * (a.Dn + a.Dv);

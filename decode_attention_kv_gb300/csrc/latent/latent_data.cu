@@ -15,7 +15,8 @@ namespace cg = cooperative_groups;
 // The sequence of a packed row comes from a binary search in new_lens.  The
 // row's own loads do not depend on the search, so they are issued first.  (2, 4
 // and 8 rows a warp copied 21000 rows of 1152 bytes no faster: 11.2, 11.9 and
-// 13.3 against 11.1 us.)  21000 rows: 4.3 TB/s read and written; 64 rows: 2.8 us.
+// 13.3 against 11.1 us.)  21000 rows: 11.3 us in a graph, 10.6 as called over inputs in
+// turn, 4.4 to 4.7 TB/s read and written; 64 rows: 2.8 and 3.3 us.
 constexpr int kAppendWarps = 8;
 constexpr int kAppendVecs = 4;  // vectors a lane holds across the search
 
@@ -108,8 +109,8 @@ append_latent_kernel(unsigned char* __restrict__ latent, unsigned char* __restri
 // worst 2^-36); these are added in 64 bits, those of a CTA's warps by one warp (a
 // 64-bit addition holds an SM's unit for 16 cycles a warp: with all warps at it
 // every few elements they took longer than the row).
-// 64 rows of 128000 fp32: 18.4 us, 3.6 TB/s, 21 instructions an element; one row of
-// 32000: 6.9 us, a chain of five memory latencies and two barriers.
+// 64 rows of 128000 fp32: 18.2 us, 3.6 TB/s, 21 instructions an element; one row of
+// 32000: 7.0 us, a chain of five memory latencies and two barriers.
 constexpr int kVerifyMaxCtas = 8;
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
@@ -125,8 +126,8 @@ __device__ __forceinline__ float as_prob(__nv_bfloat16 x) { return __bfloat162fl
 
 // kVerifyBatch elements a lane of [i0, hi): element 32 * VEC * k + VEC * lane + e
 // in x[VEC * k + e]; zeros behind hi.  VEC elements are one 16-byte load.
-// (Rows of an odd length in bf16 cut out of two aligned vectors instead of 2-byte
-// loads: 21.6 against 19.2 us for 128 x 7 drafts over 50257.)
+// (Rows of an odd length in bf16, 128 x 7 drafts over 50257: 18.4 us; cut out of two
+// aligned vectors instead of 2-byte loads they took 21.6 where these took 19.2.)
 template <typename Elem, int VEC>
 __device__ __forceinline__ void load_batch(const Elem* p, int i0, int hi, float (&x)[kVerifyBatch]) {
     const int lane = threadIdx.x & 31;

@@ -17,10 +17,11 @@
 // than 8 (log2 units), as in the decode kernel: weights stay below 2^8.
 //
 // What bounds it: at 16 rows HBM (64 sequences of 512 to 8192 tokens, R = 512:
-// 63.8 us with the merge, 5.2 TB/s; 6.2 TB/s between the first tile and the last),
-// at 64 rows the round of a stage (copy, scores, softmax, values: two tiles in
-// 5900 cycles, 1920 of MMA time each; 16 sequences of 1001 to 16384, 128 rows:
-// 90.8 us, 750 TFLOP/s).  Two stages of 72 KB are what 72 KB of queries leave.
+// 64.4 us with the merge in a graph, 65.5 as called from Python, 5.0 TB/s; 6.2 TB/s
+// where 8 sequences of 100000 stream), at 64 rows the round of a stage (copy, scores,
+// softmax, values: two tiles in 5900 cycles, 1920 of MMA time each; 16 sequences of
+// 1001 to 16384, 128 rows: 90.8 us, as called 91.5, 744 TFLOP/s).  Two stages of 72 KB
+// are what 72 KB of queries leave.
 #include "../kvd_internal.h"
 #include "latent_common.cuh"
 #include "tcgen05_ptx.cuh"
