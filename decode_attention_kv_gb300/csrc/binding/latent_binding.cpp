@@ -1,5 +1,5 @@
-// latent_binding.cpp -- the latent-cache calls of kvd.py, from torch tensors to
-// the C entry points: argument checks, outputs, device and stream.  A decode loop
+// latent_binding.cpp -- the latent-cache and serving-step calls of kvd.py, from torch
+// tensors to the C entry points: argument checks, outputs, device and stream.  A decode loop
 // makes these calls every few microseconds; with the same checks in Python and 18
 // to 25 arguments converted by ctypes the host took 9.3 us for an append, 16 for a
 // verification, 20 and 26 for the attentions; now 2.8, 5.8, 11 and 13 (their
@@ -29,6 +29,13 @@ decltype(&kvd_attend_latent_workspace_bytes) g_workspace = nullptr;
 decltype(&kvd_attend_latent) g_attend = nullptr;
 decltype(&kvd_attend_expanded) g_expanded = nullptr;
 decltype(&kvd_verify_drafts) g_verify = nullptr;
+decltype(&kvd_plan_pages) g_plan_pages = nullptr;
+decltype(&kvd_rotate) g_rotate = nullptr;
+decltype(&kvd_rotate_append_paged) g_rotate_append = nullptr;
+decltype(&kvd_attend_paged_prefix_workspace_bytes) g_prefix_workspace = nullptr;
+decltype(&kvd_attend_paged_prefix) g_prefix = nullptr;
+decltype(&kvd_sample) g_sample = nullptr;
+decltype(&kvd_filter_probs) g_filter = nullptr;
 PyObject* g_check = nullptr;  // kvd._check(name, status): raises
 
 // A Python exception that is set already.
@@ -125,6 +132,34 @@ struct Call {
         const double x = PyFloat_AsDouble(args[i]);
         if (x == -1.0 && PyErr_Occurred()) throw Raised{};
         return (float)x;
+    }
+    int whole(int i, const char* name) const {
+        const long long x = PyLong_AsLongLong(args[i]);
+        if (x == -1 && PyErr_Occurred()) throw Raised{};
+        if (x < INT32_MIN) raise(PyExc_ValueError, where(name) + " does not fit 32 bits");
+        return small(x, name);
+    }
+    bool truth(int i) const {
+        const int x = PyObject_IsTrue(args[i]);
+        if (x < 0) throw Raised{};
+        return x != 0;
+    }
+    // A tensor's first extent, for arguments whose length sets others'.
+    int64_t length(int i, const char* name, int dims, const char* form) const {
+        const at::Tensor& t = tensor(i, name);
+        if (t.dim() != dims) raise(PyExc_ValueError, where(name) + " must be " + form);
+        return t.size(0);
+    }
+    at::Tensor scratch(int i, size_t bytes) const {
+        if (given(i)) {
+            const at::Tensor& t = tensor(i, "workspace");
+            if (!t.is_cuda() || !t.is_contiguous() || t.get_device() != dev)
+                raise(PyExc_ValueError, where("workspace") +
+                                            " must be a contiguous CUDA tensor of the call's device");
+            return t;
+        }
+        return at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(
+                                               at::kCUDA, (c10::DeviceIndex)dev));
     }
     int small(int64_t x, const char* name) const {
         if (x > INT32_MAX) raise(PyExc_ValueError, where(name) + " does not fit 32 bits");
@@ -312,6 +347,181 @@ PyObject* verify_drafts(Call& c) {
     return r;
 }
 
+PyObject* tuple_of(std::initializer_list<at::Tensor> ts) {
+    PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
+    if (!r) throw Raised{};
+    Py_ssize_t i = 0;
+    for (const at::Tensor& t : ts) {
+        PyObject* o = THPVariable_Wrap(t);
+        if (!o) {
+            Py_DECREF(r);
+            throw Raised{};
+        }
+        PyTuple_SET_ITEM(r, i++, o);
+    }
+    return r;
+}
+
+int32_t* ints(void* p) { return static_cast<int32_t*>(p); }
+float* floats(void* p) { return static_cast<float*>(p); }
+
+PyObject* plan_pages(Call& c) {
+    const at::Tensor& bt = c.first(0, "block_tables", 2, "int32 [Q, cols]");
+    const int64_t Q = bt.size(0), cols = bt.size(1), F = c.length(2, "free_pages", 1, "int32 [F]");
+    int32_t* tables = ints(c.data(bt, "block_tables", kI32, {Q, cols}));
+    int32_t* held = ints(c.data(1, "pages_held", kI32, {Q}));
+    int32_t* pages = ints(c.data(2, "free_pages", kI32, {F}));
+    int32_t* count = ints(c.data(3, "free_count", kI32, {1}));
+    const int32_t* kept = ints(c.data(4, "kept_lens", kI32, {Q}));
+    const int32_t* lens = ints(c.data(5, "new_lens", kI32, {Q + 1}));
+    const int bs = c.whole(6, "block_size"), n = c.whole(7, "num_tokens");
+    if (n < 0) raise(PyExc_ValueError, c.where("num_tokens") + " must not be negative");
+    const int32_t* base = ints(c.maybe(8, "pos_base", kI32, {Q}));
+    int32_t* status = c.status(12);
+    const int q = c.small(Q, "block_tables"), co = c.small(cols, "block_tables"),
+              f = c.small(F, "free_pages");
+    at::Tensor sl = c.output(9, "seq_lens", kI32, {Q + 1}), st = c.output(10, "slots", kI32, {n}),
+               ps = c.output(11, "positions", kI32, {n});
+    c.run("kvd_plan_pages", [&](kvd_stream_t s) {
+        return g_plan_pages(tables, held, pages, count, kept, lens, base, ints(sl.data_ptr()),
+                            ints(st.data_ptr()), ints(ps.data_ptr()), q, n, bs, co, f, status, s);
+    });
+    return tuple_of({sl, st, ps});
+}
+
+PyObject* rotate(Call& c) {
+    const at::Tensor& x = c.first(0, "x", 3, "[N, H, D]");
+    const at::ScalarType dtype = x.scalar_type();
+    const int64_t N = x.size(0), H = x.size(1), D = x.size(2),
+                  F = c.length(2, "freqs", 1, "float64 [Dr / 2]");
+    const kvd_dtype dt = c.code(dtype);
+    const void* xp = c.data(x, "x", dtype, {N, H, D});
+    const int32_t* pos = ints(c.data(1, "positions", kI32, {N}));
+    auto* freqs = static_cast<const double*>(c.data(2, "freqs", at::kDouble, {F}));
+    const void* w = c.maybe(3, "weight", dtype, {D});
+    const float eps = c.number(4), scale = c.number(6);
+    const bool inter = c.truth(5);
+    int32_t* status = c.status(8);
+    const int n = c.small(N, "x"), h = c.small(H, "x"), d = c.small(D, "x"),
+              dr = c.small(2 * F, "freqs");
+    at::Tensor out = c.output(7, "out", dtype, {N, H, D});
+    c.run("kvd_rotate", [&](kvd_stream_t s) {
+        return g_rotate(xp, w, freqs, pos, out.data_ptr(), n, h, d, dr, inter, scale, eps, dt,
+                        status, s);
+    });
+    return THPVariable_Wrap(out);
+}
+
+PyObject* rotate_append_paged(Call& c) {
+    const at::Tensor& x = c.first(0, "qkv", 3, "[N, Hq + 2 Hkv, D]");
+    const at::Tensor &kc = c.tensor(1, "key_cache"), &vc = c.tensor(2, "value_cache");
+    if (kc.dim() != 4) raise(PyExc_ValueError, c.where("key_cache") + " must be [NB, BS, Hkv, D]");
+    const at::ScalarType dtype = x.scalar_type();
+    const int64_t N = x.size(0), NB = kc.size(0), BS = kc.size(1), Hkv = kc.size(2), D = kc.size(3),
+                  Hq = x.size(1) - 2 * Hkv, F = c.length(5, "freqs", 1, "float64 [Dr / 2]");
+    if (Hq < 1)
+        raise(PyExc_ValueError, c.where("qkv") + " has " + std::to_string(x.size(1)) +
+                                    " heads, " + std::to_string(Hkv) + " of them keys and " +
+                                    std::to_string(Hkv) + " values");
+    const kvd_dtype dt = c.code(dtype);
+    const void* xp = c.data(x, "qkv", dtype, {N, Hq + 2 * Hkv, D});
+    void* kp = c.data(kc, "key_cache", dtype, {NB, BS, Hkv, D});
+    void* vp = c.data(vc, "value_cache", dtype, {NB, BS, Hkv, D});
+    const int32_t* slots = ints(c.data(3, "slots", kI32, {N}));
+    const int32_t* pos = ints(c.data(4, "positions", kI32, {N}));
+    auto* freqs = static_cast<const double*>(c.data(5, "freqs", at::kDouble, {F}));
+    const void* qw = c.maybe(6, "q_weight", dtype, {D});
+    const void* kw = c.maybe(7, "k_weight", dtype, {D});
+    const float eps = c.number(8), scale = c.number(10);
+    const bool inter = c.truth(9);
+    int32_t* status = c.status(12);
+    const int n = c.small(N, "qkv"), hq = c.small(Hq, "qkv"), hk = c.small(Hkv, "key_cache"),
+              nb = c.small(NB, "key_cache"), bs = c.small(BS, "key_cache"),
+              d = c.small(D, "key_cache"), dr = c.small(2 * F, "freqs");
+    at::Tensor out = c.output(11, "out", dtype, {N, Hq, D});
+    c.run("kvd_rotate_append_paged", [&](kvd_stream_t s) {
+        return g_rotate_append(xp, qw, kw, freqs, pos, slots, out.data_ptr(), kp, vp, n, hq, hk, nb,
+                               bs, d, dr, inter, scale, eps, dt, status, s);
+    });
+    return THPVariable_Wrap(out);
+}
+
+PyObject* attend_paged_prefix(Call& c) {
+    const at::Tensor& q = c.first(0, "q", 3, "[Q, Hq, D]");
+    const at::Tensor &kc = c.tensor(1, "key_cache"), &vc = c.tensor(2, "value_cache"),
+                     &pt = c.tensor(3, "prefix_tables");
+    if (kc.dim() != 4) raise(PyExc_ValueError, c.where("key_cache") + " must be [NB, BS, Hkv, D]");
+    if (pt.dim() != 2) raise(PyExc_ValueError, c.where("prefix_tables") + " must be int32 [G, pcols]");
+    const at::ScalarType dtype = q.scalar_type();
+    const int64_t Q = q.size(0), Hq = q.size(1), D = q.size(2), NB = kc.size(0), BS = kc.size(1),
+                  Hkv = kc.size(2), G = pt.size(0), pcols = pt.size(1), cols = columns(c, 6);
+    const kvd_dtype dt = c.code(dtype);
+    const void* qp = c.data(q, "q", dtype, {Q, Hq, D});
+    const void* kp = c.data(kc, "key_cache", dtype, {NB, BS, Hkv, D});
+    const void* vp = c.data(vc, "value_cache", dtype, {NB, BS, Hkv, D});
+    const int32_t* pp = ints(c.data(pt, "prefix_tables", kI32, {G, pcols}));
+    const int32_t* pl = ints(c.data(4, "prefix_lens", kI32, {G}));
+    const int32_t* gl = ints(c.data(5, "group_lens", kI32, {G + 1}));
+    const int32_t* tables = ints(c.data(6, "block_tables", kI32, {Q, cols}));
+    const int32_t* lens = ints(c.data(7, "seq_lens", kI32, {Q + 1}));
+    const int32_t* offset = ints(c.maybe(8, "seq_offset", kI32, {Q}));
+    const float scale = c.number(9);
+    float* lse = floats(c.maybe(11, "lse", kF32, {Q, Hq}));
+    int32_t* status = c.status(13);
+    const int n = c.small(Q, "q"), g = c.small(G, "prefix_tables"), hq = c.small(Hq, "q"),
+              hk = c.small(Hkv, "key_cache"), nb = c.small(NB, "key_cache"),
+              bs = c.small(BS, "key_cache"), pc = c.small(pcols, "prefix_tables"),
+              co = c.small(cols, "block_tables"), d = c.small(D, "q");
+    at::Tensor out = c.output(10, "out", dtype, {Q, Hq, D});
+    at::Tensor ws = c.scratch(12, c.given(12) ? 0 : g_prefix_workspace(n, g, hq, hk, bs, pc, co, d, dt));
+    c.run("kvd_attend_paged_prefix", [&](kvd_stream_t s) {
+        return g_prefix(qp, kp, vp, pp, pl, gl, tables, lens, offset, out.data_ptr(), lse, n, g, hq,
+                        hk, nb, bs, pc, co, d, scale, dt, ws.data_ptr(), ws.nbytes(), status, s);
+    });
+    return THPVariable_Wrap(out);
+}
+
+PyObject* sample_rows(Call& c) {
+    const at::Tensor& l = c.first(0, "logits", 2, "[R, V]");
+    const at::ScalarType dtype = l.scalar_type();
+    const int64_t R = l.size(0), V = l.size(1);
+    const kvd_dtype dt = c.code(dtype);
+    const void* lp = c.data(l, "logits", dtype, {R, V});
+    const float* u = floats(c.data(1, "u", kF32, {R}));
+    const float* temp = floats(c.maybe(2, "temperature", kF32, {R}));
+    const int32_t* k = ints(c.maybe(3, "top_k", kI32, {R}));
+    const float* p = floats(c.maybe(4, "top_p", kF32, {R}));
+    const float* m = floats(c.maybe(5, "min_p", kF32, {R}));
+    int32_t* status = c.status(7);
+    const int r = c.small(R, "logits"), v = c.small(V, "logits");
+    at::Tensor tokens = c.output(6, "tokens", kI32, {R});
+    c.run("kvd_sample", [&](kvd_stream_t s) {
+        return g_sample(lp, temp, k, p, m, u, ints(tokens.data_ptr()), r, v, dt, status, s);
+    });
+    return THPVariable_Wrap(tokens);
+}
+
+PyObject* filter_probs(Call& c) {
+    const at::Tensor& l = c.first(0, "logits", 2, "[R, V]");
+    const at::ScalarType dtype = l.scalar_type();
+    const int64_t R = l.size(0), V = l.size(1);
+    const kvd_dtype dt = c.code(dtype);
+    const void* lp = c.data(l, "logits", dtype, {R, V});
+    const float* temp = floats(c.maybe(1, "temperature", kF32, {R}));
+    const int32_t* k = ints(c.maybe(2, "top_k", kI32, {R}));
+    const float* p = floats(c.maybe(3, "top_p", kF32, {R}));
+    const float* m = floats(c.maybe(4, "min_p", kF32, {R}));
+    const at::ScalarType to = c.given(5) ? c.tensor(5, "out").scalar_type() : dtype;
+    const kvd_dtype pt = c.code(to);
+    int32_t* status = c.status(6);
+    const int r = c.small(R, "logits"), v = c.small(V, "logits");
+    at::Tensor out = c.output(5, "out", to, {R, V});
+    c.run("kvd_filter_probs", [&](kvd_stream_t s) {
+        return g_filter(lp, temp, k, p, m, out.data_ptr(), r, v, dt, pt, status, s);
+    });
+    return THPVariable_Wrap(out);
+}
+
 // No C++ exception leaves a call.
 template <PyObject* (*F)(Call&), int N>
 PyObject* guarded(const char* fn, PyObject* const* args, Py_ssize_t n) {
@@ -346,16 +556,44 @@ PyObject* py_verify(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded<verify_drafts, 9>("verify_drafts", a, n);
 }
 
-// bind(check, five addresses): the entry points of the loaded library.
+PyObject* py_plan_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded<plan_pages, 13>("plan_pages", a, n);
+}
+PyObject* py_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded<rotate, 9>("rotate", a, n);
+}
+PyObject* py_rotate_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded<rotate_append_paged, 13>("rotate_append_paged", a, n);
+}
+PyObject* py_prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded<attend_paged_prefix, 14>("attend_paged_prefix", a, n);
+}
+PyObject* py_sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded<sample_rows, 8>("sample", a, n);
+}
+PyObject* py_filter(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded<filter_probs, 7>("filter_probs", a, n);
+}
+
+// bind(check, twelve addresses): the entry points of the loaded library.
 PyObject* py_bind(PyObject*, PyObject* args) {
     PyObject* check;
-    unsigned long long f[5];
-    if (!PyArg_ParseTuple(args, "OKKKKK", &check, f, f + 1, f + 2, f + 3, f + 4)) return nullptr;
+    unsigned long long f[12];
+    if (!PyArg_ParseTuple(args, "OKKKKKKKKKKKK", &check, f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6,
+                          f + 7, f + 8, f + 9, f + 10, f + 11))
+        return nullptr;
     g_append = reinterpret_cast<decltype(g_append)>(f[0]);
     g_workspace = reinterpret_cast<decltype(g_workspace)>(f[1]);
     g_attend = reinterpret_cast<decltype(g_attend)>(f[2]);
     g_expanded = reinterpret_cast<decltype(g_expanded)>(f[3]);
     g_verify = reinterpret_cast<decltype(g_verify)>(f[4]);
+    g_plan_pages = reinterpret_cast<decltype(g_plan_pages)>(f[5]);
+    g_rotate = reinterpret_cast<decltype(g_rotate)>(f[6]);
+    g_rotate_append = reinterpret_cast<decltype(g_rotate_append)>(f[7]);
+    g_prefix_workspace = reinterpret_cast<decltype(g_prefix_workspace)>(f[8]);
+    g_prefix = reinterpret_cast<decltype(g_prefix)>(f[9]);
+    g_sample = reinterpret_cast<decltype(g_sample)>(f[10]);
+    g_filter = reinterpret_cast<decltype(g_filter)>(f[11]);
     Py_INCREF(check);
     Py_XSETREF(g_check, check);
     Py_RETURN_NONE;
@@ -368,6 +606,12 @@ PyMethodDef g_methods[] = {
     FAST("attend_latent", py_attend),
     FAST("attend_expanded", py_expanded),
     FAST("verify_drafts", py_verify),
+    FAST("plan_pages", py_plan_pages),
+    FAST("rotate", py_rotate),
+    FAST("rotate_append_paged", py_rotate_append),
+    FAST("attend_paged_prefix", py_prefix),
+    FAST("sample", py_sample),
+    FAST("filter_probs", py_filter),
     {nullptr, nullptr, 0, nullptr},
 };
 

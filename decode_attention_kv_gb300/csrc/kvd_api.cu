@@ -383,6 +383,57 @@ namespace kvd {
 void set_last_error(const char* msg) {
     snprintf(g_last_error, sizeof g_last_error, "%s", msg);
 }
+
+PagedPartial paged_partial_plan(int Q, int Hq, int Hkv, int BS, int cols, int D, kvd_dtype dt) {
+    const Plan pl = plan_attention(Q, Hq, Hkv, cols * BS, D, dt, BS, 0);
+    PagedPartial pp{};
+    pp.S = pl.S;
+    pp.off_lse = 256;
+    pp.off_o = pp.off_lse + round256((size_t)Q * Hq * pl.S * sizeof(float));
+    pp.bytes = pp.off_o + (size_t)Q * Hq * pl.S * D * sizeof(float);
+    pp.units = pl.units;
+    return pp;
+}
+
+kvd_status launch_paged_partial(const char* fn, const PagedPartial& pp, const void* q,
+                                const void* key_cache, const void* value_cache,
+                                const int32_t* block_tables, const int32_t* seq_lens,
+                                const int32_t* seq_offset, int Q, int Hq, int Hkv, int NB, int BS,
+                                int cols, int D, float scale, kvd_dtype dt, void* region,
+                                int32_t* dev_status, cudaStream_t stream) {
+    const Plan pl = plan_attention(Q, Hq, Hkv, cols * BS, D, dt, BS, 0);
+    CUtensorMap kmap, vmap;
+    const bool mma = attend_uses_mma(dt, pl.G);
+    kvd_status st = make_cache_map(&kmap, key_cache, dt, true, (long long)NB * BS, Hkv, D, pl.tile, mma);
+    if (st != KVD_OK) return st;
+    st = make_cache_map(&vmap, value_cache, dt, true, (long long)NB * BS, Hkv, D, pl.tile, mma);
+    if (st != KVD_OK) return st;
+    AttendParams p{};
+    p.q = q;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.seq_offset = seq_offset;
+    p.dev_status = dev_status;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.g = Hq / Hkv;
+    p.BS = BS;
+    p.cols = cols;
+    p.NB = NB;
+    p.qscale = scale * kLog2e;
+    attach_workspace(p, pl, region);
+    char* base = static_cast<char*>(region);
+    p.part_lse = reinterpret_cast<float*>(base + pp.off_lse);
+    p.part_o = reinterpret_cast<float*>(base + pp.off_o);
+    if (p.direct) {  // one split: its output rows, in fp32, are the partial rows
+        p.out = p.part_o;
+        p.lse_out = p.part_lse;
+        p.out_f32 = 1;
+    }
+    const cudaError_t e = launch_attend(dt, D, pl.G, kModePaged, p, &kmap, &vmap, stream);
+    if (e != cudaSuccess) return fail(KVD_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+    return KVD_OK;
+}
 }  // namespace kvd
 
 // ===================================================================== C ABI

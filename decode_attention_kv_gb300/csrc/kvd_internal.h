@@ -60,6 +60,23 @@ cudaError_t launch_combine(const float* part_o, const float* part_lse, void* out
                            float* lse_out, int R, int S, int D, kvd_dtype out_dt,
                            cudaStream_t stream, long long gathered_stride = 0);
 
+// kvd_attend_paged up to its partial rows, for a caller that merges them with others:
+// fp32 rows part_o [Q * Hq, S, D], normalised, and part_lse [Q * Hq, S] (natural log,
+// -inf: the row was not written), whatever S is, at these offsets of its region of the
+// workspace, which begins with the work counters (two words, zero before the launch).
+struct PagedPartial {
+    int S;
+    size_t off_lse, off_o, bytes;
+    long long units;
+};
+PagedPartial paged_partial_plan(int Q, int Hq, int Hkv, int BS, int cols, int D, kvd_dtype dt);
+kvd_status launch_paged_partial(const char* fn, const PagedPartial& pp, const void* q,
+                                const void* key_cache, const void* value_cache,
+                                const int32_t* block_tables, const int32_t* seq_lens,
+                                const int32_t* seq_offset, int Q, int Hq, int Hkv, int NB, int BS,
+                                int cols, int D, float scale, kvd_dtype dt, void* region,
+                                int32_t* dev_status, cudaStream_t stream);
+
 cudaError_t launch_copy_prefix(const void* const* k_src, const void* const* v_src,
                                void* const* k_dst, void* const* v_dst, uint8_t* const* masks,
                                const int32_t* n, int L, int B, int Hkv, int C_src, int C_dst,

@@ -1,0 +1,259 @@
+// plan_pages.cu -- kvd_plan_pages: pages, slots and positions of a step's new tokens
+// from the requests' lengths.
+//
+// One cluster does the whole call, because three things have to follow one another
+// over all sequences: pages given back enter the free list, pages are taken from its
+// end, and tokens look up the tables that result.  A cluster barrier orders these in
+// a microsecond; every CTA scans all sequences by itself (1024 at a time) instead of
+// exchanging sums, and the CTAs share the pages and the tokens out by index, so that
+// one sequence of many pages takes no longer than many of one page.
+#include <cooperative_groups.h>
+
+#include "../kvd_internal.h"
+#include "serving_common.cuh"
+
+namespace kvd {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kMaxCtas = 8;
+
+struct PlanShared {
+    long long warp_sum[kWarps];
+    int end[kThreads];    // of this chunk: pages up to and with a sequence's own
+    int held[kThreads];
+};
+
+// Inclusive sums over the CTA; `total` is the last one.
+__device__ __forceinline__ long long block_sums(PlanShared& sh, long long x, long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += o;
+    }
+    __syncthreads();
+    if (lane == 31) sh.warp_sum[warp] = x;
+    __syncthreads();
+    long long s = sh.warp_sum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += o;
+    }
+    total = __shfl_sync(0xffffffffu, s, 31);
+    const long long before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+    return x + (warp > 0 ? before : 0);
+}
+
+// The sequence of the chunk that page i belongs to.
+__device__ __forceinline__ int chunk_find(const PlanShared& sh, long long i) {
+    int lo = 0, hi = kThreads - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.end[mid] > i)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    return lo;
+}
+
+// What a sequence has and wants.
+struct PlanSeq {
+    int kept, n, held, need;  // tokens, tokens, pages, pages
+    bool good;
+};
+
+// (`lens`: new_lens is in order.)
+__device__ __forceinline__ PlanSeq plan_seq(const PlanArgs& a, int q, bool lens, uint32_t& bits) {
+    PlanSeq s{0, 0, 0, 0, false};
+    if (q >= a.Q) return s;
+    const int s0 = lens ? a.new_lens[q] : 0, s1 = lens ? a.new_lens[q + 1] : 0;
+    const int kept = a.kept_lens[q], held = a.pages_held[q];
+    const long long total = (long long)kept + (s1 - s0);
+    if (kept < 0 || held < 0 || held > a.cols || kept > (long long)held * a.BS ||
+        total > 0x7fffffffll) {
+        bits |= KVD_DEV_POS_RANGE;
+        return s;
+    }
+    s.kept = kept;
+    s.n = s1 - s0;
+    s.held = held;
+    s.need = (int)((total + a.BS - 1) / a.BS);
+    s.good = true;
+    return s;
+}
+
+__global__ void __launch_bounds__(kThreads) plan_pages_kernel(const PlanArgs a) {
+    __shared__ PlanShared sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, rank = (int)cluster.block_rank(),
+              ctas = (int)cluster.num_blocks();
+    const int all = ctas * kThreads, me = rank * kThreads + tid;
+    const bool lead = rank == 0;
+    uint32_t bits = 0;
+    int count = a.free_count[0];
+    bool lens_ok = true;
+    for (int q = tid; q < a.Q; q += kThreads) {
+        const int s0 = a.new_lens[q], s1 = a.new_lens[q + 1];
+        lens_ok &= (q > 0 || s0 == 0) && s1 >= s0 && s1 <= a.N;
+    }
+    lens_ok = __syncthreads_and(lens_ok);
+    // what refuses every sequence
+    const bool usable = lens_ok && count >= 0 && count <= a.F;
+    if (!lens_ok) bits |= KVD_DEV_SEQLENS;
+    if (count < 0 || count > a.F) bits |= KVD_DEV_POS_RANGE;
+
+    // pages given back: all, or none where the list has no room for all
+    long long given = 0;
+    for (int q0 = 0; usable && q0 < a.Q; q0 += kThreads) {
+        const PlanSeq s = plan_seq(a, q0 + tid, true, bits);
+        long long t;
+        block_sums(sh, s.good && s.held > s.need ? s.held - s.need : 0, t);
+        given += t;
+    }
+    const bool give_back = usable && given <= a.F - count;
+    if (usable && !give_back) bits |= KVD_DEV_NO_PAGES;
+    if (given > 0 && give_back) {
+        long long before = 0;  // by the sequences before this chunk
+        for (int q0 = 0; q0 < a.Q; q0 += kThreads) {
+            const PlanSeq s = plan_seq(a, q0 + tid, true, bits);
+            long long t;
+            const long long end = block_sums(sh, s.good && s.held > s.need ? s.held - s.need : 0, t);
+            sh.end[tid] = (int)end;
+            sh.held[tid] = s.held;
+            __syncthreads();
+            // the last sequence's last page goes first: page i of the chunk (columns
+            // rising) lies behind all pages after it
+            const long long base = count + (given - before - t);
+            for (long long i = me; i < t; i += all) {
+                const int k = chunk_find(sh, i);
+                a.free_pages[base + t - 1 - i] =
+                    a.block_tables[(size_t)(q0 + k) * a.cols + sh.held[k] - (int)(sh.end[k] - i)];
+            }
+            before += t;
+            __syncthreads();
+        }
+    }
+    cluster.sync();  // the list is whole
+
+    const long long avail = usable ? count + (give_back ? given : 0) : 0;
+    // by the sequences before this chunk; asked: tokens of refused ones among them
+    long long wanted = 0, taken = 0, asked = 0, tokens = 0;
+    for (int q0 = 0; q0 < a.Q; q0 += kThreads) {
+        const int q = q0 + tid;
+        const PlanSeq s = plan_seq(a, q, lens_ok, bits);
+        int grow = usable && s.good && s.need > s.held ? s.need - s.held : 0;
+        bool served = s.good && usable;
+        if (grow > 0 && s.need > a.cols) {
+            bits |= KVD_DEV_TABLE_COLS;
+            grow = 0;
+            served = false;
+        }
+        long long t, lens;
+        const long long run = block_sums(sh, grow, t) + wanted;
+        wanted += t;
+        if (grow > 0 && run > avail) {
+            bits |= KVD_DEV_NO_PAGES;
+            grow = 0;
+            served = false;
+        }
+        int len = s.kept + (served ? s.n : 0);
+        const long long at = block_sums(sh, len, lens) + asked;
+        long long end = at;
+        asked += lens;
+        if (__syncthreads_or(at > 0x7fffffffll)) {  // lengths that 32 bits do not hold
+            if (at > 0x7fffffffll && len > 0) {
+                bits |= KVD_DEV_SEQLENS;
+                len = grow = 0;
+            }
+            end = block_sums(sh, len, lens) + tokens;
+        }
+        if (lead && q < a.Q) a.seq_lens[q + 1] = (int)end;
+        long long takes;
+        const long long mine = block_sums(sh, grow, takes);
+        sh.end[tid] = (int)mine;
+        sh.held[tid] = s.held;
+        __syncthreads();
+        for (long long i = me; i < takes; i += all) {
+            const int k = chunk_find(sh, i), before = k > 0 ? sh.end[k - 1] : 0;
+            a.block_tables[(size_t)(q0 + k) * a.cols + sh.held[k] + (int)(i - before)] =
+                a.free_pages[avail - 1 - taken - i];
+        }
+        taken += takes;
+        tokens += lens;
+        __syncthreads();
+    }
+    if (lead && tid == 0) a.seq_lens[0] = 0;
+    cluster.sync();  // tables and lengths are whole; nobody reads held pages or the count again
+
+    if (lead && tid == 0 && usable) a.free_count[0] = (int)(avail - taken);
+    // pages held, by the thread that reads them
+    for (int q = me; usable && q < a.Q; q += all) {
+        uint32_t none = 0;
+        const PlanSeq s = plan_seq(a, q, true, none);
+        const int len = a.seq_lens[q + 1] - a.seq_lens[q];
+        if (!s.good || len != s.kept + s.n) continue;
+        if (s.need > s.held || (s.need < s.held && give_back)) a.pages_held[q] = s.need;
+    }
+    for (int i = me; i < a.N; i += all) {
+        int lo = usable ? 0 : a.Q, hi = a.Q;  // the first sequence that ends behind i
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (a.new_lens[mid + 1] > i)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        int slot = -1, pos = -1;
+        if (lo < a.Q) {
+            const int s0 = a.new_lens[lo], n = a.new_lens[lo + 1] - s0, kept = a.kept_lens[lo];
+            const int len = a.seq_lens[lo + 1] - a.seq_lens[lo];
+            // refused ones are shorter than that
+            if (kept >= 0 && len == (long long)kept + n) {
+                const int t = kept + (i - s0);
+                const long long p = (long long)t + (a.pos_base ? a.pos_base[lo] : 0);
+                const int page = a.block_tables[(size_t)lo * a.cols + t / a.BS];
+                const long long at = (long long)page * a.BS + t % a.BS;
+                if (page < 0 || at > 0x7fffffffll) {
+                    bits |= KVD_DEV_BLOCK_RANGE;
+                } else if (p < 0 || p > 0x7fffffffll) {
+                    bits |= KVD_DEV_POS_RANGE;
+                } else {
+                    slot = (int)at;
+                    pos = (int)p;
+                }
+            }
+        }
+        a.slots[i] = slot;
+        a.positions[i] = pos;
+    }
+    if (bits) report(a.dev_status, bits);
+}
+
+}  // namespace
+
+cudaError_t launch_plan_pages(const PlanArgs& a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg{};
+    const int ctas = a.Q <= 256 && a.N <= kThreads ? 1 : kMaxCtas;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, plan_pages_kernel, a);
+}
+
+}  // namespace kvd

@@ -1,0 +1,220 @@
+// serving_common.cuh -- what the serving-step kernels share: arguments, the
+// division of shared prefixes over a grid, launchers.
+//
+// Division of kvd_attend_paged_prefix.  A segment is one tile of query rows of
+// one kv head of one group (row = sequence of the group x query head of the kv
+// head) with all key tiles of the group's prefix.  The host knows sizes, not
+// lengths, so every CTA lays all segments' key tiles in one line on the device
+// (a segment counts `lead` places more than it has, laid before its first tile:
+// what starting and finishing it costs) and takes an equal run of it.  A segment
+// that a worker holds whole goes to a row array of its own; of those that it
+// shares there are two at most, one that began before its run (slot 2w) and one
+// that goes on behind it (slot 2w + 1).
+#pragma once
+
+#include "../kvd_device.cuh"
+
+namespace kvd {
+
+constexpr int kServingSMs = 152;
+
+struct PrefixArgs {
+    const void* q;        // [Q, Hq, D]
+    const void* k;        // [NB, BS, Hkv, D]
+    const void* v;
+    const int32_t* prefix_tables;  // [G, pcols]
+    const int32_t* prefix_lens;    // [G]
+    const int32_t* group_lens;     // [G + 1]
+    void* out;            // [Q, Hq, D]
+    float* lse_out;       // [Q, Hq] or null
+    int32_t* dev_status;
+    int Q, G, Hq, Hkv, g, NB, BS, pcols, D;
+    float qscale;         // scale * log2(e)
+    int rows, keys;       // of a tile
+    int lead, workers;
+    int4* meta;           // [Q + 1] first place, row tiles, key tiles, place in the group; the line
+    float* part_lse;      // [2 * workers, rows] log2 units
+    float* part_o;        // [2 * workers, rows, D], normalised
+    float* whole_lse;     // [Q * Hq]
+    float* whole_o;       // [Q * Hq, D]
+    // the sequences' own keys: partial rows of the paged attention (natural log)
+    const float* own_lse; // [Q * Hq, S]
+    const float* own_o;   // [Q * Hq, S, D]
+    int S;
+    uint32_t* counters;   // of that attention: zero before it starts
+};
+
+constexpr int kMaxGroups = 1024;
+
+// Groups of a call, in shared memory.
+struct PrefixGroups {
+    int start[kMaxGroups + 1];  // first sequence
+    int base[kMaxGroups + 1];   // first place of the line
+    int keys[kMaxGroups];       // of the prefix
+    __device__ __forceinline__ int sequences(int i) const { return start[i + 1] - start[i]; }
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// The largest i < n with x[i] <= v (x ascending, x[0] <= v).
+__device__ __forceinline__ int last_not_above(const int* x, int n, int v) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (x[mid] <= v)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// One worker's run [first, first + n) of the line: worker w takes
+// [floor(w tot / W), floor((w + 1) tot / W)).
+struct PrefixRuns {
+    int tot, W;
+    __device__ __forceinline__ PrefixRuns(int tot_, int workers) : tot(tot_) {
+        W = max(1, min(workers, tot));
+    }
+    __device__ __forceinline__ int start(int w) const { return (int)((long long)w * tot / W); }
+    __device__ __forceinline__ int worker_of(int place) const {
+        return (int)((((long long)place + 1) * W - 1) / tot);
+    }
+};
+
+// By all threads of a CTA: reads and checks the groups, lays out the line, writes this
+// CTA's share of the meta rows; returns the length of the line.
+template <int THREADS>
+__device__ __forceinline__ int prefix_setup(const PrefixArgs& a, PrefixGroups& t) {
+    const int tid = threadIdx.x;
+    uint32_t bits = 0;
+    bool bad = false;
+    for (int i = tid; i <= a.G; i += THREADS) {
+        const int s0 = a.G > 0 ? a.group_lens[i] : 0;
+        t.start[i] = s0;
+        if (i == 0 && s0 != 0) bad = true;
+        if (i == a.G) continue;
+        const int s1 = a.group_lens[i + 1];
+        bad |= s0 < 0 || s1 < s0 || s1 > a.Q;
+        int n = a.prefix_lens[i];
+        if (n < 0) {
+            bits |= KVD_DEV_SEQLENS;
+            n = 0;
+        } else if (n > 0 && (n - 1) / a.BS >= a.pcols) {
+            bits |= KVD_DEV_TABLE_COLS;
+            n = 0;
+        }
+        t.keys[i] = n;
+    }
+    if (bad) bits |= KVD_DEV_SEQLENS;
+    if (bits && blockIdx.x == 0) report(a.dev_status, bits);
+    bad = __syncthreads_or(bad);
+    if (tid < 32) {
+        int at = 0;
+        for (int i0 = 0; i0 < a.G; i0 += 32) {
+            const int i = i0 + tid;
+            int c = 0;
+            if (i < a.G && !bad) {
+                const int kt = ceil_div(t.keys[i], a.keys);
+                c = kt > 0 ? a.Hkv * ceil_div(t.sequences(i) * a.g, a.rows) * (kt + a.lead) : 0;
+            }
+            int inc = c;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, inc, d);
+                if (tid >= d) inc += o;
+            }
+            if (i < a.G) t.base[i] = at + inc - c;
+            at += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (tid == 0) t.base[a.G] = at;
+    }
+    __syncthreads();
+    const int tot = t.base[a.G];
+    for (int q = blockIdx.x * THREADS + tid; q <= a.Q; q += gridDim.x * THREADS) {
+        int4 m = make_int4(0, 0, 0, 0);
+        if (q == a.Q) {
+            m.x = tot;
+        } else if (!bad && a.G > 0 && q < t.start[a.G]) {
+            const int i = last_not_above(t.start, a.G, q);
+            m = make_int4(t.base[i], ceil_div(t.sequences(i) * a.g, a.rows),
+                          ceil_div(t.keys[i], a.keys), q - t.start[i]);
+        }
+        a.meta[q] = m;
+    }
+    if (blockIdx.x == 0 && tid < 2) a.counters[tid] = 0;
+    return tot;
+}
+
+// The piece of a segment that a run holds.
+struct PrefixPiece {
+    int group, head, tile;  // tile: of the group's query rows
+    int k0, k1;             // key tiles
+    int slot;               // -1: the whole segment
+    int next;               // the place behind it
+};
+
+// The piece at place p of the run [lo, hi) (p >= lo).
+__device__ __forceinline__ PrefixPiece prefix_piece(const PrefixArgs& a, const PrefixGroups& t,
+                                                    int w, int lo, int hi, int p) {
+    PrefixPiece s;
+    // the last group that starts at or before p: empty ones have no places
+    s.group = last_not_above(t.base, a.G, p);
+    const int kt = ceil_div(t.keys[s.group], a.keys), span = kt + a.lead;
+    const int tiles = ceil_div(t.sequences(s.group) * a.g, a.rows);
+    const int seg = (p - t.base[s.group]) / span, first = t.base[s.group] + seg * span;
+    s.head = seg / tiles;
+    s.tile = seg - s.head * tiles;
+    s.k0 = max(0, lo - first - a.lead);
+    s.k1 = min(kt, hi - first - a.lead);
+    s.next = first + span;
+    const int tile0 = first + a.lead;
+    s.slot = s.k0 == 0 && s.k1 == kt ? -1 : 2 * w + (tile0 >= lo ? 1 : 0);
+    return s;
+}
+
+cudaError_t launch_prefix_simt(const PrefixArgs& a, kvd_dtype dt, cudaStream_t stream);
+cudaError_t launch_prefix_combine(const PrefixArgs& a, kvd_dtype dt, cudaStream_t stream);
+
+struct PlanArgs {
+    int32_t *block_tables, *pages_held, *free_pages, *free_count;
+    const int32_t *kept_lens, *new_lens, *pos_base;
+    int32_t *seq_lens, *slots, *positions;
+    int32_t* dev_status;
+    int Q, N, BS, cols, F;
+};
+cudaError_t launch_plan_pages(const PlanArgs& a, cudaStream_t stream);
+
+struct RotateArgs {
+    const void* x;            // [N, Hq + 2 Hkv, D]
+    const void* q_weight;     // [D] or null
+    const void* k_weight;
+    const double* freqs;      // [Dr / 2]
+    const int32_t* positions; // [N]
+    const int32_t* slots;     // [N]
+    void* q_out;              // [N, Hq, D]
+    void* key_cache;
+    void* value_cache;
+    int32_t* dev_status;
+    int N, Hq, Hkv, D, Dr;
+    long long rows;           // NB * BS
+    float stretch, eps;
+};
+cudaError_t launch_rotate(const RotateArgs& a, bool interleaved, kvd_dtype dt, cudaStream_t stream);
+
+struct SampleArgs {
+    const void* logits;       // [R, V]
+    const float* temperature; // [R] or null
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    const float* u;           // [R], tokens only
+    int32_t* tokens;          // [R], or null: probabilities
+    void* probs;              // [R, V]
+    int32_t* dev_status;
+    int R, V;
+    bool probs_bf16;
+};
+cudaError_t launch_sample(const SampleArgs& a, kvd_dtype dt, cudaStream_t stream);
+
+}  // namespace kvd

@@ -33,9 +33,12 @@ DEV_TIMEOUT = 32
 DEV_POINTER = 64
 DEV_TOKEN_RANGE = 128
 DEV_PROBS = 256
+DEV_NO_PAGES = 512
+DEV_PARAM = 1024
 
 # Entry points of include/kvd.h with their argument types.
 _vp, _sz, _i, _f = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
+_d = ctypes.c_double
 SIGNATURES = {
     "kvd_append": ([_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp], _i),
     "kvd_copy_prefix": ([_vp, _vp, _vp, _vp, _vp, _vp] + [_i] * 7 + [_vp, _vp], _i),
@@ -95,6 +98,14 @@ SIGNATURES = {
     "kvd_attend_latent": ([_vp] * 9 + [_i] * 8 + [_f, _i, _vp, _sz, _vp, _vp], _i),
     "kvd_attend_expanded": ([_vp] * 7 + [_i] * 7 + [_f, _i, _i, _vp, _vp], _i),
     "kvd_verify_drafts": ([_vp] * 8 + [_i] * 4 + [_vp, _vp], _i),
+    "kvd_plan_pages": ([_vp] * 10 + [_i] * 5 + [_vp, _vp], _i),
+    "kvd_rotary_freqs": ([_vp, _i, _d, _i, _d, _d, _d, _d], _i),
+    "kvd_rotate": ([_vp] * 5 + [_i] * 5 + [_f, _f, _i, _vp, _vp], _i),
+    "kvd_rotate_append_paged": ([_vp] * 9 + [_i] * 8 + [_f, _f, _i, _vp, _vp], _i),
+    "kvd_attend_paged_prefix_workspace_bytes": ([_i] * 9, _sz),
+    "kvd_attend_paged_prefix": ([_vp] * 11 + [_i] * 9 + [_f, _i, _vp, _sz, _vp, _vp], _i),
+    "kvd_sample": ([_vp] * 7 + [_i] * 3 + [_vp, _vp], _i),
+    "kvd_filter_probs": ([_vp] * 6 + [_i] * 4 + [_vp, _vp], _i),
     "kvd_status_string": ([_i], ctypes.c_char_p),
     "kvd_last_error": ([], ctypes.c_char_p),
     "kvd_version": ([], _i),
@@ -164,7 +175,8 @@ def status_tensor(device=None):
 # the KVD_DEV_* bits of kvd.h
 DEV_BITS = {1: "KVD_DEV_POS_RANGE", 2: "KVD_DEV_BLOCK_RANGE", 4: "KVD_DEV_TABLE_COLS",
             8: "KVD_DEV_SEQLENS", 16: "KVD_DEV_SEQ_OFFSET", 32: "KVD_DEV_TIMEOUT",
-            64: "KVD_DEV_POINTER", 128: "KVD_DEV_TOKEN_RANGE", 256: "KVD_DEV_PROBS"}
+            64: "KVD_DEV_POINTER", 128: "KVD_DEV_TOKEN_RANGE", 256: "KVD_DEV_PROBS",
+            512: "KVD_DEV_NO_PAGES", 1024: "KVD_DEV_PARAM"}
 
 
 class KvdDeviceError(RuntimeError):
@@ -1075,7 +1087,9 @@ def _bind():
             raise RuntimeError(f"{path} not found or not loadable: {_build.binding_error()}") from e
         m.bind(_check, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
             "kvd_append_latent", "kvd_attend_latent_workspace_bytes", "kvd_attend_latent",
-            "kvd_attend_expanded", "kvd_verify_drafts")))
+            "kvd_attend_expanded", "kvd_verify_drafts", "kvd_plan_pages", "kvd_rotate",
+            "kvd_rotate_append_paged", "kvd_attend_paged_prefix_workspace_bytes",
+            "kvd_attend_paged_prefix", "kvd_sample", "kvd_filter_probs")))
         _binding = m
     return _binding
 
@@ -1143,3 +1157,104 @@ def verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, n
     """
     return (_binding or _bind()).verify_drafts(target_probs, draft_probs, draft_tokens, u_accept,
                                                u_sample, num_drafts, tokens, accepted, dev_status)
+
+
+# ------------------------------------------------------------------ the serving step
+
+def plan_pages(block_tables, pages_held, free_pages, free_count, kept_lens, new_lens, block_size,
+               num_tokens, pos_base=None, seq_lens=None, slots=None, positions=None,
+               dev_status=None):
+    """kvd_plan_pages: pages for the step's new tokens, from the requests' lengths.
+
+    block_tables [Q, cols], pages_held [Q], free_pages [F], free_count [1]: the
+    state of the paged cache, updated in place; kept_lens [Q] (tokens in the cache
+    that stay), new_lens [Q + 1] cumsum, pos_base [Q] or None, int32;
+    ``num_tokens`` is N, the length of the packed new tokens (padding included).
+    Returns seq_lens [Q + 1], slots [N] and positions [N] int32 (-1: no place).
+    """
+    return (_binding or _bind()).plan_pages(block_tables, pages_held, free_pages, free_count,
+                                            kept_lens, new_lens, block_size, num_tokens, pos_base,
+                                            seq_lens, slots, positions, dev_status)
+
+
+ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "parts": 3}  # kvd_rope_scaling
+
+
+def rotary_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, trained=4096.0, fast=32.0,
+                 slow=1.0, device=None):
+    """kvd_rotary_freqs: the frequencies of ``rotary_dim`` rotated dims in radians a
+    position, float64 [rotary_dim / 2] on ``device`` (the current CUDA device).
+
+    scaling None, "linear" (divided by ``factor``), "base" (of a larger base) or
+    "parts" (those with more than ``fast`` turns over the ``trained`` length stay,
+    those with fewer than ``slow`` are divided, a mixture between)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"rotary_freqs: scaling {scaling!r} (None, 'linear', 'base' or 'parts')")
+    freqs = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.float64)
+    _check("kvd_rotary_freqs", load().kvd_rotary_freqs(
+        _ptr(freqs), int(rotary_dim), float(base), ROPE_SCALINGS[scaling], float(factor),
+        float(trained), float(fast), float(slow)))
+    return freqs.to(device or "cuda")
+
+
+def rotate(x, positions, freqs, weight=None, eps=1e-6, interleaved=False, rotary_scale=1.0,
+           out=None, dev_status=None):
+    """kvd_rotate: the norm (with a ``weight`` [D]) and rotation by position of every
+    head of x [N, H, D]; positions [N] int32, freqs [Dr / 2] float64.  The first Dr
+    dims are rotated, in halves or in interleaved pairs; cos and sin are multiplied by
+    ``rotary_scale``.  Returns out [N, H, D], which may be x itself."""
+    return (_binding or _bind()).rotate(x, positions, freqs, weight, eps, interleaved, rotary_scale,
+                                        out, dev_status)
+
+
+def rotate_append_paged(qkv, key_cache, value_cache, slots, positions, freqs, q_weight=None,
+                        k_weight=None, eps=1e-6, interleaved=False, rotary_scale=1.0, out=None,
+                        dev_status=None):
+    """kvd_rotate_append_paged: norm and rotation of the queries and keys of a fused
+    projection qkv [N, Hq + 2 Hkv, D], keys and values into row slots[n] of the paged
+    caches [NB, BS, Hkv, D].  Returns the queries [N, Hq, D]."""
+    return (_binding or _bind()).rotate_append_paged(qkv, key_cache, value_cache, slots, positions,
+                                                     freqs, q_weight, k_weight, eps, interleaved,
+                                                     rotary_scale, out, dev_status)
+
+
+def attend_paged_prefix_workspace_bytes(Q, G, Hq, Hkv, BS, pcols, cols, D, dtype=torch.bfloat16):
+    return load().kvd_attend_paged_prefix_workspace_bytes(
+        Q, G, Hq, Hkv, BS, pcols, cols, D, BF16 if dtype == torch.bfloat16 else F32)
+
+
+def attend_paged_prefix(q, key_cache, value_cache, prefix_tables, prefix_lens, group_lens,
+                        block_tables, seq_lens, seq_offset=None, scale=None, out=None, lse=None,
+                        workspace=None, dev_status=None):
+    """kvd_attend_paged_prefix: decode attention of groups of sequences, each group
+    behind a prefix that is kept, and read, once.
+
+    q [Q, Hq, D]; caches [NB, BS, Hkv, D]; prefix_tables [G, pcols], prefix_lens [G],
+    group_lens [G + 1] cumsum of the groups' sequences; block_tables [Q, cols],
+    seq_lens [Q + 1] cumsum, seq_offset [Q] or None: the sequences' own tokens; all
+    int32.  ``scale`` defaults to 1/sqrt(D).  Returns out [Q, Hq, D]; fills ``lse``
+    [Q, Hq] fp32 if given.
+    """
+    if scale is None:
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    return (_binding or _bind()).attend_paged_prefix(q, key_cache, value_cache, prefix_tables,
+                                                     prefix_lens, group_lens, block_tables,
+                                                     seq_lens, seq_offset, scale, out, lse,
+                                                     workspace, dev_status)
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None,
+           dev_status=None):
+    """kvd_sample: a token a row of logits [R, V] by the random numbers u [R], after
+    temperature, top-k, top-p and min-p (a value a row, [R] float32, top_k int32, or
+    None).  Returns tokens [R] int32."""
+    return (_binding or _bind()).sample(logits, u, temperature, top_k, top_p, min_p, tokens,
+                                        dev_status)
+
+
+def filter_probs(logits, temperature=None, top_k=None, top_p=None, min_p=None, out=None,
+                 dev_status=None):
+    """kvd_filter_probs: the distributions that ``sample`` draws from, [R, V] of the
+    logits' type or of that of ``out`` (bf16 or fp32), as verify_drafts takes them."""
+    return (_binding or _bind()).filter_probs(logits, temperature, top_k, top_p, min_p, out,
+                                              dev_status)

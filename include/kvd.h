@@ -81,6 +81,8 @@ typedef enum { KVD_BF16 = 0, KVD_F32 = 1 } kvd_dtype;
 #define KVD_DEV_POINTER 64u      /* a pointer read from a device pointer array is null or misaligned */
 #define KVD_DEV_TOKEN_RANGE 128u /* drafted token outside [0, V) */
 #define KVD_DEV_PROBS 256u       /* no finite positive weight to sample a token from */
+#define KVD_DEV_NO_PAGES 512u    /* the free list has too few pages, or no room for those given back */
+#define KVD_DEV_PARAM 1024u      /* a row's sampling parameter is NaN or out of range */
 
 /*
  * kvd_append -- [NPU] Part 2, update_kvcache_for: for every batch entry b
@@ -769,6 +771,190 @@ kvd_status kvd_verify_drafts(const void* target_probs, const void* draft_probs,
                              const float* u_sample, const int32_t* num_drafts, int32_t* tokens,
                              int32_t* accepted, int Q, int T, int V, kvd_dtype dtype,
                              int32_t* dev_status, kvd_stream_t stream);
+
+/*
+ * The serving step around the paged cache: pages and slots for the step's new
+ * tokens (kvd_plan_pages), their queries, keys and values normed, rotated and
+ * appended (kvd_rotate_append_paged), decode attention of sequences behind
+ * shared prefixes (kvd_attend_paged_prefix), and the next tokens from the logits
+ * (kvd_sample, or kvd_filter_probs in front of kvd_verify_drafts).
+ */
+
+/*
+ * kvd_plan_pages -- pages, slots and positions from the requests' lengths,
+ * without the host.  Sequence q keeps the kept_lens[q] first tokens that it has
+ * in the cache (fewer than before where drafted tokens were rejected, 0 where a
+ * request is over) and gets new_lens[q + 1] - new_lens[q] new ones; with
+ *   need[q] = ceil((kept + new) / BS)
+ * pages it gives pages back where it holds more and takes some where it holds
+ * fewer:
+ *  - first, all pages given back are pushed onto the free list, the last
+ *    sequence's last column first;
+ *  - then pages are taken from the list's end, the first sequence's first column
+ *    first (so that taking and giving back the same pages leaves the list as it
+ *    was), while they last: a sequence whose pages and those of all sequences
+ *    before it are more than there are gets none (KVD_DEV_NO_PAGES).
+ *   block_tables [Q, cols] int32   columns [0, pages_held[q]) are q's (in/out)
+ *   pages_held   [Q] int32         (in/out)
+ *   free_pages   [F] int32, free_count [1] int32: the first free_count entries
+ *                are free pages (in/out); F: at least all pages of the cache
+ *   kept_lens    [Q] int32;  new_lens [Q + 1] int32, cumsum starting at 0
+ *   pos_base     [Q] int32 or NULL (zeros): the position of q's first token (the
+ *                length of a shared prefix before it)
+ *   seq_lens     [Q + 1] int32 (out): cumsum of kept + new, as the attention
+ *                calls take it
+ *   slots, positions [N] int32 (out): token new_lens[q] + i of the packed new
+ *                tokens is token t = kept + i of q,
+ *                slot = block_tables[q, t / BS] * BS + t % BS, position =
+ *                pos_base[q] + t; both -1 for tokens without a place: those of a
+ *                refused sequence, and padding behind new_lens[Q]
+ * A refused sequence keeps its pages and counts kept_lens[q] tokens: too few
+ * pages left, or need above cols (KVD_DEV_TABLE_COLS).  A bad one is left alone
+ * and counts none: kept_lens negative or more than its pages hold, pages_held
+ * outside [0, cols], or kept + new past 2^31 - 1 (KVD_DEV_POS_RANGE), or an end of
+ * seq_lens past 2^31 - 1, its and those before it counted (KVD_DEV_SEQLENS).  All sequences are refused, and none
+ * gives pages back, by a new_lens that does not start at 0, decreases or passes N
+ * (KVD_DEV_SEQLENS) and by a free_count outside [0, F] (KVD_DEV_POS_RANGE).  Where
+ * the list has no room for all pages given back, none is (KVD_DEV_NO_PAGES).  A
+ * token whose page is negative or whose slot is past 2^31 - 1
+ * (KVD_DEV_BLOCK_RANGE), or whose position is
+ * outside 32 bits (KVD_DEV_POS_RANGE), has no place.  One launch; runs that
+ * change the same tables must be ordered.  Q at most 2^20.
+ */
+kvd_status kvd_plan_pages(int32_t* block_tables, int32_t* pages_held, int32_t* free_pages,
+                          int32_t* free_count, const int32_t* kept_lens, const int32_t* new_lens,
+                          const int32_t* pos_base, int32_t* seq_lens, int32_t* slots,
+                          int32_t* positions, int Q, int N, int BS, int cols, int F,
+                          int32_t* dev_status, kvd_stream_t stream);
+
+/* How rotary frequencies are stretched for contexts longer than the trained one. */
+typedef enum {
+    KVD_ROPE_PLAIN = 0,  /* f_i = base^(-2 i / Dr) */
+    KVD_ROPE_LINEAR = 1, /* f_i / factor: positions brought closer */
+    KVD_ROPE_BASE = 2,   /* base * factor^(Dr / (Dr - 2)) in place of base */
+    KVD_ROPE_PARTS = 3   /* frequencies that make more than `fast` turns over the
+                            `trained` length stay, those below `slow` turns are divided
+                            by factor, a linear mixture by turns between */
+} kvd_rope_scaling;
+
+/*
+ * kvd_rotary_freqs -- the frequencies of Dr rotated dims, in radians a position,
+ * into freqs [Dr / 2], HOST memory; the caller copies them to the device once.
+ * factor > 0 (not used by PLAIN); trained > 0 and fast > slow > 0 for PARTS only.
+ */
+kvd_status kvd_rotary_freqs(double* freqs, int Dr, double base, kvd_rope_scaling scaling,
+                            double factor, double trained, double fast, double slow);
+
+/*
+ * kvd_rotate -- norm and rotation of every head of N tokens:
+ *   y = x * weight / sqrt(mean_D(x^2) + eps)        (y = x without a weight)
+ *   pair i of the first Dr dims, (y_i, y_{i + Dr/2}), or (y_2i, y_{2i+1}) if
+ *   `interleaved`, at position p = positions[n]:
+ *     (a, b) -> (a c - b s, a s + b c),  c, s = rotary_scale * cos, sin(p freqs[i])
+ *   dims at and behind Dr are not rotated (nor scaled).
+ *   x, out [N, H, D] of `dtype` (out may be x), weight [D] of `dtype` or NULL
+ *   freqs [Dr / 2] double, device (NULL with Dr = 0);  positions [N] int32
+ * fp32 arithmetic, one rounding; the angle is taken in 64 bits, so that far
+ * positions lose nothing.  A token at position -1 is left out (its row of out
+ * stays as it was), other negative ones too and set KVD_DEV_POS_RANGE.
+ * D in {64, 128}; Dr a multiple of 16, 0 <= Dr <= D.
+ */
+kvd_status kvd_rotate(const void* x, const void* weight, const double* freqs,
+                      const int32_t* positions, void* out, int N, int H, int D, int Dr,
+                      int interleaved, float rotary_scale, float eps, kvd_dtype dtype,
+                      int32_t* dev_status, kvd_stream_t stream);
+
+/*
+ * kvd_rotate_append_paged -- kvd_rotate of a fused projection's queries and keys,
+ * the keys and the (unchanged) values straight into the paged cache:
+ *   qkv [N, Hq + 2 Hkv, D] of `dtype`: Hq queries, Hkv keys, Hkv values a token
+ *   q_out [N, Hq, D];  key_cache, value_cache [NB, BS, Hkv, D] of `dtype`
+ *   slots [N] int32: the token's row block * BS + slot of the caches, as
+ *   kvd_plan_pages gives it
+ * A token at position -1 is left out altogether; one with slot -1 has its queries
+ * rotated and nothing appended.  Any other negative position, or a slot outside
+ * [-1, NB * BS), counts as -1 and sets KVD_DEV_POS_RANGE or KVD_DEV_BLOCK_RANGE.
+ * Two tokens with one slot leave one of them there.  Otherwise as kvd_rotate.
+ */
+kvd_status kvd_rotate_append_paged(const void* qkv, const void* q_weight, const void* k_weight,
+                                   const double* freqs, const int32_t* positions,
+                                   const int32_t* slots, void* q_out, void* key_cache,
+                                   void* value_cache, int N, int Hq, int Hkv, int NB, int BS,
+                                   int D, int Dr, int interleaved, float rotary_scale, float eps,
+                                   kvd_dtype dtype, int32_t* dev_status, kvd_stream_t stream);
+
+/*
+ * kvd_attend_paged_prefix -- kvd_attend_paged for groups of sequences that share
+ * a prefix, which is kept once and read once a group: the sequences group_lens[i]
+ * <= q < group_lens[i + 1] attend over the first prefix_lens[i] tokens of the
+ * pages prefix_tables[i, :], and then over their own tokens as in
+ * kvd_attend_paged; one softmax over both.  Sequences behind group_lens[G] have
+ * no prefix.
+ *   q [Q, Hq, D], key_cache, value_cache [NB, BS, Hkv, D] of `dtype`
+ *   prefix_tables [G, pcols], prefix_lens [G], group_lens [G + 1] (cumsum of the
+ *   groups' sequences starting at 0) int32, device; NULL with G = 0
+ *   block_tables [Q, cols], seq_lens [Q + 1], seq_offset, out, lse_out, scale as
+ *   for kvd_attend_paged: a sequence's own tokens, none for some
+ * Errors of a sequence's own pages as for kvd_attend_paged (its prefix still
+ * counts).  Prefixes: a negative length (KVD_DEV_SEQLENS) or one past pcols pages
+ * (KVD_DEV_TABLE_COLS) counts as none; an out-of-range block
+ * (KVD_DEV_BLOCK_RANGE) drops its tokens; a group_lens that does not start at 0,
+ * decreases or passes Q leaves every sequence without a prefix (KVD_DEV_SEQLENS).
+ * A query without any key gives out = 0, lse = -inf.  Slots behind a prefix's or
+ * a sequence's end may hold anything (inf, NaN).
+ * Workspace: at least kvd_attend_paged_prefix_workspace_bytes(...) bytes, 256-byte
+ * aligned; its contents do not matter before a call, and calls that may overlap
+ * on the GPU must not share one.  D in {64, 128}; any Hq multiple of Hkv;
+ * G at most 1024.
+ */
+size_t kvd_attend_paged_prefix_workspace_bytes(int Q, int G, int Hq, int Hkv, int BS, int pcols,
+                                               int cols, int D, kvd_dtype dtype);
+kvd_status kvd_attend_paged_prefix(const void* q, const void* key_cache, const void* value_cache,
+                                   const int32_t* prefix_tables, const int32_t* prefix_lens,
+                                   const int32_t* group_lens, const int32_t* block_tables,
+                                   const int32_t* seq_lens, const int32_t* seq_offset, void* out,
+                                   float* lse_out, int Q, int G, int Hq, int Hkv, int NB, int BS,
+                                   int pcols, int cols, int D, float scale, kvd_dtype dtype,
+                                   void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                   kvd_stream_t stream);
+
+/*
+ * kvd_sample -- a token for each row of logits, from given random numbers.  With
+ * T = temperature[r] and w_v = exp((l_v - max l) / T), logits in falling order
+ * (equal ones by index, the lowest first):
+ *   top-k:  the first top_k[r] tokens stay (all if top_k[r] <= 0 or > V);
+ *   top-p:  of these, a token stays while the sum of the weights before it is
+ *           below top_p[r] times their sum (all if top_p[r] >= 1);
+ *   min-p:  of these, the tokens with w_v >= min_p[r] stay (all if min_p[r] <= 0;
+ *           above 1 counts as 1);
+ * the first always stays.  T = 0 keeps the first alone.  tokens[r] is the smallest
+ * v whose running sum of the weights that stay, in index order, is above u[r] times
+ * their sum.
+ *   logits [R, V] of `dtype`;  temperature [R], top_p [R], min_p [R] float and
+ *   top_k [R] int32, device, or NULL (1, all, all, all);  u [R] float in [0, 1)
+ *   tokens [R] int32
+ * NaN logits count as -inf; among infinite ones the weight is shared alike.
+ * Weights are taken to about 2^-38 of themselves and summed as whole multiples of
+ * 2^-43 of the largest, in any order to the same sum: only a draw or a top-p border
+ * closer than that to a token's border can differ from one in 64 bits.
+ * A row without a logit above -inf gives -1 (KVD_DEV_PROBS); a NaN, a temperature
+ * below 0 or infinite, or u outside [0, 1) gives -1 (KVD_DEV_PARAM).
+ * V at most 2^20.
+ */
+kvd_status kvd_sample(const void* logits, const float* temperature, const int32_t* top_k,
+                      const float* top_p, const float* min_p, const float* u, int32_t* tokens,
+                      int R, int V, kvd_dtype dtype, int32_t* dev_status, kvd_stream_t stream);
+
+/*
+ * kvd_filter_probs -- the distributions that kvd_sample draws from: probs[r, v] =
+ * w_v over the sum of the weights that stay, 0 for the others, as kvd_verify_drafts
+ * takes them.  probs [R, V] of probs_dtype, not overlapping the logits; rows that
+ * kvd_sample refuses are zero.  Otherwise as kvd_sample.
+ */
+kvd_status kvd_filter_probs(const void* logits, const float* temperature, const int32_t* top_k,
+                            const float* top_p, const float* min_p, void* probs, int R, int V,
+                            kvd_dtype dtype, kvd_dtype probs_dtype, int32_t* dev_status,
+                            kvd_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
 const char* kvd_status_string(kvd_status status);
