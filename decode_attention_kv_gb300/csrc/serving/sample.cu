@@ -1,247 +1,838 @@
 // sample.cu -- kvd_sample and kvd_filter_probs.
 //
 // w_v = exp((l_v - max) / T).  In falling order of l (ties by index) temperature,
-// top-k, top-p and min-p each keep a beginning of the row, so what is kept is a
-// smallest logit and, where equal logits are cut, a last index.
+// top-k, top-p and min-p each keep a beginning of the row, so what is kept is a cut: a
+// smallest logit and, among those equal to it, a last index.
+//
+// A cluster of 1 to 8 CTAs takes a row, a contiguous share a CTA and of that a warp.
+// The largest logit first; then a histogram of 512 bins over the logits that weigh more
+// than 2^-24 of it (linear in l, so that a bin's weights differ by a twentieth of a
+// factor of two), of counts for top-k and of counts and weights for top-p.  Every CTA
+// adds up all CTAs' bins and finds the one that the cut falls into; its elements (for a
+// small k all above it too) go to the first CTA, which sorts them and takes the cut by
+// their running sums.  Bins that hold more than a list (flat rows, ties) are divided
+// again, by the bits of the logits' order, until a list takes them or one value is left,
+// whose ties are counted through in index order.
+//
+// Whole numbers decide, so sums must not depend on an order and have to agree with sums
+// in 64 bits: a weight is computed in two fp32 words (a table of sixteenths of a factor
+// of two and a polynomial; right to 2^-34 of the largest weight, and a small one to 2^-29
+// of itself) and counted in whole multiples of 2^-42.
+#include <cooperative_groups.h>
+
 #include "../kvd_internal.h"
 #include "serving_common.cuh"
 
 namespace kvd {
 namespace {
 
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxCtas = 8;
+constexpr int kBins = kThreads;  // a thread a bin when they are added up
+constexpr int kList = 2048;      // elements that one CTA sorts
+constexpr int kBatch = 16;       // elements that a lane loads at once
+constexpr unsigned long long kOne = 1ull << 42;  // the weight 1
+constexpr float kMagic = 12582912.f;             // 1.5 * 2^23: adding it rounds to whole numbers
 
 __device__ __forceinline__ float as_logit(float x) { return x; }
 __device__ __forceinline__ float as_logit(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// A number that rises with the logit; NaN counts as the lowest.
+// A number that rises with the logit; NaN counts as -inf.
+constexpr uint32_t kLowest = 0x007fffffu;
 __device__ __forceinline__ uint32_t order_of(float x) {
-    if (!(x == x)) return 0x007fffffu;  // that of -inf
-    const uint32_t b = __float_as_uint(x + 0.f);
+    if (!(x == x)) return kLowest;
+    const uint32_t b = __float_as_uint(x + 0.f);  // -0 as 0
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float logit_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-__device__ __forceinline__ double weight_of(float x, float top, double inv_t) {
-    if (x == top) return 1.0;
-    return exp(((double)x - (double)top) * inv_t);
-}
-constexpr double kOne = 8796093022208.0;  // 2^43: weights as whole numbers, summed in any order
-__device__ __forceinline__ unsigned long long fixed_of(double w) {
-    return (unsigned long long)(w * kOne + 0.5);
+// 2^(j / 16) in two words, j = 0 .. 15 (correctly rounded; the second is what the first
+// leaves).
+struct Table {
+    float2 v[16];
+};
+
+// What the weights of a row go by.
+struct Scale {
+    float top;         // the largest logit
+    float c, c_low;    // 16 log2(e) / T in two words
+};
+
+// 2^(f / 16) - 1 = k1 f + k2 f^2 + ..., k1 = ln 2 / 16
+struct Weight {
+    float hi, lo;  // the weight is their sum
+};
+
+__device__ __forceinline__ Weight weight_of(const Table& t, const Scale& s, float x) {
+    Weight w{1.f, 0.f};
+    if (x == s.top) return w;
+    // x - top in two words (Knuth's two-sum)
+    const float d = __fsub_rn(x, s.top), b = __fsub_rn(d, x);
+    const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(s.top, b));
+    // y = 16 log2 of the weight, in two words
+    const float y = __fmul_rn(d, s.c);
+    if (!(y > -2000.f)) {  // below 2^-125, or no logit
+        w.hi = y < 0.f ? exp2f(y * 0.0625f) : 0.f;
+        return w;
+    }
+    // (Every operation rounds as written: all passes must get the same weight.)
+    const float yl = __fmaf_rn(dl, s.c, __fmaf_rn(d, s.c_low, __fmaf_rn(d, s.c, -y)));
+    const float r = __fadd_rn(y, kMagic);
+    const int n = __float_as_int(r) - __float_as_int(kMagic);
+    const float f = __fsub_rn(y, __fsub_rn(r, kMagic));  // exact, |f| <= 1/2
+    constexpr double kLn = 0.69314718055994530942 / 16.0;
+    constexpr float k1 = (float)kLn, k1l = (float)(kLn - (double)k1), k2 = (float)(kLn * kLn / 2),
+                    k3 = (float)(kLn * kLn * kLn / 6), k4 = (float)(kLn * kLn * kLn * kLn / 24);
+    // 2^((f + yl) / 16) - 1 in two words: the first order of f exactly, that of yl with
+    // the factor 2^(f / 16), higher ones in one word
+    const float p = __fmul_rn(k1, f), pl = __fmul_rn(k1, yl);
+    const float rest = __fmaf_rn(
+        __fmul_rn(f, f), __fmaf_rn(f, __fmaf_rn(f, k4, k3), k2),
+        __fadd_rn(__fmaf_rn(pl, p, pl), __fmaf_rn(k1l, f, __fmaf_rn(k1, f, -p))));
+    const float q = __fadd_rn(p, rest), ql = __fsub_rn(rest, __fsub_rn(q, p));
+    const float2 e = t.v[n & 15];
+    const float m = __fmul_rn(e.x, q);
+    const float hi = __fadd_rn(e.x, m);
+    const float lo = __fadd_rn(__fadd_rn(__fmaf_rn(e.x, ql, __fmaf_rn(e.x, q, -m)), __fmaf_rn(e.y, q, e.y)),
+                               __fsub_rn(m, __fsub_rn(hi, e.x)));
+    const float scale = __int_as_float(((n >> 4) + 127) << 23);
+    w.hi = __fmul_rn(hi, scale);
+    w.lo = __fmul_rn(lo, scale);
+    return w;
 }
 
-struct SampleShared {
-    unsigned long long mass[256];
-    unsigned int count[256];
-    unsigned long long warp_sum[kWarps];
-    uint32_t warp_max[kWarps];
-    unsigned long long carry;
-    uint32_t prefix;
-    unsigned int left;
+// In multiples of 2^-42 (a float in [4, 8) is a multiple of 2^-21).
+__device__ __forceinline__ unsigned long long fixed_of(const Weight& w) {
+    const float a = __fadd_rn(w.hi, 6.f);
+    const float rest = __fadd_rn(__fsub_rn(w.hi, __fsub_rn(a, 6.f)), w.lo);
+    const float b = __fmaf_rn(rest, 2097152.f, 6.f);
+    return ((unsigned long long)(__float_as_uint(a) - __float_as_uint(6.f)) << 21) +
+           (unsigned long long)(long long)(__float_as_int(b) - __float_as_int(6.f));
+}
+
+// A beginning of the row: order above `key`, or equal to it and an index up to `last`.
+struct Cut {
+    uint32_t key;
+    int last;
+    __device__ __forceinline__ bool keeps(uint32_t o, int i) const {
+        return o > key || (o == key && i <= last);
+    }
+};
+
+struct Shared {
+    Table table;
+    uint32_t hist[4][kBins];  // counts; weights in three words of 14 bits
+    unsigned long long list[kList];   // of this CTA; then sorted by the first
+    unsigned long long merged[kList]; // of all CTAs, at the first
+    unsigned long long warp_sum[kWarps], part_sum[kWarps];
+    unsigned long long cta_sum[kMaxCtas];
+    unsigned long long cta_top[kMaxCtas];
+    uint32_t cta_low[kMaxCtas];
+    uint32_t cta_lo[kMaxCtas], cta_hi[kMaxCtas];
+    unsigned int cta_ties[kMaxCtas];
+    Scale scale;
+    Cut cut;
+    unsigned long long before_mass;
+    unsigned int n_list, n_merged, base;
+    unsigned int bin, in_bin, before_count;
     int found;
 };
 
-__device__ __forceinline__ unsigned long long block_sum(SampleShared& sh, unsigned long long x) {
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    cluster_arrive();
+    cluster_wait();
+}
+
+// Inclusive sums in thread order.
+__device__ __forceinline__ unsigned long long block_sums(Shared& sh, unsigned long long x,
+                                                         unsigned long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const unsigned long long o = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += o;
+    }
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh.warp_sum[threadIdx.x >> 5] = x;
+    if (lane == 31) sh.warp_sum[warp] = x;
     __syncthreads();
-    x = sh.warp_sum[threadIdx.x & 31];
+    unsigned long long s = lane < kWarps ? sh.warp_sum[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < kWarps; d <<= 1) {
+        const unsigned long long o = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += o;
+    }
+    total = __shfl_sync(0xffffffffu, s, kWarps - 1);
+    const unsigned long long before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+    return x + (warp > 0 ? before : 0);
+}
+__device__ __forceinline__ unsigned long long warp_total(unsigned long long x) {
+#pragma unroll
     for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
     return x;
 }
 
-// Exclusive sums in thread order.
-__device__ __forceinline__ unsigned long long block_before(SampleShared& sh, unsigned long long x,
-                                                           unsigned long long& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned long long inc = x;
-    for (int d = 1; d < 32; d <<= 1) {
-        const unsigned long long o = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += o;
+// A row's elements as 16-byte vectors from the boundary at or before its start: vector v
+// holds the elements v * VEC - shift and so on; the outer ones are loaded one by one.
+template <typename Elem>
+struct Row {
+    static constexpr int VEC = 16 / (int)sizeof(Elem);
+    const Elem* p;
+    int V, shift, vectors;
+
+    __device__ __forceinline__ Row(const Elem* base, int V_) : p(base), V(V_) {
+        shift = (int)(reinterpret_cast<uintptr_t>(base) / sizeof(Elem) % VEC);
+        vectors = (shift + V + VEC - 1) / VEC;
     }
-    __syncthreads();
-    if (lane == 31) sh.warp_sum[warp] = inc;
-    __syncthreads();
-    unsigned long long s = sh.warp_sum[lane];
-    for (int d = 1; d < 32; d <<= 1) {
-        const unsigned long long o = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d) s += o;
+    __device__ __forceinline__ bool has(int i) const { return (unsigned)i < (unsigned)V; }
+    __device__ __forceinline__ uint4 load(int v, int end) const {
+        const int i = v * VEC - shift;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (v < end) {
+            if (i >= 0 && i + VEC <= V) {
+                w = *reinterpret_cast<const uint4*>(p + i);
+            } else {
+                Elem* e = reinterpret_cast<Elem*>(&w);
+#pragma unroll
+                for (int z = 0; z < VEC; ++z)
+                    if (has(i + z)) e[z] = p[i + z];
+            }
+        }
+        return w;
     }
-    total = __shfl_sync(0xffffffffu, s, 31);
-    const unsigned long long before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
-    return inc - x + (warp > 0 ? before : 0);
+    // f(index, logit) for the row's elements in the vectors [lo, hi), by one warp.
+    template <typename F>
+    __device__ __forceinline__ void each(int lo, int hi, F f) const {
+        constexpr int N = kBatch / VEC;
+        for (int v0 = lo + (int)(threadIdx.x & 31); v0 < hi; v0 += 32 * N) {
+            uint4 w[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) w[k] = load(v0 + 32 * k, hi);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const Elem* e = reinterpret_cast<const Elem*>(&w[k]);
+                const int i = (v0 + 32 * k) * VEC - shift;
+                if (v0 + 32 * k < hi) {
+#pragma unroll
+                    for (int z = 0; z < VEC; ++z)
+                        if (has(i + z)) f(i + z, as_logit(e[z]));
+                }
+            }
+        }
+    }
+};
+
+// n <= kList numbers of sh.merged in falling order; all threads.
+__device__ __forceinline__ void sort_falling(Shared& sh, int n) {
+    const int tid = threadIdx.x;
+    int size = 32;
+    while (size < n) size <<= 1;
+    for (int i = n + tid; i < size; i += kThreads) sh.merged[i] = 0;
+    __syncthreads();
+    for (int k = 2; k <= size; k <<= 1)
+        for (int j = k >> 1; j; j >>= 1) {
+            for (int t = tid; t < size / 2; t += kThreads) {
+                const int a = 2 * t - (t & (j - 1)), b = a + j;
+                const unsigned long long x = sh.merged[a], y = sh.merged[b];
+                if ((x < y) == ((a & k) == 0)) {
+                    sh.merged[a] = y;
+                    sh.merged[b] = x;
+                }
+            }
+            __syncthreads();
+        }
 }
 
 template <typename Elem>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a) {
-    __shared__ SampleShared sh;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int tid = threadIdx.x, row = blockIdx.x, V = a.V;
-    const Elem* l = static_cast<const Elem*>(a.logits) + (size_t)row * V;
-    auto put = [&](int i, float p) {
-        if (a.probs_bf16)
-            static_cast<__nv_bfloat16*>(a.probs)[(size_t)row * V + i] = __float2bfloat16_rn(p);
-        else
-            static_cast<float*>(a.probs)[(size_t)row * V + i] = p;
-    };
-    uint32_t top = 0;
-    for (int i = tid; i < V; i += kThreads) top = max(top, order_of(as_logit(l[i])));
-    top = __reduce_max_sync(0xffffffffu, top);
-    if ((tid & 31) == 0) sh.warp_max[tid >> 5] = top;
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, sh.warp_max[tid & 31]);
-    const float best = logit_of(top);
-    const float T = a.temperature ? a.temperature[row] : 1.f;
-    const float p = a.top_p ? a.top_p[row] : 1.f, mp = a.min_p ? fminf(a.min_p[row], 1.f) : 0.f;
-    const float u = a.u ? a.u[row] : 0.f;
-    const bool params = T >= 0.f && T < INFINITY && p == p &&
-                        !(a.min_p && a.min_p[row] != a.min_p[row]) && u >= 0.f && u < 1.f;
-    if (!params || best == -INFINITY) {
-        if (tid == 0) report(a.dev_status, params ? KVD_DEV_PROBS : KVD_DEV_PARAM);
-        if (a.tokens) {
-            if (tid == 0) a.tokens[row] = -1;
-        } else {
-            for (int i = tid; i < V; i += kThreads) put(i, 0.f);
-        }
-        return;
-    }
-    const double inv_t = 1.0 / (double)T;
-    const bool greedy = T == 0.f;
-    uint32_t cut = 0;              // smallest order that is kept
-    unsigned int ties = 0xffffffffu;  // how many of that order
-    auto counts = [&](uint32_t k) { return k >= cut; };
-    // top-k: the k-th largest, eight bits at a time
-    const int k = greedy ? 1 : a.top_k ? a.top_k[row] : 0;
-    if (k > 0 && k < V) {
-        uint32_t prefix = 0;
-        unsigned int left = k;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            __syncthreads();
-            if (tid < 256) sh.count[tid] = 0;
-            __syncthreads();
-            for (int i = tid; i < V; i += kThreads) {
-                const uint32_t o = order_of(as_logit(l[i]));
-                if (shift == 24 || (o >> (shift + 8)) == prefix)
-                    atomicAdd(&sh.count[(o >> shift) & 255u], 1u);
+struct Picker {
+    Shared& sh;
+    const Row<Elem>& row;
+    cg::cluster_group& cluster;
+    int rank, ctas, wlo, whi;  // of this warp's vectors
+    uint32_t low;              // the smallest order above kLowest, or the largest
+
+    // Gathers the elements that `take` accepts at the first CTA; n of them in all.
+    template <typename F>
+    __device__ __forceinline__ void gather(F take) {
+        const int tid = threadIdx.x;
+        if (tid == 0) sh.n_list = 0;
+        if (rank == 0 && tid == 0) sh.n_merged = 0;
+        __syncthreads();
+        cluster_sync();
+        row.each(wlo, whi, [&](int i, float x) {
+            const uint32_t o = order_of(x);
+            if (take(i, x, o)) {
+                const unsigned int at = atomicAdd(&sh.n_list, 1u);
+                if (at < kList) sh.list[at] = (unsigned long long)o << 32 | (0xffffffffu - (uint32_t)i);
             }
-            __syncthreads();
-            if (tid == 0) {
-                int b = 255;
-                while (sh.count[b] < left) left -= sh.count[b--];
-                sh.prefix = prefix << 8 | (uint32_t)b;
-                sh.left = left;
-            }
-            __syncthreads();
-            prefix = sh.prefix;
-            left = sh.left;
-        }
-        cut = prefix;
-        ties = left;
+        });
+        __syncthreads();
+        const unsigned int n = min(sh.n_list, (unsigned int)kList);
+        if (tid == 0 && n > 0) sh.base = atomicAdd(cluster.map_shared_rank(&sh.n_merged, 0), n);
+        __syncthreads();
+        unsigned long long* to = cluster.map_shared_rank(&sh.merged[0], 0);
+        for (unsigned int i = tid; i < n; i += kThreads)
+            if (sh.base + i < kList) to[sh.base + i] = sh.list[i];
+        cluster_sync();
     }
-    if (!greedy && p < 1.f) {
-        // the sum of the first k; equal logits at the cut count as often as they are kept
-        unsigned long long sum = 0;
-        for (int i = tid; i < V; i += kThreads) {
-            const float x = as_logit(l[i]);
-            if (order_of(x) > cut) sum += fixed_of(weight_of(x, best, inv_t));
-        }
-        const unsigned long long at_cut =
-            cut ? ties * fixed_of(weight_of(logit_of(cut), best, inv_t)) : 0;
-        const unsigned long long total = block_sum(sh, sum) + at_cut;
-        double want = ceil((double)p * (double)total);
-        unsigned long long left = want < 1.0 ? 1ull : (unsigned long long)want;
-        uint32_t prefix = 0;
-        const uint32_t kcut = cut;
-        for (int shift = 24; shift >= 0; shift -= 8) {
+
+    // The first `count` elements of `set` (count > 0) or as many as reach the share p of
+    // its sum (count = 0).  Where the list that decides holds everything that is kept
+    // (`whole`: count and then p, both) it stays sorted at the first CTA, with the
+    // number kept in sh.found; returns whether it does.
+    __device__ __forceinline__ bool find(unsigned int count, float p, const Cut set, bool all,
+                                         Cut& out) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        const bool mass = count == 0;
+        const Scale s = sh.scale;
+        // the first bins: over the logits above 2^-24 of the largest
+        const float span = fminf(24.f * 16.f / s.c, s.top - logit_of(low));
+        const float per = span > 0.f && s.top < INFINITY ? fminf((kBins - 1) / span, 1e30f) : 1.f;
+        auto first_bin = [&](float x) {
+            if (x == s.top) return 0;
+            return (int)fminf((s.top - x) * per, (float)(kBins - 1));  // NaN: the last
+        };
+        unsigned long long above = 0, want = 0;  // of the summed kind
+        unsigned int above_count = 0;
+        uint32_t klo = 0, khi = 0xffffffffu;
+        int shift = 32;
+        for (int round = 0;; ++round) {
+            for (int i = tid; i < 4 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
             __syncthreads();
-            if (tid < 256) sh.mass[tid] = 0;
-            __syncthreads();
-            for (int i = tid; i < V; i += kThreads) {
-                const float x = as_logit(l[i]);
+            unsigned int last_n = 0;
+            unsigned long long last_w = 0;
+            row.each(wlo, whi, [&](int i, float x) {
                 const uint32_t o = order_of(x);
-                if (o > kcut && (shift == 24 || (o >> (shift + 8)) == prefix))
-                    atomicAdd(&sh.mass[(o >> shift) & 255u], fixed_of(weight_of(x, best, inv_t)));
+                if (!all && !set.keeps(o, i)) return;
+                int b;
+                if (round == 0) {
+                    b = first_bin(x);
+                } else {
+                    if (o < klo || o > khi) return;
+                    b = (int)((khi - o) >> shift);
+                }
+                const unsigned long long u = mass ? fixed_of(weight_of(sh.table, s, x)) : 0;
+                if (round == 0 && b == kBins - 1) {  // most of a steep row
+                    ++last_n;
+                    last_w += u;
+                    return;
+                }
+                atomicAdd(&sh.hist[0][b], 1u);
+                if (mass) {
+                    atomicAdd(&sh.hist[1][b], (uint32_t)(u >> 28));
+                    atomicAdd(&sh.hist[2][b], (uint32_t)(u >> 14) & 0x3fffu);
+                    atomicAdd(&sh.hist[3][b], (uint32_t)u & 0x3fffu);
+                }
+            });
+            if (round == 0) {
+                const unsigned int n = __reduce_add_sync(0xffffffffu, last_n);
+                if (lane == 0 && n) atomicAdd(&sh.hist[0][kBins - 1], n);
+                if (mass) {
+                    const unsigned long long u = warp_total(last_w);
+                    if (lane == 0 && u) {
+                        atomicAdd(&sh.hist[1][kBins - 1], (uint32_t)(u >> 28));
+                        atomicAdd(&sh.hist[2][kBins - 1], (uint32_t)(u >> 14) & 0x3fffu);
+                        atomicAdd(&sh.hist[3][kBins - 1], (uint32_t)u & 0x3fffu);
+                    }
+                }
             }
-            if (tid == 0 && kcut && (shift == 24 || (kcut >> (shift + 8)) == prefix))
-                atomicAdd(&sh.mass[(kcut >> shift) & 255u], at_cut);
+            cluster_sync();
+            unsigned int n = 0;
+            unsigned long long w = 0;
+            for (int r = 0; r < ctas; ++r) {
+                const uint32_t* h = cluster.map_shared_rank(&sh.hist[0][0], r);
+                n += h[tid];
+                if (mass)
+                    w += ((unsigned long long)h[kBins + tid] << 28) +
+                         ((unsigned long long)h[2 * kBins + tid] << 14) + h[3 * kBins + tid];
+            }
+            if (tid == 0) sh.bin = kBins;
+            unsigned long long total;
+            const unsigned long long mine = mass ? w : n, end = block_sums(sh, mine, total);
+            if (round == 0) {
+                if (mass) {
+                    const double x = ceil((double)p * (double)total);
+                    want = x < 1.0 ? 1ull : (unsigned long long)x;
+                } else {
+                    want = count;
+                }
+            }
+            const unsigned long long left = want - above;
+            if (end >= left && end - mine < left) {
+                sh.bin = tid;
+                sh.in_bin = n;
+                sh.before_mass = end - mine;
+            }
+            unsigned long long skip;
+            const unsigned long long counts = mass ? block_sums(sh, n, skip) : end;
             __syncthreads();
+            const unsigned int bin = sh.bin, in_bin = sh.in_bin;
+            if (bin == kBins) {  // the sums are exact, so that one bin is reached
+                cluster_sync();
+                out = set;
+                return false;
+            }
+            if (tid == (int)bin) sh.before_count = (unsigned int)(counts - n);
+            above += sh.before_mass;
+            __syncthreads();
+            above_count += sh.before_count;
+            auto in_round = [&](int i, float x, uint32_t o, bool up) {
+                if (!all && !set.keeps(o, i)) return false;
+                if (round == 0) return up ? first_bin(x) <= (int)bin : first_bin(x) == (int)bin;
+                return o >= klo && o <= khi && ((khi - o) >> shift) == bin;
+            };
+            const bool whole = !mass && round == 0 && above_count + in_bin <= kList;
+            if (in_bin <= kList) {
+                gather([&](int i, float x, uint32_t o) { return in_round(i, x, o, whole); });
+                if (rank == 0) {
+                    const int m = (int)min(sh.n_merged, (unsigned int)kList);
+                    sort_falling(sh, m);
+                    if (whole)
+                        finish_whole((int)count, m, p, s);
+                    else
+                        finish(want - above, m, mass, s);
+                    if (tid > 0 && tid < ctas) *cluster.map_shared_rank(&sh.cut, tid) = sh.cut;
+                }
+                cluster_sync();
+                out = sh.cut;
+                return whole;
+            }
+            // too many: their range of orders, divided again by its upper bits
+            uint32_t lo = 0xffffffffu, hi = 0;
+            row.each(wlo, whi, [&](int i, float x) {
+                const uint32_t o = order_of(x);
+                if (in_round(i, x, o, false)) {
+                    lo = min(lo, o);
+                    hi = max(hi, o);
+                }
+            });
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
             if (tid == 0) {
-                int b = 255;
-                while (b > 0 && sh.mass[b] < left) left -= sh.mass[b--];
-                sh.prefix = prefix << 8 | (uint32_t)b;
-                sh.carry = left;
+                sh.base = 0xffffffffu;  // smallest and largest of the CTA
+                sh.n_list = 0;
             }
             __syncthreads();
-            prefix = sh.prefix;
-            left = sh.carry;
+            if (lane == 0) {
+                atomicMin(&sh.base, lo);
+                atomicMax(&sh.n_list, hi);
+            }
+            __syncthreads();
+            if (tid < ctas) {
+                cluster.map_shared_rank(&sh.cta_lo[0], tid)[rank] = sh.base;
+                cluster.map_shared_rank(&sh.cta_hi[0], tid)[rank] = sh.n_list;
+            }
+            cluster_sync();
+            klo = 0xffffffffu;
+            khi = 0;
+            for (int r = 0; r < ctas; ++r) {
+                klo = min(klo, sh.cta_lo[r]);
+                khi = max(khi, sh.cta_hi[r]);
+            }
+            if (klo == khi) {
+                // ties: as many as are needed, in index order
+                unsigned long long need = want - above;
+                if (mass) {
+                    const unsigned long long each = fixed_of(weight_of(sh.table, s, logit_of(klo)));
+                    need = each ? (need + each - 1) / each : in_bin;
+                }
+                out.key = klo;
+                out.last = nth_tie(klo, (unsigned int)min(need, (unsigned long long)in_bin), set, all);
+                return false;
+            }
+            shift = max(0, 32 - __clz(khi - klo) - 9);
+            cluster_sync();  // all have read the ranges and the bins
         }
-        const unsigned long long each = fixed_of(weight_of(logit_of(prefix), best, inv_t));
-        const unsigned long long some = each ? (left + each - 1) / each : 0xffffffffull;
-        if (prefix > kcut)
-            ties = (unsigned int)min(some, 0xffffffffull);
-        else
-            ties = (unsigned int)min(some, (unsigned long long)ties);
-        cut = prefix;
     }
-    // the last index of the cut's ties, if not all are kept
-    int last = V;
-    if (ties != 0xffffffffu) {
-        unsigned long long before = 0;
-        if (tid == 0) sh.found = V;
-        for (int i0 = 0; i0 < V; i0 += kThreads) {
-            const int i = i0 + tid;
-            const unsigned long long is = i < V && order_of(as_logit(l[i])) == cut;
-            unsigned long long t;
-            const unsigned long long at = block_before(sh, is, t) + before;
-            if (is && at + 1 == ties) sh.found = i;
-            before += t;
+
+    // The first `need` numbers of a sorted list, by count or by weight.
+    __device__ __forceinline__ void finish(unsigned long long need, int m, bool mass,
+                                           const Scale& s) {
+        const int tid = threadIdx.x;
+        if (!mass) {
+            if (tid == 0) set_cut(sh.merged[min(need, (unsigned long long)m) - 1]);
+        } else {
+            unsigned long long before = 0;
+            if (tid == 0) set_cut(sh.merged[m - 1]);
+            __syncthreads();
+            for (int i0 = 0; i0 < m && before < need; i0 += kThreads) {
+                const int i = i0 + tid;
+                const unsigned long long u =
+                    i < m ? fixed_of(weight_of(sh.table, s, logit_of((uint32_t)(sh.merged[i] >> 32)))) : 0;
+                unsigned long long total;
+                const unsigned long long end = block_sums(sh, u, total) + before;
+                if (i < m && end >= need && end - u < need) set_cut(sh.merged[i]);
+                before += total;
+            }
         }
         __syncthreads();
-        last = sh.found;
     }
-    auto weight = [&](int i) {
-        const float x = as_logit(l[i]);
-        const uint32_t o = order_of(x);
-        if (o < cut || (o == cut && i > last) || (x != x)) return 0.0;
-        const double w = weight_of(x, best, inv_t);
-        return w >= (double)mp ? w : 0.0;
+
+    // A sorted list that begins the row: the first `count`, and of these the share p.
+    __device__ __forceinline__ void finish_whole(int count, int m, float p, const Scale& s) {
+        const int tid = threadIdx.x;
+        m = min(m, count);
+        unsigned long long u[kList / kThreads], total = 0;
+        // each thread a run of the list
+        const int per = (m + kThreads - 1) / kThreads, lo = tid * per;
+        unsigned long long mine = 0;
+#pragma unroll
+        for (int k = 0; k < kList / kThreads; ++k) {
+            u[k] = k < per && lo + k < m
+                       ? fixed_of(weight_of(sh.table, s, logit_of((uint32_t)(sh.merged[lo + k] >> 32))))
+                       : 0;
+            mine += u[k];
+        }
+        unsigned long long at = block_sums(sh, mine, total) - mine;
+        unsigned long long want = total;
+        if (p < 1.f) {
+            const double x = ceil((double)p * (double)total);
+            want = x < 1.0 ? 1ull : (unsigned long long)x;
+        }
+        if (tid == 0) {
+            sh.found = m;
+            set_cut(sh.merged[m - 1]);
+        }
+        __syncthreads();
+        if (p < 1.f) {
+#pragma unroll
+            for (int k = 0; k < kList / kThreads; ++k) {
+                if (u[k] > 0 && at < want && at + u[k] >= want) {
+                    sh.found = lo + k + 1;
+                    set_cut(sh.merged[lo + k]);
+                }
+                at += u[k];
+            }
+            __syncthreads();
+        }
+    }
+
+    __device__ __forceinline__ void set_cut(unsigned long long e) {
+        sh.cut.key = (uint32_t)(e >> 32);
+        sh.cut.last = (int)(0xffffffffu - (uint32_t)e);
+    }
+
+    // The index of the need-th element of this order (need >= 1).
+    __device__ __forceinline__ int nth_tie(uint32_t key, unsigned int need, const Cut set, bool all) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        unsigned int n = 0;
+        auto is = [&](int i, float x) {
+            const uint32_t o = order_of(x);
+            return o == key && (all || set.keeps(o, i));
+        };
+        row.each(wlo, whi, [&](int i, float x) { n += is(i, x); });
+        n = __reduce_add_sync(0xffffffffu, n);
+        unsigned long long total;
+        const unsigned long long end = block_sums(sh, lane == 0 ? n : 0, total);  // lane 0's: with its warp
+        if (tid < ctas) cluster.map_shared_rank(&sh.cta_ties[0], tid)[rank] = (unsigned int)total;
+        cluster_sync();
+        unsigned int before = 0;
+        for (int r = 0; r < rank; ++r) before += sh.cta_ties[r];
+        const unsigned int wend = before + (unsigned int)__shfl_sync(0xffffffffu, end, 0);
+        if (need > wend - n && need <= wend) {
+            // this warp's: 32 vectors at a time, in order
+            unsigned int at = wend - n;
+            for (int v0 = wlo; v0 < whi; v0 += 32) {
+                const uint4 w = row.load(v0 + lane, whi);
+                const Elem* e = reinterpret_cast<const Elem*>(&w);
+                const int i = (v0 + lane) * Row<Elem>::VEC - row.shift;
+                unsigned int c = 0;
+                for (int z = 0; z < Row<Elem>::VEC; ++z)
+                    c += v0 + lane < whi && row.has(i + z) && is(i + z, as_logit(e[z]));
+                unsigned int inc = c;
+                for (int d = 1; d < 32; d <<= 1) {
+                    const unsigned int o = __shfl_up_sync(0xffffffffu, inc, d);
+                    if (lane >= d) inc += o;
+                }
+                unsigned int run = at + inc - c;
+                for (int z = 0; z < Row<Elem>::VEC; ++z)
+                    if (v0 + lane < whi && row.has(i + z) && is(i + z, as_logit(e[z])) &&
+                        ++run == need) {
+                        for (int r = 0; r < ctas; ++r)
+                            *cluster.map_shared_rank(&sh.cut.last, r) = i + z;
+                    }
+                at += __shfl_sync(0xffffffffu, inc, 31);
+            }
+        }
+        cluster_sync();
+        return sh.cut.last;
+    }
+};
+
+template <typename Elem, bool kProbs>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, const Table table) {
+    __shared__ Shared sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster_arrive();  // waited for before the first write into another CTA
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    const int r = blockIdx.x / ctas, V = a.V;
+    const float T = a.temperature ? a.temperature[r] : 1.f;
+    const float p = a.top_p ? a.top_p[r] : 1.f, m = a.min_p ? a.min_p[r] : 0.f;
+    const float u = !kProbs ? a.u[r] : 0.f;
+    const int k = a.top_k ? a.top_k[r] : 0;
+    if (tid < 16) sh.table.v[tid] = table.v[tid];
+    const Row<Elem> row(static_cast<const Elem*>(a.logits) + (size_t)r * V, V);
+    const int share = (row.vectors + ctas - 1) / ctas, lo = min(rank * share, row.vectors),
+              hi = min(lo + share, row.vectors);
+    const int part = (hi - lo + kWarps - 1) / kWarps, wlo = min(lo + warp * part, hi),
+              whi = min(wlo + part, hi);
+
+    // the largest logit, the first where there are several; the smallest above -inf
+    float best = -INFINITY, least = INFINITY;
+    int where = 0x7fffffff;
+    row.each(wlo, whi, [&](int i, float x) {
+        if (x > best) {
+            best = x;
+            where = i;
+        }
+        if (x > -INFINITY) least = fminf(least, x);
+    });
+    unsigned long long top = (unsigned long long)order_of(best) << 32 | (0xffffffffu - (uint32_t)where);
+    uint32_t low = order_of(least);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const unsigned long long o = __shfl_xor_sync(0xffffffffu, top, d);
+        top = o > top ? o : top;
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == 0) {
+        sh.warp_sum[warp] = top;
+        sh.part_sum[warp] = low;
+    }
+    cluster_wait();
+    __syncthreads();
+    if (warp == 0) {
+        top = lane < kWarps ? sh.warp_sum[lane] : 0;
+        low = lane < kWarps ? (uint32_t)sh.part_sum[lane] : 0xffffffffu;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const unsigned long long o = __shfl_xor_sync(0xffffffffu, top, d);
+            top = o > top ? o : top;
+        }
+        low = __reduce_min_sync(0xffffffffu, low);
+        if (lane < ctas) {
+            cluster.map_shared_rank(&sh.cta_top[0], lane)[rank] = top;
+            cluster.map_shared_rank(&sh.cta_low[0], lane)[rank] = low;
+        }
+    }
+    cluster_sync();
+    top = 0;
+    low = 0xffffffffu;
+    for (int c = 0; c < ctas; ++c) {
+        top = sh.cta_top[c] > top ? sh.cta_top[c] : top;
+        low = min(low, sh.cta_low[c]);
+    }
+    const uint32_t top_key = (uint32_t)(top >> 32);
+    const int top_at = (int)(0xffffffffu - (uint32_t)top);
+
+    auto put = [&](int i, float x) {
+        const size_t at = (size_t)r * V + i;
+        if (a.probs_bf16)
+            static_cast<__nv_bfloat16*>(a.probs)[at] = __float2bfloat16_rn(x);
+        else
+            static_cast<float*>(a.probs)[at] = x;
     };
-    unsigned long long sum = 0;
-    for (int i = tid; i < V; i += kThreads) sum += fixed_of(weight(i));
-    sum = block_sum(sh, sum);
-    if (!a.tokens) {
-        const double inv = kOne / (double)sum;
-        for (int i = tid; i < V; i += kThreads) put(i, (float)(weight(i) * inv));
+    auto zeros_but = [&](int at) {
+        row.each(wlo, whi, [&](int i, float) { put(i, i == at ? 1.f : 0.f); });
+    };
+    const bool params = T >= 0.f && T <= 1e30f && p == p && m == m && u >= 0.f && u < 1.f;
+    const bool some = top_key > kLowest;
+    if (!params || !some || T == 0.f) {
+        const bool good = params && some;
+        if (!good && rank == 0 && tid == 0)
+            report(a.dev_status, params ? KVD_DEV_PROBS : KVD_DEV_PARAM);
+        if (kProbs)
+            zeros_but(good ? top_at : -1);
+        else if (rank == 0 && tid == 0)
+            a.tokens[r] = good ? top_at : -1;
         return;
     }
-    const unsigned long long want = (unsigned long long)((double)u * (double)sum);
-    unsigned long long before = 0;
-    __syncthreads();
-    if (tid == 0) sh.found = -1;
-    for (int i0 = 0; i0 < V; i0 += kThreads) {
-        const int i = i0 + tid;
-        const unsigned long long w = i < V ? fixed_of(weight(i)) : 0;
-        unsigned long long t;
-        const unsigned long long at = block_before(sh, w, t) + before;
-        if (w > 0 && at <= want && at + w > want) sh.found = i;
-        before += t;
-        if (before > want) break;
+    if (tid == 0) {
+        const double c = 23.083120654223414 / (double)T;  // 16 log2(e)
+        sh.scale.top = logit_of(top_key);
+        sh.scale.c = (float)c;
+        sh.scale.c_low = (float)(c - (double)(float)c);
     }
     __syncthreads();
-    if (tid == 0) a.tokens[row] = sh.found;
+    const Scale s = sh.scale;
+
+    Picker<Elem> pick{sh, row, cluster, rank, ctas, wlo, whi, low};
+    Cut cut{0u, 0x7fffffff};
+    bool whole = false;
+    if (k > 0 && k < V) whole = pick.find((unsigned int)k, p, cut, true, cut);
+    if (!whole && p < 1.f) {
+        const Cut set = cut;
+        cluster_sync();
+        pick.find(0u, p, set, k <= 0 || k >= V, cut);
+    }
+    const float least_w = fminf(m, 1.f);
+    // kept: by the cut, and heavy enough
+    auto heavy = [&](const Weight& w) {
+        return w.hi > least_w || (w.hi == least_w && w.lo >= 0.f);
+    };
+    auto counted = [&](int i, float x) -> unsigned long long {
+        if (!cut.keeps(order_of(x), i)) return 0;
+        const Weight w = weight_of(sh.table, s, x);
+        return heavy(w) ? fixed_of(w) : 0;
+    };
+    if (!kProbs && whole) {
+        // all that is kept is in the first CTA's list: in index order there
+        if (rank != 0) return;
+        const int n = sh.found;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            const unsigned long long e = sh.merged[i];
+            sh.list[i] = e;
+        }
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            const unsigned long long e = sh.list[i];
+            sh.merged[i] = e << 32 | (e >> 32);  // falling: indices rise
+        }
+        __syncthreads();
+        sort_falling(sh, n);
+        unsigned long long w[kList / kThreads], mine = 0, total;
+        const int per = (n + kThreads - 1) / kThreads, at0 = tid * per;
+#pragma unroll
+        for (int z = 0; z < kList / kThreads; ++z) {
+            w[z] = 0;
+            if (z < per && at0 + z < n) {
+                const Weight x = weight_of(sh.table, s, logit_of((uint32_t)sh.merged[at0 + z]));
+                w[z] = heavy(x) ? fixed_of(x) : 0;
+            }
+            mine += w[z];
+        }
+        unsigned long long at = block_sums(sh, mine, total) - mine;
+        const unsigned long long want = (unsigned long long)((double)u * (double)total);
+#pragma unroll
+        for (int z = 0; z < kList / kThreads; ++z) {
+            if (at <= want && at + w[z] > want)
+                a.tokens[r] = (int)(0xffffffffu - (uint32_t)(sh.merged[at0 + z] >> 32));
+            at += w[z];
+        }
+        return;
+    }
+
+    // sums of what is kept, a warp and a CTA
+    unsigned long long sum = 0;
+    row.each(wlo, whi, [&](int i, float x) { sum += counted(i, x); });
+    sum = warp_total(sum);
+    __syncthreads();
+    if (lane == 0) sh.part_sum[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        const unsigned long long t = warp_total(lane < kWarps ? sh.part_sum[lane] : 0);
+        if (lane < ctas) cluster.map_shared_rank(&sh.cta_sum[0], lane)[rank] = t;
+    }
+    cluster_sync();
+    unsigned long long total = 0, before = 0;
+    for (int c = 0; c < ctas; ++c) {
+        if (c < rank) before += sh.cta_sum[c];
+        total += sh.cta_sum[c];
+    }
+    if constexpr (kProbs) {
+        const float inv = (float)((double)kOne / (double)total);
+        row.each(wlo, whi, [&](int i, float x) {
+            float y = 0.f;
+            if (cut.keeps(order_of(x), i)) {
+                const Weight w = weight_of(sh.table, s, x);
+                if (heavy(w)) y = w.hi * inv;
+            }
+            put(i, y);
+        });
+        return;
+    }
+    const unsigned long long want = (unsigned long long)((double)u * (double)total);
+    if (want < before || want >= before + sh.cta_sum[rank]) return;
+    // in this CTA: the warp's part, a sixteenth of it a warp, then in order
+    unsigned long long at = before;
+    int w = 0;
+    while (w < kWarps - 1 && at + sh.part_sum[w] <= want) at += sh.part_sum[w++];
+    const int plo = min(lo + w * part, hi), phi = min(plo + part, hi);
+    const int sub = (phi - plo + kWarps - 1) / kWarps;
+    unsigned long long sum2 = 0;
+    row.each(min(plo + warp * sub, phi), min(plo + (warp + 1) * sub, phi),
+             [&](int i, float x) { sum2 += counted(i, x); });
+    sum2 = warp_total(sum2);
+    if (lane == 0) sh.warp_sum[warp] = sum2;
+    __syncthreads();
+    if (warp != 0) return;
+    w = 0;
+    while (w < kWarps - 1 && at + sh.warp_sum[w] <= want) at += sh.warp_sum[w++];
+    const int slo = min(plo + w * sub, phi), shi = min(slo + sub, phi);
+    for (int v0 = slo; v0 < shi; v0 += 32) {
+        const uint4 x = row.load(v0 + lane, shi);
+        const Elem* e = reinterpret_cast<const Elem*>(&x);
+        const int i = (v0 + lane) * Row<Elem>::VEC - row.shift;
+        unsigned long long c[Row<Elem>::VEC], mine = 0;
+#pragma unroll
+        for (int z = 0; z < Row<Elem>::VEC; ++z) {
+            c[z] = v0 + lane < shi && row.has(i + z) ? counted(i + z, as_logit(e[z])) : 0;
+            mine += c[z];
+        }
+        unsigned long long inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const unsigned long long o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        unsigned long long run = at + inc - mine;
+#pragma unroll
+        for (int z = 0; z < Row<Elem>::VEC; ++z) {
+            if (run <= want && run + c[z] > want) a.tokens[r] = i + z;
+            run += c[z];
+        }
+        at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+}
+
+template <typename Elem>
+cudaError_t go_sample(const SampleArgs& a, cudaStream_t stream) {
+    Table t;
+    for (int j = 0; j < 16; ++j) {
+        const double x = exp2(j / 16.0);
+        t.v[j] = make_float2((float)x, (float)(x - (double)(float)x));
+    }
+    // CTAs a row: while two an SM are not passed, with 2048 elements a CTA at least; a
+    // share of 2^17 at most, so that a bin's words of 14 bits hold its sums
+    int ctas = 1;
+    while (ctas < kMaxCtas && ((2 * ctas * (long long)a.R <= 2 * kServingSMs &&
+                                a.V / (2 * ctas) >= 4 * kThreads) ||
+                               a.V / ctas > (1 << 17) - 64))
+        ctas *= 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.R * ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return a.tokens ? cudaLaunchKernelEx(&cfg, sample_kernel<Elem, false>, a, t)
+                    : cudaLaunchKernelEx(&cfg, sample_kernel<Elem, true>, a, t);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs& a, kvd_dtype dt, cudaStream_t stream) {
-    return dt == KVD_BF16
-               ? launch_pdl(sample_kernel<__nv_bfloat16>, dim3(a.R), dim3(kThreads), 0, stream, a)
-               : launch_pdl(sample_kernel<float>, dim3(a.R), dim3(kThreads), 0, stream, a);
+    return dt == KVD_BF16 ? go_sample<__nv_bfloat16>(a, stream) : go_sample<float>(a, stream);
 }
 
 }  // namespace kvd

@@ -59,7 +59,8 @@ def same(kvd, logits, u, T=None, k=None, p=None, m=None, probs=(BF, F32)):
         g = got.double()
         assert torch.equal(g > 0, q.to(dt) > 0) or \
             float((g - q).abs()[(g > 0) != (q.to(dt) > 0)].max()) < 2.0 ** -125
-        # w: 2^-38 and its sum 2^-43 V; fp32 product and factor: a rounding each
+        # w (rounded to fp32), the factor and their product: a rounding each; below 2^-125
+        # of the largest a weight may lose its last places
         tol = q * (ref.U[dt] + 3 * 2.0 ** -24) + 2.0 ** -126
         assert float(((g - q).abs() / tol).max()) <= 1.0
     assert int(status.item()) == (0 if all(some) else kvd.DEV_PROBS)
