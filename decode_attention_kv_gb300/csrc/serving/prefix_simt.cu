@@ -1,4 +1,4 @@
-// prefix_simt.cu -- kvd_attend_paged_prefix: the shared prefixes on CUDA cores,
+// prefix_simt.cu -- kvd_attend_paged_prefix: the shared prefixes in fp32, on CUDA cores,
 // and the merge of all partial rows.
 //
 // A tile is 16 query rows (sequences x query heads of one kv head of a group) x 32
@@ -13,9 +13,10 @@ namespace {
 
 constexpr int kThreads = 256, kRows = 16, kKeys = 32;
 
-template <typename Elem, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(const PrefixArgs a) {
-    constexpr int kStride = D + 4, kVec = 16 / (int)sizeof(Elem);
+    using Elem = float;
+    constexpr int kStride = D + 4, kVec = 4;
     __shared__ PrefixGroups groups;
     extern __shared__ __align__(16) float sm[];
     float* qs = sm;                       // [kRows, kStride]
@@ -158,13 +159,13 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(const PrefixArgs 
     }
 }
 
-template <typename Elem, int D>
+template <int D>
 cudaError_t go_simt(const PrefixArgs& a, cudaStream_t stream) {
     const int bytes = ((kRows + kKeys) * (D + 4) + kKeys * D + kRows * (kKeys + 1)) * 4;
     const cudaError_t e = cudaFuncSetAttribute(
-        prefix_simt_kernel<Elem, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        prefix_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(prefix_simt_kernel<Elem, D>, dim3(a.workers), dim3(kThreads), bytes, stream, a);
+    return launch_pdl(prefix_simt_kernel<D>, dim3(a.workers), dim3(kThreads), bytes, stream, a);
 }
 
 // ------------------------------------------------------------ merge
@@ -263,11 +264,8 @@ cudaError_t go_combine(const PrefixArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_prefix_simt(const PrefixArgs& a, kvd_dtype dt, cudaStream_t stream) {
-    if (dt == KVD_BF16)
-        return a.D == 64 ? go_simt<__nv_bfloat16, 64>(a, stream)
-                         : go_simt<__nv_bfloat16, 128>(a, stream);
-    return a.D == 64 ? go_simt<float, 64>(a, stream) : go_simt<float, 128>(a, stream);
+cudaError_t launch_prefix_simt(const PrefixArgs& a, cudaStream_t stream) {
+    return a.D == 64 ? go_simt<64>(a, stream) : go_simt<128>(a, stream);
 }
 
 cudaError_t launch_prefix_combine(const PrefixArgs& a, kvd_dtype dt, cudaStream_t stream) {

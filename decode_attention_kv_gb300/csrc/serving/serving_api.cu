@@ -71,10 +71,13 @@ kvd_status prefix_plan(const char* fn, int Q, int G, int Hq, int Hkv, int BS, in
         return fail(KVD_ERR_UNSUPPORTED, "%s: cols*BS or pcols*BS >= 2^31", fn);
     if ((long long)Q * Hq > (1ll << 28)) return fail(KVD_ERR_UNSUPPORTED, "%s: Q*Hq > 2^28", fn);
     const int g = Hq / Hkv, n = Q < 1 ? 1 : Q;
-    pl->rows = 16;
-    pl->keys = 32;
-    pl->lead = 2;
-    pl->workers = 2 * kServingSMs;
+    const bool mma = dt == KVD_BF16;
+    const int piece = prefix_piece_rows(BS);
+    // bf16: two tiles of 128 rows a CTA, one where all sequences together have no more
+    pl->rows = mma ? ((long long)n * g > 128 ? 256 : 128) : 16;
+    pl->keys = mma ? 128 / piece * piece : 32;
+    pl->lead = mma ? 1 : 2;
+    pl->workers = mma ? kServingSMs : 2 * kServingSMs;
     // the longest line that the groups can make
     const long long tiles = (long long)n * g / pl->rows + G + 1,
                     span = (long long)pcols * BS / pl->keys + 1 + pl->lead;
@@ -290,7 +293,8 @@ kvd_status kvd_attend_paged_prefix(const void* q, const void* key_cache, const v
     a.own_o = reinterpret_cast<const float*>(ws + pl.own.off_o);
     a.S = pl.own.S;
     a.counters = reinterpret_cast<uint32_t*>(ws);
-    cudaError_t e = launch_prefix_simt(a, dtype, (cudaStream_t)stream);
+    cudaError_t e = dtype == KVD_BF16 ? launch_prefix_mma(a, (cudaStream_t)stream)
+                                      : launch_prefix_simt(a, (cudaStream_t)stream);
     if (e != cudaSuccess) return launched(fn, e);
     st = launch_paged_partial(fn, pl.own, q, key_cache, value_cache, block_tables, seq_lens,
                               seq_offset, Q, Hq, Hkv, NB, BS, cols, D, scale, dtype, ws, dev_status,

@@ -173,7 +173,15 @@ __device__ __forceinline__ PrefixPiece prefix_piece(const PrefixArgs& a, const P
     return s;
 }
 
-cudaError_t launch_prefix_simt(const PrefixArgs& a, kvd_dtype dt, cudaStream_t stream);
+// Rows of a copy box: the largest divisor of the page size not above a tile of 128 keys.
+inline int prefix_piece_rows(int BS) {
+    int t = BS < 128 ? BS : 128;
+    while (BS % t) --t;
+    return t;
+}
+
+cudaError_t launch_prefix_mma(const PrefixArgs& a, cudaStream_t stream);   // bf16
+cudaError_t launch_prefix_simt(const PrefixArgs& a, cudaStream_t stream);  // fp32
 cudaError_t launch_prefix_combine(const PrefixArgs& a, kvd_dtype dt, cudaStream_t stream);
 
 struct PlanArgs {
