@@ -111,6 +111,11 @@ struct AttendParams {
     const int32_t* pos;          // [rows]
     uint8_t* mask_w;             // the mask, written at pos
     int out_f32;                 // out is fp32 whatever the element type (a range's partial)
+    // The launch runs beside the kernel before it on the stream, which leaves SMs free and
+    // whose results it does not read: that kernel waits for all before it and only then
+    // lets this one start, so this one waits at its end, for the kernels behind it.  CTAs
+    // may start late, so every unit comes from the work counter.
+    int beside;
     int small_push;              // one-launch kernel: the splits push partials into split 0
     int small_nwg;               // one-launch kernel: consumer warp groups per CTA (1 or 2)
     // sliding window (static buffer): row b attends to the masked slots of
@@ -674,7 +679,7 @@ attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap kmap,
         prefetch_tensormap(&vmap);
     }
     pdl_launch_dependents();
-    pdl_wait();
+    if (!p.beside) pdl_wait();
     __syncthreads();
 
     if (warp >= kSched0 && warp < kSched0 + kSchedN) {
@@ -693,7 +698,7 @@ attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap kmap,
         // share their mask row or sequence, so that the metadata reads after
         // the first hit L1 -- else the first units are spread over all CTAs.
         const int n_sched = kSchedN * (int)gridDim.x;
-        const int first_units = n_sched;
+        const int first_units = p.beside ? 0 : n_sched;
         int u = p.units >= n_sched ? (int)blockIdx.x * kSchedN + sw
                                    : sw * (int)gridDim.x + (int)blockIdx.x;
         auto publish = [&](int slot) {
@@ -721,7 +726,7 @@ attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap kmap,
             }
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
         };
-        bool first = true;
+        bool first = !p.beside;
         // Scheduler 0 of the static buffer publishes its first slot without
         // the lookahead gate: the loader waits for that slot first (its
         // unit's first tiles were loaded speculatively) and takes no other
@@ -868,6 +873,7 @@ attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap kmap,
                 eph ^= 1u;
             }
         }
+        if (p.beside) pdl_wait();
         return;
     }
 

@@ -422,6 +422,7 @@ kvd_status launch_paged_partial(const char* fn, const PagedPartial& pp, const vo
     p.NB = NB;
     p.qscale = scale * kLog2e;
     attach_workspace(p, pl, region);
+    p.beside = 1;
     char* base = static_cast<char*>(region);
     p.part_lse = reinterpret_cast<float*>(base + pp.off_lse);
     p.part_o = reinterpret_cast<float*>(base + pp.off_o);

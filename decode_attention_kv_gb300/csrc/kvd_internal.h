@@ -64,6 +64,8 @@ cudaError_t launch_combine(const float* part_o, const float* part_lse, void* out
 // fp32 rows part_o [Q * Hq, S, D], normalised, and part_lse [Q * Hq, S] (natural log,
 // -inf: the row was not written), whatever S is, at these offsets of its region of the
 // workspace, which begins with the work counters (two words, zero before the launch).
+// The launch runs beside the kernel before it on the stream (AttendParams::beside): that
+// one must call pdl_launch_dependents() behind its pdl_wait().
 struct PagedPartial {
     int S;
     size_t off_lse, off_o, bytes;

@@ -16,8 +16,7 @@
 // above 128 rows) in a ring of eight blocks of 128 tokens x 64 elements.
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, a row a thread; they also lay out the
-// queries.  Warps 8 and 9 issue the MMAs of tile 0 and 1.  Warp 10 looks up pages and
-// issues the copies.
+// queries.  Warp 8 issues the MMAs.  Warp 9 looks up pages and issues the copies.
 #include "../kvd_internal.h"
 #include "../latent/latent_common.cuh"  // encode_rows, FastDiv, kTinyScale
 #include "../latent/tcgen05_ptx.cuh"
@@ -33,8 +32,8 @@ constexpr int kSteps = 4;            // steps with barriers of their own (the ri
 // Steps whose valid words are kept: those of step i are written when the scores of step
 // i - 4 at the latest are complete, so that step i - 5 has been through the softmax.
 constexpr int kValid = 8;
-constexpr int kMmaWarp = 8, kCopyWarp = 10;
-constexpr int kThreads = 384;  // warp 11 completes the third warpgroup
+constexpr int kMmaWarp = 8, kCopyWarp = 9;
+constexpr int kThreads = 384;  // warps 10 and 11 complete the third warpgroup
 // Registers a thread: the softmax holds a row of 128 scores.  2 x 208 + 80 is
 // within the 3 x 168 that three warpgroups start with.
 constexpr int kSoftmaxRegs = 208, kIssueRegs = 80;
@@ -44,7 +43,7 @@ constexpr uint32_t kTmemCols = 512;
 struct MmaShared {
     alignas(16) uint32_t valid[kValid][4];  // keys of a step that count
     uint64_t q_full[2], k_full[kSteps], v_full[kSteps], empty[kRing];
-    uint64_t s_full[2], p_full[2], o_full[2], turn, drain[2];
+    uint64_t s_full[2], p_full[2], o_full[2], drain;
     uint32_t tmem;
     int abort;
     PrefixGroups groups;
@@ -58,13 +57,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
         if (__any_sync(0xffffffffu, *abort_flag || now - since > kWaitLimitNs)) return false;
     }
     return true;
-}
-
-// 32 bytes of a row of partial results.
-__device__ __forceinline__ void store8(float* p, const float* x) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]),
-                 "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
 }
 
 // Bits [b0, b1) of four words.
@@ -90,14 +82,13 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
             mbar_init(&sh.s_full[s], 2);  // the scores; the valid words
             mbar_init(&sh.p_full[s], kRows / 32);
             mbar_init(&sh.o_full[s], 1);
-            mbar_init(&sh.drain[s], 1);
         }
         for (int i = 0; i < kSteps; ++i) {
             mbar_init(&sh.k_full[i], 1);
             mbar_init(&sh.v_full[i], 1);
         }
-        for (int i = 0; i < kRing; ++i) mbar_init(&sh.empty[i], 2);  // both tiles are done with it
-        mbar_init(&sh.turn, 1);
+        for (int i = 0; i < kRing; ++i) mbar_init(&sh.empty[i], 1);
+        mbar_init(&sh.drain, 1);
         sh.abort = 0;
         fence_barrier_init();
     }
@@ -111,16 +102,14 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
             reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
         fence_async_smem();
     }
-    pdl_launch_dependents();
     pdl_wait();
     tc_fence_before();
-    const int tot = prefix_setup<kThreads>(a, sh.groups);  // ends with a barrier
+    const PrefixRuns runs = prefix_setup<kThreads>(a, sh.groups);  // with barriers
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     volatile int* abort_flag = &sh.abort;
-    const PrefixRuns runs(tot, a.workers);
     const int w = blockIdx.x;
-    const bool works = tot > 0 && w < runs.W;
+    const bool works = runs.tot > 0 && w < runs.W;
     const int lo = works ? runs.start(w) : 0, hi = works ? runs.start(w + 1) : 0;
     bool bad = false;
 
@@ -143,26 +132,28 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
             p = s.next;
             const int n = sh.groups.keys[s.group], chunk = s.head * KC;
             const int32_t* table = a.prefix_tables + (size_t)s.group * a.pcols;
+            // first row in the cache of piece p of key tile k, or -1
+            auto source = [&](int k, int p) {
+                const int key = k * a.keys + p * piece;
+                if (p >= pieces || key >= n) return -1;
+                const int page = by_page(key), phys = __ldg(table + page);
+                return phys < 0 || phys >= a.NB ? -2 : phys * a.BS + key - page * a.BS;
+            };
             for (int k = s.k0; k < s.k1 && !bad; ++k, ++it) {
-                int src[4];  // first row of this lane's pieces in the cache, or -1
+                int src[4];  // first row of this lane's pieces in the cache
                 uint32_t valid[4] = {0u, 0u, 0u, 0u};
                 int loads = 0;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     src[u] = -1;
                     if (32 * u >= pieces) continue;
-                    const int b0 = (lane + 32 * u) * piece, key = k * a.keys + b0;
-                    if (lane + 32 * u < pieces && key < n) {
-                        const int page = by_page(key), phys = __ldg(table + page);
-                        if (phys < 0 || phys >= a.NB) {
-                            report(a.dev_status, KVD_DEV_BLOCK_RANGE);
-                        } else {
-                            src[u] = phys * a.BS + key - page * a.BS;
+                    src[u] = source(k, lane + 32 * u);
+                    const int b0 = (lane + 32 * u) * piece;
+                    if (src[u] == -2) report(a.dev_status, KVD_DEV_BLOCK_RANGE);
+                    if (src[u] >= 0)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                valid[x] |= range_word(b0, b0 + min(piece, n - key), x);
-                        }
-                    }
+                        for (int x = 0; x < 4; ++x)
+                            valid[x] |= range_word(b0, b0 + min(piece, n - k * a.keys - b0), x);
                     loads += __popc(__ballot_sync(0xffffffffu, src[u] >= 0));
                 }
 #pragma unroll
@@ -207,117 +198,89 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
             while (global_timer_ns() - since < 1000000ull) {
             }
         }
-    } else if (warp < kCopyWarp) {
+    } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issue
-        const int s = uniform(warp - kMmaWarp);
-        const uint32_t sdesc = mma_desc(kRows, kRows), odesc = mma_desc(kRows, 64, kBMn);
-        const uint32_t tm = uniform(tmem);
-        const uint32_t q_low = uniform(desc_low(smem_u32(sm) + s * KC * kBlock, 16));
-        const uint32_t td = uniform(tm + s * kRows), to = uniform(tm + 256 + s * kRows);
-        const uint32_t base = uniform(smem_u32(ring));
-        int it = 0, cnt = 0, seg = 0;
-        uint32_t k_low[KC];
-        auto keys_of = [&](int i) {
-#pragma unroll
-            for (int c = 0; c < KC; ++c)
-                k_low[c] = uniform(desc_low(base + (i * per + c) % kRing * kBlock, 16));
-        };
-        auto scores = [&](int i) {
+        // One warp in a fixed order, S0(0) S1(0) PV0(0) S0(1) PV1(0) S1(1) PV0(1) ..: a warp
+        // per tile leaves the tiles in step (the products of both, then the softmax of
+        // both: 4400 cycles a step).
+        constexpr int kN = 64 * KC;
+        const uint32_t sdesc = mma_desc(kRows, kRows), odesc = mma_desc(kRows, kN, kBMn);
+        const uint32_t tm = uniform(tmem), base = uniform(smem_u32(ring));
+        const uint32_t q_base = uniform(smem_u32(sm));
+        int it = 0, cnt[2] = {0, 0}, seg[2] = {0, 0};
+        // scores of tile s, step i; the keys are free behind the last tile's
+        auto scores = [&](int s, int i, bool last) {
+            const uint32_t q_low = uniform(desc_low(q_base + s * KC * kBlock, 16));
+            const uint32_t k_low = uniform(desc_low(base + (i * per) % kRing * kBlock, 16));
             if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < KC; ++c)
 #pragma unroll
                     for (int z = 0; z < 4; ++z)
-                        mma_ss(td, desc_of(q_low + ((c * kBlock) >> 4) + 2 * z),
-                               desc_of(k_low[c] + 2 * z), sdesc, c > 0 || z > 0);
+                        mma_ss(tm + s * kRows, desc_of(q_low + ((c * kBlock) >> 4) + 2 * z),
+                               desc_of(k_low + ((c * kBlock) >> 4) + 2 * z), sdesc, c > 0 || z > 0);
                 // the copying warp's valid words (this warp has waited for the keys) are
                 // ordered before the softmax's reads by an arrival of its own
                 mbar_arrive(&sh.s_full[s]);
                 mma_commit(&sh.s_full[s]);
+                if (last)
 #pragma unroll
-                for (int c = 0; c < KC; ++c) mma_commit(&sh.empty[(i * per + c) % kRing]);
+                    for (int c = 0; c < KC; ++c) mma_commit(&sh.empty[(i * per + c) % kRing]);
             }
             __syncwarp();
+        };
+        auto values = [&](int s, int i, bool keep, bool end, bool last) {
+            const uint32_t v_low =
+                uniform(desc_low(base + (i * per + KC) % kRing * kBlock, KC > 1 ? kBlock : 16));
+            if (elect_one()) {
+#pragma unroll
+                for (int z = 0; z < 8; ++z)
+                    mma_ts(tm + 256 + s * kRows, tm + s * kRows + 8 * z,
+                           desc_of(v_low + ((z * 2048) >> 4)), odesc, z > 0 || keep);
+                if (end) mma_commit(&sh.o_full[s]);
+                if (last)
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) mma_commit(&sh.empty[(i * per + KC + c) % kRing]);
+            }
+            __syncwarp();
+        };
+        auto await = [&](uint64_t* bar, uint32_t parity) {
+            if (!bad && !warp_wait(bar, parity, abort_flag)) bad = true;
+            return !bad;
         };
         for (int p = lo; p < hi && !bad;) {
             const PrefixPiece pc = prefix_piece(a, sh.groups, w, lo, hi, p);
             p = uniform(pc.next);
-            const int n = uniform(max(pc.k1 - pc.k0, 0)), rows = uniform(rows_of(pc));
+            const int n = uniform(max(pc.k1 - pc.k0, 0)), tiles = uniform(rows_of(pc)) > kRows ? 2 : 1;
             if (n == 0) continue;
-            const int end = it + n;
-            if (s * kRows >= rows) {  // only the other tile has rows
-                for (; it < end && !bad; ++it) {
-                    if (!warp_wait(&sh.v_full[it % kSteps], (it / kSteps) & 1, abort_flag)) {
-                        bad = true;
-                        break;
-                    }
-                    if (elect_one())
-                        for (int c = 0; c < per; ++c) mbar_arrive(&sh.empty[(it * per + c) % kRing]);
-                    __syncwarp();
-                }
-                continue;
-            }
-            // tile 1 starts half a step behind tile 0, so that one's products and the
-            // other's softmax take turns from the first step on
-            if (s == 1 && it == 0) bad = !warp_wait(&sh.turn, 0, abort_flag);
-            bad = bad || !warp_wait(&sh.q_full[s], seg & 1, abort_flag) ||
-                  !warp_wait(&sh.k_full[it % kSteps], (it / kSteps) & 1, abort_flag);
-            ++seg;
-            tc_fence_after();
-            keys_of(it);
-            if (!bad) scores(it);
-            for (int i0 = it; it < end && !bad; ++it, ++cnt) {
-                const uint32_t keep = uniform((int)(it > i0));
-                const int b0 = it * per + KC;
-                uint32_t v_low[KC];
-#pragma unroll
-                for (int c = 0; c < KC; ++c)
-                    v_low[c] = uniform(desc_low(base + (b0 + c) % kRing * kBlock, 16));
-                keys_of(it + 1);
-                uint64_t* kf = &sh.k_full[(it + 1) % kSteps];
-                const uint32_t kpar = ((it + 1) / kSteps) & 1;
-                if (!warp_wait(&sh.v_full[it % kSteps], (it / kSteps) & 1, abort_flag)) {
-                    bad = true;
-                    break;
-                }
-                // looked at while the softmax still runs; not waited for before the values,
-                // whose blocks the keys' copies may need
-                const bool keys = it + 1 < end && __all_sync(0xffffffffu, mbar_test(kf, kpar));
-                if (!warp_wait(&sh.p_full[s], cnt & 1, abort_flag)) {
-                    bad = true;
-                    break;
-                }
+            const int first = it, end = it + n;
+            await(&sh.k_full[it % kSteps], (it / kSteps) & 1);
+            for (int s = 0; s < tiles; ++s) {
+                if (!await(&sh.q_full[s], seg[s]++ & 1)) break;
                 tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int c = 0; c < KC; ++c)
-#pragma unroll
-                        for (int z = 0; z < 8; ++z)
-                            mma_ts(to + 64 * c, td + 8 * z, desc_of(v_low[c] + ((z * 2048) >> 4)),
-                                   odesc, z > 0 || keep);
-#pragma unroll
-                    for (int c = 0; c < KC; ++c) mma_commit(&sh.empty[(b0 + c) % kRing]);
-                    if (it + 1 == end) mma_commit(&sh.o_full[s]);
-                    if (s == 0 && it == 0) mbar_arrive(&sh.turn);
-                }
-                __syncwarp();
-                if (it + 1 < end) {
-                    if (!keys && !warp_wait(kf, kpar, abort_flag)) {
-                        bad = true;
-                        break;
-                    }
+                scores(s, it, s + 1 == tiles);
+            }
+            for (; it < end && !bad; ++it) {
+                await(&sh.v_full[it % kSteps], (it / kSteps) & 1);
+                for (int s = 0; s < tiles && !bad; ++s) {
+                    if (!await(&sh.p_full[s], cnt[s]++ & 1)) break;
                     tc_fence_after();
-                    scores(it + 1);
+                    values(s, it, it > first, it + 1 == end, s + 1 == tiles);
+                    if (it + 1 < end) {
+                        if (!await(&sh.k_full[(it + 1) % kSteps], ((it + 1) / kSteps) & 1)) break;
+                        tc_fence_after();
+                        scores(s, it + 1, s + 1 == tiles);
+                    }
                 }
             }
         }
         if (bad) {
             if (lane == 0) sh.abort = 1;
             __syncwarp();
-            if (elect_one()) mma_commit(&sh.drain[s]);
+            if (elect_one()) mma_commit(&sh.drain);
             __syncwarp();
             const unsigned long long since = global_timer_ns();
-            while (!mbar_try_wait(&sh.drain[s], 0) && global_timer_ns() - since < kWaitLimitNs) {
+            while (!mbar_try_wait(&sh.drain, 0) && global_timer_ns() - since < kWaitLimitNs) {
             }
         }
     }
@@ -346,18 +309,26 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
                 const int r = pc.tile * a.rows + in_tile, seq = by_head(live ? r : 0);
                 if (live)
                     at = (size_t)(sh.groups.start[pc.group] + seq) * a.Hq + pc.head * a.g + r - seq * a.g;
-                const uint4* q = reinterpret_cast<const uint4*>(
-                    static_cast<const __nv_bfloat16*>(a.q) + at * D);
-                const int row = in_tile & (kRows - 1);
+                // whole rows at a time: D / 8 lanes a row
+                constexpr int kLanes = D / 8, kAt = 32 / kLanes;
+                const uint4* q = static_cast<const uint4*>(a.q);
+                const int j = lane % kLanes;
+                unsigned char* to = sm + (s * KC + j / 8) * kBlock;
+                const uint32_t rows_live = __ballot_sync(0xffffffffu, live);
 #pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    uint4 x[8];
+                for (int i0 = 0; i0 < kLanes; i0 += kLanes) {
+                    uint4 x[kLanes];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = live ? q[8 * c + j] : make_uint4(0, 0, 0, 0);
+                    for (int i = 0; i < kLanes; ++i) {
+                        const int r = (i0 + i) * kAt + lane / kLanes;
+                        const unsigned long long from = __shfl_sync(0xffffffffu, (unsigned long long)at, r);
+                        x[i] = (rows_live >> r) & 1u ? q[from * kLanes + j] : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4*>(sm + (s * KC + c) * kBlock + row * 128 +
-                                                  ((j ^ (row & 7)) << 4)) = x[j];
+                    for (int i = 0; i < kLanes; ++i) {
+                        const int row = 32 * (warp & 3) + (i0 + i) * kAt + lane / kLanes;
+                        *reinterpret_cast<uint4*>(to + row * 128 + (((j & 7) ^ (row & 7)) << 4)) = x[i];
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -463,17 +434,39 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
             if (a.qscale != a.qscale && l != 0.f) l = a.qscale;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t row = pc.slot < 0 ? at : (size_t)pc.slot * a.rows + in_tile;
-            float* out = (pc.slot < 0 ? a.whole_o : a.part_o) + row * D;
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(to + c, reinterpret_cast<uint32_t*>(o));
-                tmem_wait_ld();
+            // through shared memory (the queries' place: their products are complete), so that
+            // a store covers whole rows; kDims dims of the warp's 32 rows at a time
+            constexpr int kDims = 32 * KC, kVecs = kDims / 4;
+            float* out = pc.slot < 0 ? a.whole_o : a.part_o;
+            uint4* stage = reinterpret_cast<uint4*>(sm + s * KC * kBlock) + (warp & 3) * 32 * kVecs;
+            const uint32_t rows_live = __ballot_sync(0xffffffffu, live);
+#pragma unroll 1
+            for (int c = 0; c < D; c += kDims) {
+                for (int half = 0; half < (rows_live ? KC : 0); ++half) {
+                    float o[32];
+                    tmem_ld32(to + c + 32 * half, reinterpret_cast<uint32_t*>(o));
+                    tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= inv;
-                if (live) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) store8(out + c + e, o + e);
+                    for (int e = 0; e < 32; e += 4) {
+                        const int j = 8 * half + e / 4;
+                        stage[lane * kVecs + (j ^ (lane & (kVecs - 1)))] =
+                            make_uint4(__float_as_uint(o[e] * inv), __float_as_uint(o[e + 1] * inv),
+                                       __float_as_uint(o[e + 2] * inv), __float_as_uint(o[e + 3] * inv));
+                    }
                 }
+                __syncwarp();
+                const int count = __popc(rows_live);  // the warp's first rows
+#pragma unroll 8
+                for (int i = 0; i < kVecs; ++i) {
+                    if ((32 / kVecs) * i >= count) break;
+                    const int r = (32 / kVecs) * i + lane / kVecs, j = lane % kVecs;
+                    const unsigned long long to_row =
+                        __shfl_sync(0xffffffffu, (unsigned long long)row, r);
+                    if ((rows_live >> r) & 1u)
+                        *reinterpret_cast<uint4*>(out + to_row * D + c + 4 * j) =
+                            stage[r * kVecs + (j ^ (r & (kVecs - 1)))];
+                }
+                __syncwarp();
             }
             if (live)
                 (pc.slot < 0 ? a.whole_lse : a.part_lse)[row] =

@@ -24,13 +24,11 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(const PrefixArgs 
     float* vs = ks + kKeys * kStride;     // [kKeys, D]
     float* ps = vs + kKeys * D;           // [kRows, kKeys + 1]
     __shared__ uint32_t valid_bits;
-    pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, row = tid >> 4, sub = tid & 15;
-    const int tot = prefix_setup<kThreads>(a, groups);
-    const PrefixRuns runs(tot, a.workers);
+    const PrefixRuns runs = prefix_setup<kThreads>(a, groups);
     const int w = blockIdx.x;
-    if (tot == 0 || w >= runs.W) return;
+    if (runs.tot == 0 || w >= runs.W) return;
     const int lo = runs.start(w), hi = runs.start(w + 1);
     const Elem* qg = static_cast<const Elem*>(a.q);
     const Elem* kg = static_cast<const Elem*>(a.k);
@@ -184,16 +182,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_combine_kernel(const 
     if (row >= a.Q * a.Hq) return;
     const int q = row / a.Hq, hq = row - q * a.Hq, h = hq / a.g;
     const int4 meta = a.meta[q];
-    const int tot = a.meta[a.Q].x;
+    const int4 line = a.meta[a.Q];
     int w0 = 0, pieces = 0, in_tile = 0;  // pieces of the prefix
-    if (meta.z > 0) {
-        const PrefixRuns runs(tot, a.workers);
+    // (a launch that gave up on a wait may have left no division behind)
+    if (meta.z > 0 && line.x > 0 && line.y > 0 && line.y <= a.workers) {
+        const PrefixRuns runs(line.x, line.y);
         const int r = meta.w * a.g + hq - h * a.g, tile = r / a.rows;
         in_tile = r - tile * a.rows;
         const int first = meta.x + (h * meta.y + tile) * (meta.z + a.lead) + a.lead;
         w0 = runs.worker_of(first);
         pieces = runs.worker_of(first + meta.z - 1) - w0 + 1;
-        // a launch that gave up on a wait may have left no division behind
         if (w0 < 0 || pieces < 1 || w0 + pieces > a.workers) pieces = 0;
     }
     const int n = pieces + a.S;

@@ -284,6 +284,11 @@ kvd_status kvd_attend_paged_prefix(const void* q, const void* key_cache, const v
     a.keys = pl.keys;
     a.lead = pl.lead;
     a.workers = pl.workers;
+    if (dtype == KVD_BF16) {
+        a.place_cost = 4.f;
+        a.token_cost = (float)Hkv * D * 4 / 45000.f;
+    }
+    a.seq_lens = seq_lens;
     a.meta = reinterpret_cast<int4*>(ws + pl.off_meta);
     a.part_lse = reinterpret_cast<float*>(ws + pl.off_plse);
     a.part_o = reinterpret_cast<float*>(ws + pl.off_po);

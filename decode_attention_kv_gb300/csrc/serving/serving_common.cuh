@@ -32,7 +32,13 @@ struct PrefixArgs {
     float qscale;         // scale * log2(e)
     int rows, keys;       // of a tile
     int lead, workers;
-    int4* meta;           // [Q + 1] first place, row tiles, key tiles, place in the group; the line
+    // SM microseconds that a place of the line costs, and a token of a sequence's own: how
+    // many SMs the prefixes take while the sequences' own keys go through the others (0:
+    // as many as there are)
+    float place_cost, token_cost;
+    const int32_t* seq_lens;
+    int4* meta;           // [Q + 1] first place, row tiles, key tiles, place in the group;
+                          // last the line's length and the workers that share it
     float* part_lse;      // [2 * workers, rows] log2 units
     float* part_o;        // [2 * workers, rows, D], normalised
     float* whole_lse;     // [Q * Hq]
@@ -73,9 +79,7 @@ __device__ __forceinline__ int last_not_above(const int* x, int n, int v) {
 // [floor(w tot / W), floor((w + 1) tot / W)).
 struct PrefixRuns {
     int tot, W;
-    __device__ __forceinline__ PrefixRuns(int tot_, int workers) : tot(tot_) {
-        W = max(1, min(workers, tot));
-    }
+    __device__ __forceinline__ PrefixRuns(int tot_, int W_) : tot(tot_), W(W_) {}
     __device__ __forceinline__ int start(int w) const { return (int)((long long)w * tot / W); }
     __device__ __forceinline__ int worker_of(int place) const {
         return (int)((((long long)place + 1) * W - 1) / tot);
@@ -83,12 +87,23 @@ struct PrefixRuns {
 };
 
 // By all threads of a CTA: reads and checks the groups, lays out the line, writes this
-// CTA's share of the meta rows; returns the length of the line.
+// CTA's share of the meta rows; returns the line's division.  The attention over the
+// sequences' own keys, which is launched behind, runs beside this kernel: it may start
+// from here on, when everything before both is complete and its counters are zero.
 template <int THREADS>
-__device__ __forceinline__ int prefix_setup(const PrefixArgs& a, PrefixGroups& t) {
+__device__ __forceinline__ PrefixRuns prefix_setup(const PrefixArgs& a, PrefixGroups& t) {
     const int tid = threadIdx.x;
+    if (blockIdx.x == 0) {
+        if (tid < 2) {
+            a.counters[tid] = 0;
+            __threadfence();
+        }
+        __syncthreads();
+    }
+    pdl_launch_dependents();
     uint32_t bits = 0;
     bool bad = false;
+    const int own = a.place_cost > 0.f ? a.seq_lens[a.Q] : 0;
     for (int i = tid; i <= a.G; i += THREADS) {
         const int s0 = a.G > 0 ? a.group_lens[i] : 0;
         t.start[i] = s0;
@@ -131,10 +146,16 @@ __device__ __forceinline__ int prefix_setup(const PrefixArgs& a, PrefixGroups& t
     }
     __syncthreads();
     const int tot = t.base[a.G];
+    int W = min(a.workers, max(tot, 1));
+    if (own > 0) {
+        const float mine = a.place_cost * (float)tot, theirs = a.token_cost * (float)own;
+        W = max(1, min(W, (int)(a.workers * mine / (mine + theirs) + 0.5f)));
+    }
     for (int q = blockIdx.x * THREADS + tid; q <= a.Q; q += gridDim.x * THREADS) {
         int4 m = make_int4(0, 0, 0, 0);
         if (q == a.Q) {
             m.x = tot;
+            m.y = W;
         } else if (!bad && a.G > 0 && q < t.start[a.G]) {
             const int i = last_not_above(t.start, a.G, q);
             m = make_int4(t.base[i], ceil_div(t.sequences(i) * a.g, a.rows),
@@ -142,8 +163,7 @@ __device__ __forceinline__ int prefix_setup(const PrefixArgs& a, PrefixGroups& t
         }
         a.meta[q] = m;
     }
-    if (blockIdx.x == 0 && tid < 2) a.counters[tid] = 0;
-    return tot;
+    return PrefixRuns(tot, W);
 }
 
 // The piece of a segment that a run holds.
