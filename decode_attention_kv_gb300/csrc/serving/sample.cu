@@ -4,15 +4,19 @@
 // top-k, top-p and min-p each keep a beginning of the row, so what is kept is a cut: a
 // smallest logit and, among those equal to it, a last index.
 //
-// A cluster of 1 to 8 CTAs takes a row, a contiguous share a CTA and of that a warp.
-// The largest logit first; then a histogram of 512 bins over the logits that weigh more
-// than 2^-24 of it (linear in l, so that a bin's weights differ by a twentieth of a
-// factor of two), of counts for top-k and of counts and weights for top-p.  Every CTA
-// adds up all CTAs' bins and finds the one that the cut falls into; its elements (for a
-// small k all above it too) go to the first CTA, which sorts them and takes the cut by
-// their running sums.  Bins that hold more than a list (flat rows, ties) are divided
-// again, by the bits of the logits' order, until a list takes them or one value is left,
-// whose ties are counted through in index order.
+// A cluster of 1 to 8 CTAs takes a row, a contiguous share a CTA and of that a warp; the
+// row comes from memory once and is read again from L2.
+//   First pass: the largest logit, and with top-k a histogram of the logits' orders.  The
+//   bins that hold the first k go to the first CTA, which sorts them, takes both cuts and
+//   draws.
+//   Without top-k, second pass: a histogram of approximate weights, which brackets the
+//   top-p border (to a hundred elements or so).  Third pass: the exact sums of the row and of what
+//   lies above the bracket; the bracket's elements go to the first CTA, which sorts them
+//   and takes the cut.  The draw then reads again only the part of one warp.
+//   Where a list does not hold what it should (flat rows, ties, large k), the row is
+//   divided into 512 bins of exact counts or weights, the bin of the border again, and so
+//   on by the orders' bits, until a list takes it or one value is left, whose ties are
+//   counted through in index order.
 //
 // Whole numbers decide, so sums must not depend on an order and have to agree with sums
 // in 64 bits: a weight is computed in two fp32 words (a table of sixteenths of a factor
@@ -31,6 +35,9 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;
 constexpr int kBins = kThreads;  // a thread a bin when they are added up
+// Bits of an order that its bin of the first pass leaves out: eight bins a factor of two
+// (finer ones take longer to clear and to add up, and a list holds 2048 elements).
+constexpr int kOrderShift = 20, kOrders = 1 << (32 - kOrderShift);
 constexpr int kList = 2048;      // elements that one CTA sorts
 constexpr int kBatch = 16;       // elements that a lane loads at once
 constexpr unsigned long long kOne = 1ull << 42;  // the weight 1
@@ -125,11 +132,18 @@ struct Cut {
 
 struct Shared {
     Table table;
-    uint32_t hist[4][kBins];  // counts; weights in three words of 14 bits
+    union {
+        uint32_t hist[4][kBins];  // counts; weights in three words of 14 bits
+        uint32_t orders[kOrders]; // first pass: counts by the upper bits of the orders
+        float rough[kBins];       // second pass: approximate weights
+    };
     unsigned long long list[kList];   // of this CTA; then sorted by the first
     unsigned long long merged[kList]; // of all CTAs, at the first
     unsigned long long warp_sum[kWarps], part_sum[kWarps];
-    unsigned long long cta_sum[kMaxCtas];
+    unsigned long long cta_sum[kMaxCtas], cta_above[kMaxCtas];
+    unsigned long long kept;      // the sum of what is kept, from the first CTA
+    float hi, lo;                 // the bracket of the top-p border
+    int good;                     // the bracket held it
     unsigned long long cta_top[kMaxCtas];
     uint32_t cta_low[kMaxCtas];
     uint32_t cta_lo[kMaxCtas], cta_hi[kMaxCtas];
@@ -194,9 +208,11 @@ struct Row {
         vectors = (shift + V + VEC - 1) / VEC;
     }
     __device__ __forceinline__ bool has(int i) const { return (unsigned)i < (unsigned)V; }
+    // (-inf where the row has no element)
     __device__ __forceinline__ uint4 load(int v, int end) const {
         const int i = v * VEC - shift;
-        uint4 w = make_uint4(0, 0, 0, 0);
+        constexpr uint32_t kNone = sizeof(Elem) == 4 ? 0xff800000u : 0xff80ff80u;
+        uint4 w = make_uint4(kNone, kNone, kNone, kNone);
         if (v < end) {
             if (i >= 0 && i + VEC <= V) {
                 w = *reinterpret_cast<const uint4*>(p + i);
@@ -208,6 +224,25 @@ struct Row {
             }
         }
         return w;
+    }
+    // f(vector, logits) for the vectors [lo, hi), by one warp.
+    template <typename F>
+    __device__ __forceinline__ void vectors_of(int lo, int hi, F f) const {
+        constexpr int N = kBatch / VEC;
+        for (int v0 = lo + (int)(threadIdx.x & 31); v0 < hi; v0 += 32 * N) {
+            uint4 w[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) w[k] = load(v0 + 32 * k, hi);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (v0 + 32 * k >= hi) break;
+                const Elem* e = reinterpret_cast<const Elem*>(&w[k]);
+                float x[VEC];
+#pragma unroll
+                for (int z = 0; z < VEC; ++z) x[z] = as_logit(e[z]);
+                f(v0 + 32 * k, x);
+            }
+        }
     }
     // f(index, logit) for the row's elements in the vectors [lo, hi), by one warp.
     template <typename F>
@@ -260,6 +295,64 @@ struct Picker {
     int rank, ctas, wlo, whi;  // of this warp's vectors
     uint32_t low;              // the smallest order above kLowest, or the largest
 
+    // Elements on their way to the first CTA: into this CTA's list, then all at once.
+    __device__ __forceinline__ void note(int i, float x) {
+        const unsigned int at = atomicAdd(&sh.n_list, 1u);
+        if (at < kList)
+            sh.list[at] = (unsigned long long)order_of(x) << 32 | (0xffffffffu - (uint32_t)i);
+    }
+    // (With what must be visible there as well; ends with a barrier of the cluster.)
+    __device__ __forceinline__ void send() {
+        const int tid = threadIdx.x;
+        __syncthreads();
+        const unsigned int n = sh.n_list;
+        if (tid == 0 && n > 0) sh.base = atomicAdd(cluster.map_shared_rank(&sh.n_merged, 0), n);
+        __syncthreads();
+        unsigned long long* to = cluster.map_shared_rank(&sh.merged[0], 0);
+        for (unsigned int i = tid; i < min(n, (unsigned int)kList); i += kThreads)
+            if (sh.base + i < kList) to[sh.base + i] = sh.list[i];
+        cluster_sync();
+    }
+
+    // The first `count` elements, and of these the share p, from the first pass's counts:
+    // sorted at the first CTA (see find's `whole`).  False where no list holds them.
+    __device__ __forceinline__ bool find_first(unsigned int count, float p, uint32_t top_key,
+                                               float& from) {
+        const int tid = threadIdx.x;
+        const int bin = (int)(top_key >> kOrderShift) - tid;
+        unsigned int n = 0;
+        if (bin >= 0)
+            for (int r = 0; r < ctas; ++r) n += cluster.map_shared_rank(&sh.orders[0], r)[bin];
+        if (tid == 0) sh.bin = kBins;
+        unsigned long long total;
+        const unsigned long long end = block_sums(sh, n, total);
+        if (end >= count && end - n < count) {
+            sh.bin = tid;
+            sh.in_bin = (unsigned int)end;
+        }
+        if (tid == 0) sh.n_list = 0;
+        __syncthreads();
+        if (sh.bin == kBins || sh.in_bin > kList) {
+            cluster_sync();  // the counts are no longer read
+            return false;
+        }
+        const uint32_t key = ((top_key >> kOrderShift) - sh.bin) << kOrderShift;
+        from = key > kLowest ? logit_of(key) : -INFINITY;
+        row.vectors_of(wlo, whi, [&](int v, const float (&x)[Row<Elem>::VEC]) {
+#pragma unroll
+            for (int z = 0; z < Row<Elem>::VEC; ++z)
+                if (x[z] >= from && row.has(v * Row<Elem>::VEC - row.shift + z))
+                    note(v * Row<Elem>::VEC - row.shift + z, x[z]);
+        });
+        send();
+        if (rank == 0) {
+            const int m = (int)min(sh.n_merged, (unsigned int)kList);
+            sort_falling(sh, m);
+            finish_whole((int)count, m, p, sh.scale);
+        }
+        return true;
+    }
+
     // Gathers the elements that `take` accepts at the first CTA; n of them in all.
     template <typename F>
     __device__ __forceinline__ void gather(F take) {
@@ -269,20 +362,9 @@ struct Picker {
         __syncthreads();
         cluster_sync();
         row.each(wlo, whi, [&](int i, float x) {
-            const uint32_t o = order_of(x);
-            if (take(i, x, o)) {
-                const unsigned int at = atomicAdd(&sh.n_list, 1u);
-                if (at < kList) sh.list[at] = (unsigned long long)o << 32 | (0xffffffffu - (uint32_t)i);
-            }
+            if (take(i, x, order_of(x))) note(i, x);
         });
-        __syncthreads();
-        const unsigned int n = min(sh.n_list, (unsigned int)kList);
-        if (tid == 0 && n > 0) sh.base = atomicAdd(cluster.map_shared_rank(&sh.n_merged, 0), n);
-        __syncthreads();
-        unsigned long long* to = cluster.map_shared_rank(&sh.merged[0], 0);
-        for (unsigned int i = tid; i < n; i += kThreads)
-            if (sh.base + i < kList) to[sh.base + i] = sh.list[i];
-        cluster_sync();
+        send();
     }
 
     // The first `count` elements of `set` (count > 0) or as many as reach the share p of
@@ -454,14 +536,15 @@ struct Picker {
         }
     }
 
-    // The first `need` numbers of a sorted list, by count or by weight.
-    __device__ __forceinline__ void finish(unsigned long long need, int m, bool mass,
+    // The first `need` numbers of a sorted list, by count or by weight; whether it has as many.
+    __device__ __forceinline__ bool finish(unsigned long long need, int m, bool mass,
                                            const Scale& s) {
         const int tid = threadIdx.x;
+        unsigned long long before = 0;
         if (!mass) {
             if (tid == 0) set_cut(sh.merged[min(need, (unsigned long long)m) - 1]);
+            before = m;
         } else {
-            unsigned long long before = 0;
             if (tid == 0) set_cut(sh.merged[m - 1]);
             __syncthreads();
             for (int i0 = 0; i0 < m && before < need; i0 += kThreads) {
@@ -475,6 +558,7 @@ struct Picker {
             }
         }
         __syncthreads();
+        return before >= need;
     }
 
     // A sorted list that begins the row: the first `count`, and of these the share p.
@@ -570,7 +654,8 @@ struct Picker {
 
 template <typename Elem, bool kProbs>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, const Table table) {
-    __shared__ Shared sh;
+    extern __shared__ __align__(16) unsigned char raw[];
+    Shared& sh = *reinterpret_cast<Shared*>(raw);
     cg::cluster_group cluster = cg::this_cluster();
     cluster_arrive();  // waited for before the first write into another CTA
     pdl_launch_dependents();
@@ -589,15 +674,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const int part = (hi - lo + kWarps - 1) / kWarps, wlo = min(lo + warp * part, hi),
               whi = min(wlo + part, hi);
 
-    // the largest logit, the first where there are several; the smallest above -inf
+    constexpr int VEC = Row<Elem>::VEC;
+    const bool first_k = k > 0 && k < V;
+    if (first_k) {
+        for (int i = tid; i < kOrders; i += kThreads) sh.orders[i] = 0;
+        __syncthreads();
+    }
+    // the largest logit and the first vector that holds it; the smallest
     float best = -INFINITY, least = INFINITY;
-    int where = 0x7fffffff;
-    row.each(wlo, whi, [&](int i, float x) {
-        if (x > best) {
-            best = x;
-            where = i;
+    int where = 0;
+    row.vectors_of(wlo, whi, [&](int v, const float (&x)[VEC]) {
+        float most = x[0];
+#pragma unroll
+        for (int z = 0; z < VEC; ++z) {
+            most = fmaxf(most, x[z]);
+            least = fminf(least, x[z]);
         }
-        if (x > -INFINITY) least = fminf(least, x);
+        if (most > best) {
+            best = most;
+            where = v;
+        }
+        if (first_k) {
+#pragma unroll
+            for (int z = 0; z < VEC; ++z) {
+                const int b = __float_as_int(x[z] + 0.f);  // -0 as 0
+                if (x[z] == x[z])
+                    atomicAdd(&sh.orders[(uint32_t)(b ^ ((b >> 31) | (int)0x80000000)) >> kOrderShift], 1u);
+            }
+        }
     });
     unsigned long long top = (unsigned long long)order_of(best) << 32 | (0xffffffffu - (uint32_t)where);
     uint32_t low = order_of(least);
@@ -610,6 +714,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     if (lane == 0) {
         sh.warp_sum[warp] = top;
         sh.part_sum[warp] = low;
+    }
+    if (tid == 0) {
+        sh.n_merged = 0;
+        sh.n_list = 0;
     }
     cluster_wait();
     __syncthreads();
@@ -635,17 +743,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         low = min(low, sh.cta_low[c]);
     }
     const uint32_t top_key = (uint32_t)(top >> 32);
-    const int top_at = (int)(0xffffffffu - (uint32_t)top);
 
-    auto put = [&](int i, float x) {
-        const size_t at = (size_t)r * V + i;
-        if (a.probs_bf16)
-            static_cast<__nv_bfloat16*>(a.probs)[at] = __float2bfloat16_rn(x);
-        else
-            static_cast<float*>(a.probs)[at] = x;
-    };
-    auto zeros_but = [&](int at) {
-        row.each(wlo, whi, [&](int i, float) { put(i, i == at ? 1.f : 0.f); });
+    // outputs of a vector, whole where the rows of both start alike
+    const size_t out_row = (size_t)r * V;
+    const bool whole_out =
+        a.probs_bf16 == (sizeof(Elem) == 2) &&
+        ((reinterpret_cast<uintptr_t>(a.probs) - reinterpret_cast<uintptr_t>(a.logits)) & 15u) == 0;
+    auto put = [&](int v, const float (&y)[VEC]) {
+        const int i = v * VEC - row.shift;
+        if (whole_out && i >= 0 && i + VEC <= V) {
+            uint4 w;
+            if constexpr (sizeof(Elem) == 4) {
+                w = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]),
+                               __float_as_uint(y[3]));
+            } else {
+                uint32_t h[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const __nv_bfloat162 q = __floats2bfloat162_rn(y[2 * z], y[2 * z + 1]);
+                    h[z] = *reinterpret_cast<const uint32_t*>(&q);
+                }
+                w = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            *reinterpret_cast<uint4*>(static_cast<Elem*>(a.probs) + out_row + i) = w;
+            return;
+        }
+#pragma unroll
+        for (int z = 0; z < VEC; ++z) {
+            if (!row.has(i + z)) continue;
+            if (a.probs_bf16)
+                static_cast<__nv_bfloat16*>(a.probs)[out_row + i + z] = __float2bfloat16_rn(y[z]);
+            else
+                static_cast<float*>(a.probs)[out_row + i + z] = y[z];
+        }
     };
     const bool params = T >= 0.f && T <= 1e30f && p == p && m == m && u >= 0.f && u < 1.f;
     const bool some = top_key > kLowest;
@@ -653,10 +783,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         const bool good = params && some;
         if (!good && rank == 0 && tid == 0)
             report(a.dev_status, params ? KVD_DEV_PROBS : KVD_DEV_PARAM);
-        if (kProbs)
-            zeros_but(good ? top_at : -1);
-        else if (rank == 0 && tid == 0)
-            a.tokens[r] = good ? top_at : -1;
+        int at = -1;
+        if (good) {  // the first of the largest logits
+            const int v = (int)(0xffffffffu - (uint32_t)top);
+            const uint4 w = row.load(v, row.vectors);
+            const Elem* e = reinterpret_cast<const Elem*>(&w);
+            for (int z = VEC - 1; z >= 0; --z)
+                if (order_of(as_logit(e[z])) == top_key && row.has(v * VEC - row.shift + z))
+                    at = v * VEC - row.shift + z;
+        }
+        if (kProbs) {
+            row.vectors_of(wlo, whi, [&](int v, const float (&)[VEC]) {
+                float y[VEC];
+#pragma unroll
+                for (int z = 0; z < VEC; ++z) y[z] = v * VEC - row.shift + z == at ? 1.f : 0.f;
+                put(v, y);
+            });
+        } else if (rank == 0 && tid == 0) {
+            a.tokens[r] = at;
+        }
         return;
     }
     if (tid == 0) {
@@ -667,42 +812,157 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
     __syncthreads();
     const Scale s = sh.scale;
-
-    Picker<Elem> pick{sh, row, cluster, rank, ctas, wlo, whi, low};
-    Cut cut{0u, 0x7fffffff};
-    bool whole = false;
-    if (k > 0 && k < V) whole = pick.find((unsigned int)k, p, cut, true, cut);
-    if (!whole && p < 1.f) {
-        const Cut set = cut;
-        cluster_sync();
-        pick.find(0u, p, set, k <= 0 || k >= V, cut);
-    }
     const float least_w = fminf(m, 1.f);
-    // kept: by the cut, and heavy enough
+    // heavy enough for min-p
     auto heavy = [&](const Weight& w) {
         return w.hi > least_w || (w.hi == least_w && w.lo >= 0.f);
     };
-    auto counted = [&](int i, float x) -> unsigned long long {
-        if (!cut.keeps(order_of(x), i)) return 0;
-        const Weight w = weight_of(sh.table, s, x);
-        return heavy(w) ? fixed_of(w) : 0;
-    };
-    if (!kProbs && whole) {
-        // all that is kept is in the first CTA's list: in index order there
-        if (rank != 0) return;
+
+    Picker<Elem> pick{sh, row, cluster, rank, ctas, wlo, whi, low};
+    Cut cut{0u, 0x7fffffff};
+    // whole: all that is kept is sorted in the first CTA's list; summed: part_sum holds
+    // the sums of what is kept, a warp
+    bool whole = false, summed = false;
+    float from = -INFINITY;  // nothing below is kept
+    if (first_k) {
+        whole = pick.find_first((unsigned int)k, p, top_key, from);
+        if (!whole) whole = pick.find((unsigned int)k, p, cut, true, cut);
+    }
+    if (!whole && !first_k) {
+        float hi = -INFINITY, lo_x = -INFINITY;
+        if (p < 1.f) {
+            // approximate weights by distance from the largest logit
+            sh.rough[tid] = 0.f;
+            __syncthreads();
+            const float span = fminf(24.f * 16.f / s.c, s.top - logit_of(low));
+            const float per = span > 0.f && s.top < INFINITY ? fminf((kBins - 2) / span, 1e30f) : 1.f;
+            const float c = s.c * 0.0625f;
+            float rest = 0.f;
+            row.vectors_of(wlo, whi, [&](int, const float (&x)[VEC]) {
+#pragma unroll
+                for (int z = 0; z < VEC; ++z) {
+                    const float d = s.top - x[z];
+                    const float w = fast_exp2(-d * c);
+                    const int b = __float_as_int(fminf(d * per, (float)(kBins - 1)) + kMagic) & 0x7ff;
+                    if (b < kBins - 1)
+                        atomicAdd(&sh.rough[b], w);
+                    else if (w == w)
+                        rest += w;
+                }
+            });
+#pragma unroll
+            for (int d = 16; d; d >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, d);
+            if (lane == 0 && rest > 0.f) atomicAdd(&sh.rough[kBins - 1], rest);
+            cluster_sync();
+            float mine = 0.f;
+            for (int c2 = 0; c2 < ctas; ++c2) mine += cluster.map_shared_rank(&sh.rough[0], c2)[tid];
+            // (in units of 2^-20, whole numbers from here on: every CTA gets the same bracket)
+            const float units = fminf(mine * 1048576.f, 1e18f);
+            const unsigned long long n = units > 0.f ? (unsigned long long)units : 0;
+            if (tid == 0) sh.bin = sh.base = kBins - 1;
+            unsigned long long total;
+            const unsigned long long end = block_sums(sh, n, total);
+            const double at_least = ((double)p - 1e-4) * (double)total,
+                         at_most = ((double)p + 1e-4) * (double)total;
+            if (at_least <= 0.0 ? tid == 0
+                                : (double)end > at_least && (double)(end - n) <= at_least)
+                sh.bin = tid;
+            if ((double)end > at_most && (double)(end - n) <= at_most) sh.base = tid;
+            __syncthreads();
+            // a bin's border lies half a bin before it
+            hi = sh.bin > 0 ? s.top - ((float)sh.bin - 0.5f) / per : INFINITY;
+            lo_x = sh.base < kBins - 1 ? s.top - ((float)sh.base + 0.5f) / per : -INFINITY;
+            __syncthreads();
+        }
+        // exact sums: of the row, above the bracket, and of what is kept there
+        unsigned long long all = 0, above = 0, kept = 0;
+        row.vectors_of(wlo, whi, [&](int v, const float (&x)[VEC]) {
+#pragma unroll
+            for (int z = 0; z < VEC; ++z) {
+                const Weight w = weight_of(sh.table, s, x[z]);
+                const unsigned long long q = fixed_of(w);
+                all += q;
+                if (x[z] > hi || p >= 1.f) {
+                    above += q;
+                    kept += heavy(w) ? q : 0;
+                } else if (x[z] >= lo_x && row.has(v * VEC - row.shift + z)) {
+                    pick.note(v * VEC - row.shift + z, x[z]);
+                }
+            }
+        });
+        all = warp_total(all);
+        above = warp_total(above);
+        kept = warp_total(kept);
+        __syncthreads();
+        if (lane == 0) {
+            sh.part_sum[warp] = kept;
+            sh.warp_sum[warp] = all;
+            sh.merged[warp] = above;  // before any CTA sends
+        }
+        __syncthreads();
+        summed = true;
+        if (p < 1.f) {
+            if (warp == 0) {
+                const unsigned long long t = warp_total(lane < kWarps ? sh.warp_sum[lane] : 0);
+                const unsigned long long b = warp_total(lane < kWarps ? sh.merged[lane] : 0);
+                if (lane == 0) {
+                    cluster.map_shared_rank(&sh.cta_sum[0], 0)[rank] = t;
+                    cluster.map_shared_rank(&sh.cta_above[0], 0)[rank] = b;
+                }
+            }
+            cluster_sync();  // everybody's use of `merged` is over
+            pick.send();
+            if (rank == 0) {
+                unsigned long long total = 0, over = 0;
+                for (int c = 0; c < ctas; ++c) {
+                    total += sh.cta_sum[c];
+                    over += sh.cta_above[c];
+                }
+                const double x = ceil((double)p * (double)total);
+                const unsigned long long want = x < 1.0 ? 1ull : (unsigned long long)x;
+                const int n = (int)min(sh.n_merged, (unsigned int)kList);
+                bool good = sh.n_merged <= kList && n > 0 && want > over;
+                if (good) {
+                    sort_falling(sh, n);
+                    good = pick.finish(want - over, n, true, s);
+                }
+                if (tid < ctas) {
+                    *cluster.map_shared_rank(&sh.good, tid) = good;
+                    *cluster.map_shared_rank(&sh.cut, tid) = sh.cut;
+                }
+            }
+            cluster_sync();
+            summed = sh.good;
+            if (summed) {
+                // what the cut keeps of this CTA's part of the bracket
+                cut = sh.cut;
+                for (unsigned int i = tid; i < sh.n_list; i += kThreads) {
+                    const uint32_t o = (uint32_t)(sh.list[i] >> 32);
+                    const int at = (int)(0xffffffffu - (uint32_t)sh.list[i]);
+                    const Weight w = weight_of(sh.table, s, logit_of(o));
+                    if (cut.keeps(o, at) && heavy(w))
+                        atomicAdd(&sh.part_sum[((at + row.shift) / VEC - lo) / part], fixed_of(w));
+                }
+            } else {
+                pick.find(0u, p, cut, true, cut);
+            }
+            __syncthreads();
+        }
+    } else if (!whole && p < 1.f) {
+        const Cut set = cut;
+        cluster_sync();
+        pick.find(0u, p, set, false, cut);
+    }
+    if (whole && rank == 0) {
+        // the first CTA draws, or adds up, in index order
         const int n = sh.found;
         __syncthreads();
-        for (int i = tid; i < n; i += kThreads) {
-            const unsigned long long e = sh.merged[i];
-            sh.list[i] = e;
-        }
+        for (int i = tid; i < n; i += kThreads) sh.list[i] = sh.merged[i];
         __syncthreads();
-        for (int i = tid; i < n; i += kThreads) {
-            const unsigned long long e = sh.list[i];
-            sh.merged[i] = e << 32 | (e >> 32);  // falling: indices rise
-        }
+        for (int i = tid; i < n; i += kThreads)
+            sh.merged[i] = sh.list[i] << 32 | (sh.list[i] >> 32);  // falling: indices rise
         __syncthreads();
-        sort_falling(sh, n);
+        if (!kProbs) sort_falling(sh, n);
         unsigned long long w[kList / kThreads], mine = 0, total;
         const int per = (n + kThreads - 1) / kThreads, at0 = tid * per;
 #pragma unroll
@@ -715,42 +975,67 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             mine += w[z];
         }
         unsigned long long at = block_sums(sh, mine, total) - mine;
-        const unsigned long long want = (unsigned long long)((double)u * (double)total);
+        if constexpr (kProbs) {
+            if (tid < ctas) {
+                *cluster.map_shared_rank(&sh.cut, tid) = sh.cut;
+                *cluster.map_shared_rank(&sh.kept, tid) = total;
+            }
+        } else {
+            const unsigned long long want = (unsigned long long)((double)u * (double)total);
 #pragma unroll
-        for (int z = 0; z < kList / kThreads; ++z) {
-            if (at <= want && at + w[z] > want)
-                a.tokens[r] = (int)(0xffffffffu - (uint32_t)(sh.merged[at0 + z] >> 32));
-            at += w[z];
+            for (int z = 0; z < kList / kThreads; ++z) {
+                if (at <= want && at + w[z] > want)
+                    a.tokens[r] = (int)(0xffffffffu - (uint32_t)(sh.merged[at0 + z] >> 32));
+                at += w[z];
+            }
         }
-        return;
     }
+    if (!kProbs && whole) return;
 
-    // sums of what is kept, a warp and a CTA
-    unsigned long long sum = 0;
-    row.each(wlo, whi, [&](int i, float x) { sum += counted(i, x); });
-    sum = warp_total(sum);
-    __syncthreads();
-    if (lane == 0) sh.part_sum[warp] = sum;
-    __syncthreads();
-    if (warp == 0) {
-        const unsigned long long t = warp_total(lane < kWarps ? sh.part_sum[lane] : 0);
-        if (lane < ctas) cluster.map_shared_rank(&sh.cta_sum[0], lane)[rank] = t;
-    }
-    cluster_sync();
+    auto counted = [&](int i, float x) -> unsigned long long {
+        if (!cut.keeps(order_of(x), i)) return 0;
+        const Weight w = weight_of(sh.table, s, x);
+        return heavy(w) ? fixed_of(w) : 0;
+    };
     unsigned long long total = 0, before = 0;
-    for (int c = 0; c < ctas; ++c) {
-        if (c < rank) before += sh.cta_sum[c];
-        total += sh.cta_sum[c];
+    if (!whole) {
+        // sums of what is kept, a warp and a CTA
+        if (!summed) {
+            unsigned long long sum = 0;
+            row.each(wlo, whi, [&](int i, float x) { sum += counted(i, x); });
+            sum = warp_total(sum);
+            __syncthreads();
+            if (lane == 0) sh.part_sum[warp] = sum;
+            __syncthreads();
+        }
+        if (warp == 0) {
+            const unsigned long long t = warp_total(lane < kWarps ? sh.part_sum[lane] : 0);
+            if (lane < ctas) cluster.map_shared_rank(&sh.cta_sum[0], lane)[rank] = t;
+        }
+        cluster_sync();
+        for (int c = 0; c < ctas; ++c) {
+            if (c < rank) before += sh.cta_sum[c];
+            total += sh.cta_sum[c];
+        }
+    } else {
+        cluster_sync();
+        cut = sh.cut;
+        total = sh.kept;
     }
     if constexpr (kProbs) {
         const float inv = (float)((double)kOne / (double)total);
-        row.each(wlo, whi, [&](int i, float x) {
-            float y = 0.f;
-            if (cut.keeps(order_of(x), i)) {
-                const Weight w = weight_of(sh.table, s, x);
-                if (heavy(w)) y = w.hi * inv;
+        const float least_x = logit_of(max(cut.key, kLowest));
+        row.vectors_of(wlo, whi, [&](int v, const float (&x)[VEC]) {
+            float y[VEC];
+#pragma unroll
+            for (int z = 0; z < VEC; ++z) {
+                y[z] = 0.f;
+                if (x[z] >= least_x && cut.keeps(order_of(x[z]), v * VEC - row.shift + z)) {
+                    const Weight w = weight_of(sh.table, s, x[z]);
+                    if (heavy(w)) y[z] = w.hi * inv;
+                }
             }
-            put(i, y);
+            put(v, y);
         });
         return;
     }
@@ -775,10 +1060,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     for (int v0 = slo; v0 < shi; v0 += 32) {
         const uint4 x = row.load(v0 + lane, shi);
         const Elem* e = reinterpret_cast<const Elem*>(&x);
-        const int i = (v0 + lane) * Row<Elem>::VEC - row.shift;
-        unsigned long long c[Row<Elem>::VEC], mine = 0;
+        const int i = (v0 + lane) * VEC - row.shift;
+        unsigned long long c[VEC], mine = 0;
 #pragma unroll
-        for (int z = 0; z < Row<Elem>::VEC; ++z) {
+        for (int z = 0; z < VEC; ++z) {
             c[z] = v0 + lane < shi && row.has(i + z) ? counted(i + z, as_logit(e[z])) : 0;
             mine += c[z];
         }
@@ -790,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         }
         unsigned long long run = at + inc - mine;
 #pragma unroll
-        for (int z = 0; z < Row<Elem>::VEC; ++z) {
+        for (int z = 0; z < VEC; ++z) {
             if (run <= want && run + c[z] > want) a.tokens[r] = i + z;
             run += c[z];
         }
@@ -815,7 +1100,12 @@ cudaError_t go_sample(const SampleArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(a.R * ctas);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = stream;
+    auto kernel = a.tokens ? sample_kernel<Elem, false> : sample_kernel<Elem, true>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Shared));
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -825,8 +1115,7 @@ cudaError_t go_sample(const SampleArgs& a, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return a.tokens ? cudaLaunchKernelEx(&cfg, sample_kernel<Elem, false>, a, t)
-                    : cudaLaunchKernelEx(&cfg, sample_kernel<Elem, true>, a, t);
+    return cudaLaunchKernelEx(&cfg, kernel, a, t);
 }
 
 }  // namespace
