@@ -9,20 +9,24 @@
 //   First pass: the largest logit, and with top-k a histogram of the logits' orders.  The
 //   bins that hold the first k go to the first CTA, which sorts them, takes both cuts and
 //   draws.
-//   Without top-k, second pass: a histogram of approximate weights, which brackets the
-//   top-p border (to a hundred elements or so).  Third pass: the exact sums of the row and of what
-//   lies above the bracket; the bracket's elements go to the first CTA, which sorts them
-//   and takes the cut.  The draw then reads again only the part of one warp.
+//   Without top-k, second pass (top-p): counts by distance from the largest logit, which
+//   bracket the border (to a hundred elements or so) and tell whether min-p cuts well
+//   before it.  Third pass: exact sums, of what min-p keeps where that decides alone, else
+//   of the row and of what lies above the bracket; the bracket's elements go to the first
+//   CTA, which sorts them and takes the cut.  The draw then reads again only the part of
+//   one warp.
 //   Where a list does not hold what it should (flat rows, ties, large k), the row is
 //   divided into 512 bins of exact counts or weights, the bin of the border again, and so
 //   on by the orders' bits, until a list takes it or one value is left, whose ties are
 //   counted through in index order.
 //
 // Whole numbers decide, so sums must not depend on an order and have to agree with sums
-// in 64 bits: a weight is computed in two fp32 words (a table of sixteenths of a factor
-// of two and a polynomial; right to 2^-34 of the largest weight, and a small one to 2^-29
-// of itself) and counted in whole multiples of 2^-42.
+// in 64 bits: a weight is a table's sixteenth of a factor of two times a polynomial, right
+// to about 2^-28 of itself without a trend, and is counted in whole multiples of 2^-42.
 #include <cooperative_groups.h>
+
+#include <cmath>
+#include <cstring>
 
 #include "../kvd_internal.h"
 #include "serving_common.cuh"
@@ -57,68 +61,93 @@ __device__ __forceinline__ float logit_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// 2^(j / 16) in two words, j = 0 .. 15 (correctly rounded; the second is what the first
-// leaves).
+// 2^(j / 16), j = 0 .. 15: in units of 2^-31, and in two fp32 words.
 struct Table {
-    float2 v[16];
+    uint2 fixed[16];  // the number, and fp32 of it
+    float low[16];    // what fp32 of 2^(j / 16) leaves
 };
 
 // What the weights of a row go by.
 struct Scale {
-    float top;         // the largest logit
-    float c, c_low;    // 16 log2(e) / T in two words
+    float top;       // the largest logit
+    float c, c_low;  // 16 log2(e) / T in two words
+    // top c = whole + rest: whole a multiple of 1/64, so that sums with whole numbers are
+    // exact; fast: |top c| is below 2^16, where that holds
+    float whole, rest;
+    int fast;
 };
 
-// 2^(f / 16) - 1 = k1 f + k2 f^2 + ..., k1 = ln 2 / 16
-struct Weight {
-    float hi, lo;  // the weight is their sum
-};
+constexpr double kLn = 0.69314718055994530942 / 16.0;  // 2^(f / 16) - 1 = k1 f + k2 f^2 + ...
+constexpr float kK1 = (float)kLn, kK2 = (float)(kLn * kLn / 2), kK3 = (float)(kLn * kLn * kLn / 6),
+                kK4 = (float)(kLn * kLn * kLn * kLn / 24);
 
-__device__ __forceinline__ Weight weight_of(const Table& t, const Scale& s, float x) {
-    Weight w{1.f, 0.f};
-    if (x == s.top) return w;
-    // x - top in two words (Knuth's two-sum)
-    const float d = __fsub_rn(x, s.top), b = __fsub_rn(d, x);
-    const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(s.top, b));
-    // y = 16 log2 of the weight, in two words
-    const float y = __fmul_rn(d, s.c);
-    if (!(y > -2000.f)) {  // below 2^-125, or no logit
-        w.hi = y < 0.f ? exp2f(y * 0.0625f) : 0.f;
-        return w;
-    }
-    // (Every operation rounds as written: all passes must get the same weight.)
-    const float yl = __fmaf_rn(dl, s.c, __fmaf_rn(d, s.c_low, __fmaf_rn(d, s.c, -y)));
-    const float r = __fadd_rn(y, kMagic);
-    const int n = __float_as_int(r) - __float_as_int(kMagic);
-    const float f = __fsub_rn(y, __fsub_rn(r, kMagic));  // exact, |f| <= 1/2
-    constexpr double kLn = 0.69314718055994530942 / 16.0;
-    constexpr float k1 = (float)kLn, k1l = (float)(kLn - (double)k1), k2 = (float)(kLn * kLn / 2),
-                    k3 = (float)(kLn * kLn * kLn / 6), k4 = (float)(kLn * kLn * kLn * kLn / 24);
-    // 2^((f + yl) / 16) - 1 in two words: the first order of f exactly, that of yl with
-    // the factor 2^(f / 16), higher ones in one word
-    const float p = __fmul_rn(k1, f), pl = __fmul_rn(k1, yl);
-    const float rest = __fmaf_rn(
-        __fmul_rn(f, f), __fmaf_rn(f, __fmaf_rn(f, k4, k3), k2),
-        __fadd_rn(__fmaf_rn(pl, p, pl), __fmaf_rn(k1l, f, __fmaf_rn(k1, f, -p))));
-    const float q = __fadd_rn(p, rest), ql = __fsub_rn(rest, __fsub_rn(q, p));
-    const float2 e = t.v[n & 15];
-    const float m = __fmul_rn(e.x, q);
-    const float hi = __fadd_rn(e.x, m);
-    const float lo = __fadd_rn(__fadd_rn(__fmaf_rn(e.x, ql, __fmaf_rn(e.x, q, -m)), __fmaf_rn(e.y, q, e.y)),
-                               __fsub_rn(m, __fsub_rn(hi, e.x)));
-    const float scale = __int_as_float(((n >> 4) + 127) << 23);
-    w.hi = __fmul_rn(hi, scale);
-    w.lo = __fmul_rn(lo, scale);
-    return w;
+constexpr float kLeast = -2000.f;                  // 2^-125: smaller weights are zero
+constexpr float kUnit = 4.656612873077393e-10f;    // 2^-31
+
+// exp((x - top) / T) = 2^((n + f) / 16), n whole and |f| <= 1/2: n is a multiple of 1/16 of a
+// factor of two, f comes from one rounding of x c - (whole + n), which is exact before it.
+struct Split {
+    int n;
+    float q;  // 2^(f / 16) - 1
+};
+// 2^(f / 16) - 1
+__device__ __forceinline__ float power_of(float f) {
+    return __fmul_rn(f, __fmaf_rn(f, __fmaf_rn(f, __fmaf_rn(f, kK4, kK3), kK2), kK1));
+}
+__device__ __forceinline__ Split split_fast(const Scale& s, float x) {
+    const float y = __fmaf_rn(x, s.c, -s.whole);
+    const float r = __fadd_rn(y, kMagic), n = __fsub_rn(r, kMagic);
+    const float f = __fadd_rn(__fmaf_rn(x, s.c, -__fadd_rn(n, s.whole)), __fmaf_rn(x, s.c_low, -s.rest));
+    // (NaN and -inf fail the comparison)
+    return Split{y > kLeast ? __float_as_int(r) - __float_as_int(kMagic) : (int)kLeast, power_of(f)};
 }
 
-// In multiples of 2^-42 (a float in [4, 8) is a multiple of 2^-21).
-__device__ __forceinline__ unsigned long long fixed_of(const Weight& w) {
-    const float a = __fadd_rn(w.hi, 6.f);
-    const float rest = __fadd_rn(__fsub_rn(w.hi, __fsub_rn(a, 6.f)), w.lo);
-    const float b = __fmaf_rn(rest, 2097152.f, 6.f);
-    return ((unsigned long long)(__float_as_uint(a) - __float_as_uint(6.f)) << 21) +
-           (unsigned long long)(long long)(__float_as_int(b) - __float_as_int(6.f));
+// The same where top / T is too large for that: the difference from the largest logit
+// first, in two words.  (Far off the way: logits above 2800 T.)
+__device__ __noinline__ int2 split_slow(const Scale& s, float x) {
+    const float d = __fsub_rn(x, s.top), b = __fsub_rn(d, x);
+    const float dl = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(s.top, b));
+    const float y = __fmul_rn(d, s.c);
+    if (!(y > kLeast)) return make_int2((int)kLeast, 0);
+    const float yl = __fmaf_rn(dl, s.c, __fmaf_rn(d, s.c_low, __fmaf_rn(d, s.c, -y)));
+    const float r = __fadd_rn(y, kMagic);
+    const float f = __fadd_rn(__fsub_rn(y, __fsub_rn(r, kMagic)), yl);
+    return make_int2(__float_as_int(r) - __float_as_int(kMagic), __float_as_int(power_of(f)));
+}
+__device__ __forceinline__ Split split_of(const Scale& s, float x) {
+    if (s.fast) return split_fast(s, x);
+    const int2 w = split_slow(s, x);
+    return Split{w.x, __int_as_float(w.y)};
+}
+
+// A weight in multiples of 2^-42.  (Every operation rounds as written: all passes must get
+// the same.)
+__device__ __forceinline__ unsigned long long fixed_of(const Table& t, const Scale& s, float x) {
+    if (x == s.top) return kOne;
+    const Split p = split_of(s, x);
+    if (p.n <= -688) return 0;  // half a unit
+    const uint2 e = t.fixed[p.n & 15];
+    const uint32_t v = e.x + (uint32_t)__float2int_rn(__fmul_rn(__uint_as_float(e.y), p.q));
+    // units of 2^-31 of a factor of two down to those of 2^-42 of one, rounded
+    return ((((unsigned long long)v << 32) >> (20 - (p.n >> 4))) + 1) >> 1;
+}
+
+// The same as a number; and whether it is at least m, without that number's rounding.
+__device__ __forceinline__ float weight_of(const Table& t, const Scale& s, float x) {
+    if (x == s.top) return 1.f;
+    const Split p = split_of(s, x);
+    if (p.n <= (int)kLeast) return 0.f;
+    const float hi = __fmul_rn(__uint_as_float(t.fixed[p.n & 15].y), kUnit);
+    const float w = __fadd_rn(hi, __fmaf_rn(hi, p.q, t.low[p.n & 15]));
+    return __fmul_rn(w, __int_as_float(((p.n >> 4) + 127) << 23));
+}
+__device__ __forceinline__ bool at_least(const Table& t, const Scale& s, float x, float m) {
+    if (x == s.top) return true;
+    const Split p = split_of(s, x);
+    if (p.n <= (int)kLeast) return false;
+    const float hi = __fmul_rn(__uint_as_float(t.fixed[p.n & 15].y), kUnit);
+    const float scaled = m * __int_as_float((127 - (p.n >> 4)) << 23);
+    return __fadd_rn(__fsub_rn(hi, scaled), __fmaf_rn(hi, p.q, t.low[p.n & 15])) >= 0.f;
 }
 
 // A beginning of the row: order above `key`, or equal to it and an index up to `last`.
@@ -134,23 +163,23 @@ struct Shared {
     Table table;
     union {
         uint32_t hist[4][kBins];  // counts; weights in three words of 14 bits
-        uint32_t orders[kOrders]; // first pass: counts by the upper bits of the orders
-        float rough[kBins];       // second pass: approximate weights
+        uint32_t orders[kOrders]; // first pass: counts by the upper bits of the orders;
+                                  // second pass: by the distance from the largest logit
     };
     unsigned long long list[kList];   // of this CTA; then sorted by the first
     unsigned long long merged[kList]; // of all CTAs, at the first
     unsigned long long warp_sum[kWarps], part_sum[kWarps];
     unsigned long long cta_sum[kMaxCtas], cta_above[kMaxCtas];
     unsigned long long kept;      // the sum of what is kept, from the first CTA
-    float hi, lo;                 // the bracket of the top-p border
-    int good;                     // the bracket held it
+    float least;                  // the smallest logit that min-p keeps; one over the sum
+    int good;                     // the bracket of the top-p border held it; min-p decides alone
     unsigned long long cta_top[kMaxCtas];
     uint32_t cta_low[kMaxCtas];
     uint32_t cta_lo[kMaxCtas], cta_hi[kMaxCtas];
     unsigned int cta_ties[kMaxCtas];
     Scale scale;
     Cut cut;
-    unsigned long long before_mass;
+    unsigned long long before_mass, want[3];
     unsigned int n_list, n_merged, base;
     unsigned int bin, in_bin, before_count;
     int found;
@@ -195,6 +224,16 @@ __device__ __forceinline__ unsigned long long warp_total(unsigned long long x) {
     return x;
 }
 
+// What a share p of a sum asks for, rounded up, one at least; and where u of it ends.  64-bit
+// floating point is a small unit's work here: one thread does it and shares the result.
+__device__ __forceinline__ unsigned long long share_of(float p, unsigned long long total) {
+    const double x = ceil((double)p * (double)total);
+    return x < 1.0 ? 1ull : (unsigned long long)x;
+}
+__device__ __forceinline__ unsigned long long part_of(float u, unsigned long long total) {
+    return (unsigned long long)((double)u * (double)total);
+}
+
 // A row's elements as 16-byte vectors from the boundary at or before its start: vector v
 // holds the elements v * VEC - shift and so on; the outer ones are loaded one by one.
 template <typename Elem>
@@ -208,6 +247,12 @@ struct Row {
         vectors = (shift + V + VEC - 1) / VEC;
     }
     __device__ __forceinline__ bool has(int i) const { return (unsigned)i < (unsigned)V; }
+    __device__ __forceinline__ static float most(const float (&x)[VEC]) {
+        float y = x[0];
+#pragma unroll
+        for (int z = 1; z < VEC; ++z) y = fmaxf(y, x[z]);
+        return y;  // (NaN only where all are)
+    }
     // (-inf where the row has no element)
     __device__ __forceinline__ uint4 load(int v, int end) const {
         const int i = v * VEC - shift;
@@ -225,10 +270,10 @@ struct Row {
         }
         return w;
     }
-    // f(vector, logits) for the vectors [lo, hi), by one warp.
-    template <typename F>
+    // f(vector, logits) for the vectors [lo, hi), by one warp, BATCH elements a lane at once.
+    template <int BATCH = kBatch, typename F>
     __device__ __forceinline__ void vectors_of(int lo, int hi, F f) const {
-        constexpr int N = kBatch / VEC;
+        constexpr int N = BATCH / VEC;
         for (int v0 = lo + (int)(threadIdx.x & 31); v0 < hi; v0 += 32 * N) {
             uint4 w[N];
 #pragma unroll
@@ -271,6 +316,28 @@ __device__ __forceinline__ void sort_falling(Shared& sh, int n) {
     const int tid = threadIdx.x;
     int size = 32;
     while (size < n) size <<= 1;
+    if (size <= kThreads) {  // a number a thread: most steps stay within a warp
+        unsigned long long v = tid < n ? sh.merged[tid] : 0;
+#pragma unroll 1
+        for (int k = 2; k <= size; k <<= 1)
+#pragma unroll 1
+            for (int j = k >> 1; j; j >>= 1) {
+                unsigned long long o;
+                if (j >= 32) {
+                    __syncthreads();
+                    sh.merged[tid] = v;
+                    __syncthreads();
+                    o = sh.merged[tid ^ j];
+                } else {
+                    o = __shfl_xor_sync(0xffffffffu, v, j);
+                }
+                if ((o > v) == (((tid & j) == 0) == ((tid & k) == 0))) v = o;
+            }
+        __syncthreads();
+        sh.merged[tid] = v;
+        __syncthreads();
+        return;
+    }
     for (int i = n + tid; i < size; i += kThreads) sh.merged[i] = 0;
     __syncthreads();
     for (int k = 2; k <= size; k <<= 1)
@@ -338,7 +405,8 @@ struct Picker {
         }
         const uint32_t key = ((top_key >> kOrderShift) - sh.bin) << kOrderShift;
         from = key > kLowest ? logit_of(key) : -INFINITY;
-        row.vectors_of(wlo, whi, [&](int v, const float (&x)[Row<Elem>::VEC]) {
+        row.template vectors_of<2 * kBatch>(wlo, whi, [&](int v, const float (&x)[Row<Elem>::VEC]) {
+            if (row.most(x) >= from)
 #pragma unroll
             for (int z = 0; z < Row<Elem>::VEC; ++z)
                 if (x[z] >= from && row.has(v * Row<Elem>::VEC - row.shift + z))
@@ -402,7 +470,7 @@ struct Picker {
                     if (o < klo || o > khi) return;
                     b = (int)((khi - o) >> shift);
                 }
-                const unsigned long long u = mass ? fixed_of(weight_of(sh.table, s, x)) : 0;
+                const unsigned long long u = mass ? fixed_of(sh.table, s, x) : 0;
                 if (round == 0 && b == kBins - 1) {  // most of a steep row
                     ++last_n;
                     last_w += u;
@@ -442,8 +510,9 @@ struct Picker {
             const unsigned long long mine = mass ? w : n, end = block_sums(sh, mine, total);
             if (round == 0) {
                 if (mass) {
-                    const double x = ceil((double)p * (double)total);
-                    want = x < 1.0 ? 1ull : (unsigned long long)x;
+                    if (tid == 0) sh.want[0] = share_of(p, total);
+                    __syncthreads();
+                    want = sh.want[0];
                 } else {
                     want = count;
                 }
@@ -524,7 +593,7 @@ struct Picker {
                 // ties: as many as are needed, in index order
                 unsigned long long need = want - above;
                 if (mass) {
-                    const unsigned long long each = fixed_of(weight_of(sh.table, s, logit_of(klo)));
+                    const unsigned long long each = fixed_of(sh.table, s, logit_of(klo));
                     need = each ? (need + each - 1) / each : in_bin;
                 }
                 out.key = klo;
@@ -550,7 +619,7 @@ struct Picker {
             for (int i0 = 0; i0 < m && before < need; i0 += kThreads) {
                 const int i = i0 + tid;
                 const unsigned long long u =
-                    i < m ? fixed_of(weight_of(sh.table, s, logit_of((uint32_t)(sh.merged[i] >> 32)))) : 0;
+                    i < m ? fixed_of(sh.table, s, logit_of((uint32_t)(sh.merged[i] >> 32))) : 0;
                 unsigned long long total;
                 const unsigned long long end = block_sums(sh, u, total) + before;
                 if (i < m && end >= need && end - u < need) set_cut(sh.merged[i]);
@@ -572,22 +641,19 @@ struct Picker {
 #pragma unroll
         for (int k = 0; k < kList / kThreads; ++k) {
             u[k] = k < per && lo + k < m
-                       ? fixed_of(weight_of(sh.table, s, logit_of((uint32_t)(sh.merged[lo + k] >> 32))))
+                       ? fixed_of(sh.table, s, logit_of((uint32_t)(sh.merged[lo + k] >> 32)))
                        : 0;
             mine += u[k];
         }
         unsigned long long at = block_sums(sh, mine, total) - mine;
-        unsigned long long want = total;
-        if (p < 1.f) {
-            const double x = ceil((double)p * (double)total);
-            want = x < 1.0 ? 1ull : (unsigned long long)x;
-        }
         if (tid == 0) {
             sh.found = m;
             set_cut(sh.merged[m - 1]);
+            if (p < 1.f) sh.want[0] = share_of(p, total);
         }
         __syncthreads();
         if (p < 1.f) {
+            const unsigned long long want = sh.want[0];
 #pragma unroll
             for (int k = 0; k < kList / kThreads; ++k) {
                 if (u[k] > 0 && at < want && at + u[k] >= want) {
@@ -667,7 +733,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     const float p = a.top_p ? a.top_p[r] : 1.f, m = a.min_p ? a.min_p[r] : 0.f;
     const float u = !kProbs ? a.u[r] : 0.f;
     const int k = a.top_k ? a.top_k[r] : 0;
-    if (tid < 16) sh.table.v[tid] = table.v[tid];
+    if (tid < 16) {
+        sh.table.fixed[tid] = table.fixed[tid];
+        sh.table.low[tid] = table.low[tid];
+    }
     const Row<Elem> row(static_cast<const Elem*>(a.logits) + (size_t)r * V, V);
     const int share = (row.vectors + ctas - 1) / ctas, lo = min(rank * share, row.vectors),
               hi = min(lo + share, row.vectors);
@@ -676,6 +745,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
 
     constexpr int VEC = Row<Elem>::VEC;
     const bool first_k = k > 0 && k < V;
+    if (tid == kThreads - 1) {
+        const double c = 23.083120654223414 / (double)T;  // 16 log2(e)
+        sh.scale.c = (float)c;
+        sh.scale.c_low = (float)(c - (double)(float)c);
+    }
     if (first_k) {
         for (int i = tid; i < kOrders; i += kThreads) sh.orders[i] = 0;
         __syncthreads();
@@ -805,18 +879,31 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         return;
     }
     if (tid == 0) {
-        const double c = 23.083120654223414 / (double)T;  // 16 log2(e)
-        sh.scale.top = logit_of(top_key);
-        sh.scale.c = (float)c;
-        sh.scale.c_low = (float)(c - (double)(float)c);
+        const float x = logit_of(top_key);
+        const double y = (double)x * ((double)sh.scale.c + (double)sh.scale.c_low);
+        sh.scale.top = x;
+        sh.scale.fast = fabs(y) < 65536.0;
+        sh.scale.whole = rintf((float)y * 64.f) * 0.015625f;
+        sh.scale.rest = (float)(y - (double)sh.scale.whole);
     }
     __syncthreads();
     const Scale s = sh.scale;
-    const float least_w = fminf(m, 1.f);
-    // heavy enough for min-p
-    auto heavy = [&](const Weight& w) {
-        return w.hi > least_w || (w.hi == least_w && w.lo >= 0.f);
-    };
+    if (warp == 0) {
+        // the smallest logit that min-p keeps: 32 orders a round
+        uint32_t lo_key = kLowest, hi_key = top_key;  // hi_key is kept, lo_key not (or below all)
+        const float least_w = fminf(m, 1.f);
+        while (m > 0.f && hi_key - lo_key > 1) {
+            const uint32_t step = (hi_key - lo_key + 31) / 32;
+            const uint32_t key = lo_key + min(step * (lane + 1), hi_key - lo_key);
+            const uint32_t yes = __ballot_sync(0xffffffffu, at_least(sh.table, s, logit_of(key), least_w));
+            const int first = __ffs(yes) - 1;  // the last lane's is kept
+            hi_key = lo_key + min(step * (first + 1), hi_key - lo_key);
+            lo_key = first > 0 ? lo_key + step * first : lo_key;
+        }
+        if (lane == 0) sh.least = m > 0.f ? logit_of(hi_key) : -INFINITY;
+    }
+    __syncthreads();
+    const float least_x = sh.least;
 
     Picker<Elem> pick{sh, row, cluster, rank, ctas, wlo, whi, low};
     Cut cut{0u, 0x7fffffff};
@@ -830,69 +917,117 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
     if (!whole && !first_k) {
         float hi = -INFINITY, lo_x = -INFINITY;
-        if (p < 1.f) {
-            // approximate weights by distance from the largest logit
-            sh.rough[tid] = 0.f;
+        bool border = p < 1.f;  // top-p's has to be found
+        if (border) {
+            for (int i = tid; i < kOrders; i += kThreads) sh.orders[i] = 0;
             __syncthreads();
-            const float span = fminf(24.f * 16.f / s.c, s.top - logit_of(low));
-            const float per = span > 0.f && s.top < INFINITY ? fminf((kBins - 2) / span, 1e30f) : 1.f;
-            const float c = s.c * 0.0625f;
-            float rest = 0.f;
+            // bins of a 128th of a factor of two, as far as 2^-32 (or the smallest logit)
+            const float span = fminf(32.f * 16.f / s.c, s.top - logit_of(low));
+            const float per = span > 0.f && s.top < INFINITY ? fminf((kOrders - 2) / span, 1e30f) : 1.f;
+            unsigned int behind = 0;
             row.vectors_of(wlo, whi, [&](int, const float (&x)[VEC]) {
 #pragma unroll
                 for (int z = 0; z < VEC; ++z) {
-                    const float d = s.top - x[z];
-                    const float w = fast_exp2(-d * c);
-                    const int b = __float_as_int(fminf(d * per, (float)(kBins - 1)) + kMagic) & 0x7ff;
-                    if (b < kBins - 1)
-                        atomicAdd(&sh.rough[b], w);
-                    else if (w == w)
-                        rest += w;
+                    const float d = fminf((s.top - x[z]) * per, (float)(kOrders - 1));  // NaN: the last
+                    const int b = __float_as_int(d + kMagic) & (kOrders - 1);
+                    if (b < kOrders - 1)
+                        atomicAdd(&sh.orders[b], 1u);
+                    else
+                        ++behind;
                 }
             });
-#pragma unroll
-            for (int d = 16; d; d >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, d);
-            if (lane == 0 && rest > 0.f) atomicAdd(&sh.rough[kBins - 1], rest);
+            behind = __reduce_add_sync(0xffffffffu, behind);
+            if (lane == 0 && behind) atomicAdd(&sh.orders[kOrders - 1], behind);
             cluster_sync();
-            float mine = 0.f;
-            for (int c2 = 0; c2 < ctas; ++c2) mine += cluster.map_shared_rank(&sh.rough[0], c2)[tid];
-            // (in units of 2^-20, whole numbers from here on: every CTA gets the same bracket)
-            const float units = fminf(mine * 1048576.f, 1e18f);
-            const unsigned long long n = units > 0.f ? (unsigned long long)units : 0;
-            if (tid == 0) sh.bin = sh.base = kBins - 1;
-            unsigned long long total;
-            const unsigned long long end = block_sums(sh, n, total);
-            const double at_least = ((double)p - 1e-4) * (double)total,
-                         at_most = ((double)p + 1e-4) * (double)total;
-            if (at_least <= 0.0 ? tid == 0
-                                : (double)end > at_least && (double)(end - n) <= at_least)
-                sh.bin = tid;
-            if ((double)end > at_most && (double)(end - n) <= at_most) sh.base = tid;
-            __syncthreads();
-            // a bin's border lies half a bin before it
-            hi = sh.bin > 0 ? s.top - ((float)sh.bin - 0.5f) / per : INFINITY;
-            lo_x = sh.base < kBins - 1 ? s.top - ((float)sh.base + 0.5f) / per : -INFINITY;
-            __syncthreads();
-        }
-        // exact sums: of the row, above the bracket, and of what is kept there
-        unsigned long long all = 0, above = 0, kept = 0;
-        row.vectors_of(wlo, whi, [&](int v, const float (&x)[VEC]) {
+            // approximate weights in whole units of 2^-32: every CTA gets the same bracket
+            constexpr int kPer = kOrders / kThreads;
+            unsigned int n[kPer] = {};
+            for (int c = 0; c < ctas; ++c) {
+                const uint4* h = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&sh.orders[0], c)) +
+                                 tid * (kPer / 4);
 #pragma unroll
-            for (int z = 0; z < VEC; ++z) {
-                const Weight w = weight_of(sh.table, s, x[z]);
-                const unsigned long long q = fixed_of(w);
-                all += q;
-                if (x[z] > hi || p >= 1.f) {
-                    above += q;
-                    kept += heavy(w) ? q : 0;
-                } else if (x[z] >= lo_x && row.has(v * VEC - row.shift + z)) {
-                    pick.note(v * VEC - row.shift + z, x[z]);
+                for (int z = 0; z < kPer / 4; ++z) {
+                    const uint4 q = h[z];
+                    n[4 * z] += q.x;
+                    n[4 * z + 1] += q.y;
+                    n[4 * z + 2] += q.z;
+                    n[4 * z + 3] += q.w;
                 }
             }
-        });
+            unsigned long long w[kPer], mine = 0, total;
+#pragma unroll
+            for (int z = 0; z < kPer; ++z) {
+                const float e = 32.f - (float)(tid * kPer + z) * (s.c * 0.0625f) / per;
+                w[z] = (unsigned long long)n[z] * (unsigned long long)exp2f(fmaxf(e, -1.f));
+                mine += w[z];
+            }
+            if (tid == 0) {
+                sh.bin = sh.base = kOrders - 1;
+                sh.good = 0;
+            }
+            unsigned long long at = block_sums(sh, mine, total) - mine;
+            if (tid == 0) {
+                const double want = (double)p * (double)total,
+                             off = 1e-3 * fmin((double)p, 1.0 - (double)p) * (double)total;
+                sh.want[0] = (unsigned long long)fmax(want - off, 0.0);
+                sh.want[1] = (unsigned long long)fmax(want + off, 0.0);
+                sh.want[2] = (unsigned long long)fmax(want * 0.99, 0.0);
+            }
+            __syncthreads();
+            const unsigned long long from_w = sh.want[0], to_w = sh.want[1], surely = sh.want[2];
+            // where min-p cuts: a bin's weights are within 0.3 % of its middle's
+            const int bin_m = (int)fminf((s.top - least_x) * per + 0.5f, (float)(kOrders - 1));
+#pragma unroll
+            for (int z = 0; z < kPer; ++z) {
+                const int b = tid * kPer + z;
+                const unsigned long long end = at + w[z];
+                if (end > from_w && at <= from_w) sh.bin = b;
+                if (end > to_w && at <= to_w) sh.base = b;
+                if (b == bin_m + 1 && at < surely) sh.good = 1;
+                at = end;
+            }
+            __syncthreads();
+            // a bin's border lies half a bin before it; one bin more on either side
+            const int b0 = (int)sh.bin - 1, b1 = (int)sh.base + 1;
+            hi = b0 > 0 ? s.top - ((float)b0 - 0.5f) / per : INFINITY;
+            lo_x = b1 < kOrders - 1 ? s.top - ((float)b1 + 0.5f) / per : -INFINITY;
+            if (sh.good) border = false;
+            __syncthreads();
+        }
+        summed = true;
+        unsigned long long all = 0, above = 0, kept = 0;
+        if (!border && least_x > -INFINITY) {
+            // min-p's alone: the sum of the few that it keeps
+            row.template vectors_of<2 * kBatch>(wlo, whi, [&](int, const float (&x)[VEC]) {
+                if (row.most(x) >= least_x)
+#pragma unroll 1
+                    for (int z = 0; z < VEC; ++z) {
+                        float y = x[0];
+#pragma unroll
+                        for (int k2 = 1; k2 < VEC; ++k2) y = z == k2 ? x[k2] : y;
+                        if (y >= least_x) kept += fixed_of(sh.table, s, y);
+                    }
+            });
+        } else {
+            // exact sums: of the row, above the bracket (without one: all), and of what is
+            // kept there
+            row.vectors_of(wlo, whi, [&](int v, const float (&x)[VEC]) {
+#pragma unroll
+                for (int z = 0; z < VEC; ++z) {
+                    const unsigned long long q = fixed_of(sh.table, s, x[z]);
+                    all += q;
+                    if (x[z] > hi) {
+                        above += q;
+                        kept += x[z] >= least_x ? q : 0;
+                    } else if (border && x[z] >= lo_x && row.has(v * VEC - row.shift + z)) {
+                        pick.note(v * VEC - row.shift + z, x[z]);
+                    }
+                }
+            });
+        }
+        kept = warp_total(kept);
         all = warp_total(all);
         above = warp_total(above);
-        kept = warp_total(kept);
         __syncthreads();
         if (lane == 0) {
             sh.part_sum[warp] = kept;
@@ -900,8 +1035,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             sh.merged[warp] = above;  // before any CTA sends
         }
         __syncthreads();
-        summed = true;
-        if (p < 1.f) {
+        if (!border) {
+            cut.key = order_of(least_x);
+        } else {
             if (warp == 0) {
                 const unsigned long long t = warp_total(lane < kWarps ? sh.warp_sum[lane] : 0);
                 const unsigned long long b = warp_total(lane < kWarps ? sh.merged[lane] : 0);
@@ -918,8 +1054,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                     total += sh.cta_sum[c];
                     over += sh.cta_above[c];
                 }
-                const double x = ceil((double)p * (double)total);
-                const unsigned long long want = x < 1.0 ? 1ull : (unsigned long long)x;
+                if (tid == 0) sh.want[0] = share_of(p, total);
+                __syncthreads();
+                const unsigned long long want = sh.want[0];
                 const int n = (int)min(sh.n_merged, (unsigned int)kList);
                 bool good = sh.n_merged <= kList && n > 0 && want > over;
                 if (good) {
@@ -939,9 +1076,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                 for (unsigned int i = tid; i < sh.n_list; i += kThreads) {
                     const uint32_t o = (uint32_t)(sh.list[i] >> 32);
                     const int at = (int)(0xffffffffu - (uint32_t)sh.list[i]);
-                    const Weight w = weight_of(sh.table, s, logit_of(o));
-                    if (cut.keeps(o, at) && heavy(w))
-                        atomicAdd(&sh.part_sum[((at + row.shift) / VEC - lo) / part], fixed_of(w));
+                    if (cut.keeps(o, at) && logit_of(o) >= least_x)
+                        atomicAdd(&sh.part_sum[((at + row.shift) / VEC - lo) / part],
+                                  fixed_of(sh.table, s, logit_of(o)));
                 }
             } else {
                 pick.find(0u, p, cut, true, cut);
@@ -969,8 +1106,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         for (int z = 0; z < kList / kThreads; ++z) {
             w[z] = 0;
             if (z < per && at0 + z < n) {
-                const Weight x = weight_of(sh.table, s, logit_of((uint32_t)sh.merged[at0 + z]));
-                w[z] = heavy(x) ? fixed_of(x) : 0;
+                const float x = logit_of((uint32_t)sh.merged[at0 + z]);
+                w[z] = x >= least_x ? fixed_of(sh.table, s, x) : 0;
             }
             mine += w[z];
         }
@@ -981,7 +1118,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                 *cluster.map_shared_rank(&sh.kept, tid) = total;
             }
         } else {
-            const unsigned long long want = (unsigned long long)((double)u * (double)total);
+            if (tid == 0) sh.want[0] = part_of(u, total);
+            __syncthreads();
+            const unsigned long long want = sh.want[0];
 #pragma unroll
             for (int z = 0; z < kList / kThreads; ++z) {
                 if (at <= want && at + w[z] > want)
@@ -993,9 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     if (!kProbs && whole) return;
 
     auto counted = [&](int i, float x) -> unsigned long long {
-        if (!cut.keeps(order_of(x), i)) return 0;
-        const Weight w = weight_of(sh.table, s, x);
-        return heavy(w) ? fixed_of(w) : 0;
+        return x >= least_x && cut.keeps(order_of(x), i) ? fixed_of(sh.table, s, x) : 0;
     };
     unsigned long long total = 0, before = 0;
     if (!whole) {
@@ -1023,23 +1160,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         total = sh.kept;
     }
     if constexpr (kProbs) {
-        const float inv = (float)((double)kOne / (double)total);
-        const float least_x = logit_of(max(cut.key, kLowest));
+        if (tid == 0) sh.least = (float)((double)kOne / (double)total);
+        __syncthreads();
+        const float inv = sh.least;
+        const float from_x = fmaxf(least_x, logit_of(max(cut.key, kLowest)));
         row.vectors_of(wlo, whi, [&](int v, const float (&x)[VEC]) {
             float y[VEC];
 #pragma unroll
             for (int z = 0; z < VEC; ++z) {
                 y[z] = 0.f;
-                if (x[z] >= least_x && cut.keeps(order_of(x[z]), v * VEC - row.shift + z)) {
-                    const Weight w = weight_of(sh.table, s, x[z]);
-                    if (heavy(w)) y[z] = w.hi * inv;
-                }
+                if (x[z] >= from_x && cut.keeps(order_of(x[z]), v * VEC - row.shift + z))
+                    y[z] = weight_of(sh.table, s, x[z]) * inv;
             }
             put(v, y);
         });
         return;
     }
-    const unsigned long long want = (unsigned long long)((double)u * (double)total);
+    if (tid == 0) sh.want[0] = part_of(u, total);
+    __syncthreads();
+    const unsigned long long want = sh.want[0];
     if (want < before || want >= before + sh.cta_sum[rank]) return;
     // in this CTA: the warp's part, a sixteenth of it a warp, then in order
     unsigned long long at = before;
@@ -1088,7 +1227,10 @@ cudaError_t go_sample(const SampleArgs& a, cudaStream_t stream) {
     Table t;
     for (int j = 0; j < 16; ++j) {
         const double x = exp2(j / 16.0);
-        t.v[j] = make_float2((float)x, (float)(x - (double)(float)x));
+        const float y = (float)(x * 2147483648.0);
+        t.fixed[j].x = (uint32_t)(unsigned long long)(x * 2147483648.0 + 0.5);
+        memcpy(&t.fixed[j].y, &y, 4);
+        t.low[j] = (float)(x - (double)(float)x);
     }
     // CTAs a row: while two an SM are not passed, with 2048 elements a CTA at least; a
     // share of 2^17 at most, so that a bin's words of 14 bits hold its sums

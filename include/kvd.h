@@ -934,10 +934,9 @@ kvd_status kvd_attend_paged_prefix(const void* q, const void* key_cache, const v
  *   top_k [R] int32, device, or NULL (1, all, all, all);  u [R] float in [0, 1)
  *   tokens [R] int32
  * NaN logits count as -inf; among infinite ones the weight is shared alike.
- * Weights are right to about 2^-34 of the largest (a small one to 2^-29 of itself)
- * and are summed as whole multiples of 2^-42 of the largest, in any order to the same
- * sum: only a draw or a top-p border closer than that to a token's border can differ
- * from one in 64 bits.
+ * Weights are right to about 2^-28 of themselves, without a trend, and are summed as
+ * whole multiples of 2^-42 of the largest, in any order to the same sum: a draw or a
+ * top-p border that differs from one in 64 bits lies within 2^-28 of a token's border.
  * A row without a logit above -inf gives -1 (KVD_DEV_PROBS); a NaN, a temperature
  * below 0 or above 1e30, or u outside [0, 1) gives -1 (KVD_DEV_PARAM).
  * V at most 2^20.

@@ -139,6 +139,21 @@ def test_all_equal_and_steep(kvd):
     same(kvd, tail, u, p=torch.full((6,), 0.9975, device="cuda"))
 
 
+@pytest.mark.parametrize("shift,T", [(100.0, 0.01), (-3000.0, 0.7), (2.0 ** 20, 30.0)])
+def test_logits_far_from_zero(kvd, shift, T):
+    """The largest logit over the temperature up to 4 * 10^4: the differences count, taken
+    before anything is rounded (the logits lie on fp32's grid there)."""
+    R, V = 12, 7001
+    g = torch.Generator().manual_seed(11)
+    logits = (torch.randn(R, V, generator=g) * 3 * T + shift).cuda()
+    u = torch.rand(R, generator=g).cuda()
+    _, k, p, m = settings(R, g)
+    temp = torch.full((R,), T, device="cuda")
+    same(kvd, logits, u, T=temp)
+    same(kvd, logits, u, T=temp, p=p)
+    same(kvd, logits, u, T=temp, k=k, p=p, m=m)
+
+
 def test_infinities_and_nan(kvd):
     V = 5000
     g = torch.Generator().manual_seed(9)
