@@ -42,6 +42,7 @@ constexpr int kBins = kThreads;  // a thread a bin when they are added up
 // Bits of an order that its bin of the first pass leaves out: eight bins a factor of two
 // (finer ones take longer to clear and to add up, and a list holds 2048 elements).
 constexpr int kOrderShift = 20, kOrders = 1 << (32 - kOrderShift);
+constexpr int kFine = 2048;      // bins of the second pass
 constexpr int kList = 2048;      // elements that one CTA sorts
 constexpr int kBatch = 16;       // elements that a lane loads at once
 constexpr unsigned long long kOne = 1ull << 42;  // the weight 1
@@ -122,14 +123,30 @@ __device__ __forceinline__ Split split_of(const Scale& s, float x) {
 
 // A weight in multiples of 2^-42.  (Every operation rounds as written: all passes must get
 // the same.)
-__device__ __forceinline__ unsigned long long fixed_of(const Table& t, const Scale& s, float x) {
-    if (x == s.top) return kOne;
-    const Split p = split_of(s, x);
-    if (p.n <= -688) return 0;  // half a unit
-    const uint2 e = t.fixed[p.n & 15];
-    const uint32_t v = e.x + (uint32_t)__float2int_rn(__fmul_rn(__uint_as_float(e.y), p.q));
+__device__ __forceinline__ unsigned long long fixed_fast(const Table& t, const Scale& s, float x) {
+    // (far below, -inf and NaN: shifted out whatever the polynomial gives)
+    const float y = fmaxf(__fmaf_rn(x, s.c, -s.whole), -704.f);
+    const float r = __fadd_rn(y, kMagic), n = __fsub_rn(r, kMagic);
+    const float f = __fadd_rn(__fmaf_rn(x, s.c, -__fadd_rn(n, s.whole)), __fmaf_rn(x, s.c_low, -s.rest));
+    const uint2 e = t.fixed[__float_as_int(r) & 15];
+    const uint32_t v =
+        e.x + (uint32_t)__float2int_rn(__fmul_rn(__uint_as_float(e.y), power_of(f)));
     // units of 2^-31 of a factor of two down to those of 2^-42 of one, rounded
-    return ((((unsigned long long)v << 32) >> (20 - (p.n >> 4))) + 1) >> 1;
+    const int down = (__float_as_int(kMagic) + 15 - __float_as_int(r)) >> 4;
+    if (down >= 12) return (__funnelshift_rc(v, 0u, down - 12) + 1u) >> 1;
+    return (unsigned long long)v << (11 - down);
+}
+__device__ __noinline__ unsigned long long fixed_slow(const Table& t, const Scale& s, float x) {
+    if (x == s.top) return kOne;
+    const int2 w = split_slow(s, x);
+    if (w.x <= -688) return 0;  // half a unit
+    const uint2 e = t.fixed[w.x & 15];
+    const uint32_t v =
+        e.x + (uint32_t)__float2int_rn(__fmul_rn(__uint_as_float(e.y), __int_as_float(w.y)));
+    return ((((unsigned long long)v << 32) >> (20 - (w.x >> 4))) + 1) >> 1;
+}
+__device__ __forceinline__ unsigned long long fixed_of(const Table& t, const Scale& s, float x) {
+    return s.fast ? fixed_fast(t, s, x) : fixed_slow(t, s, x);
 }
 
 // The same as a number; and whether it is at least m, without that number's rounding.
@@ -888,8 +905,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
     __syncthreads();
     const Scale s = sh.scale;
-    if (warp == 0) {
-        // the smallest logit that min-p keeps: 32 orders a round
+    if (warp == kWarps - 1) {
+        // the smallest logit that min-p keeps: 32 orders a round (while the others go on; the
+        // barriers before its first use are the passes')
         uint32_t lo_key = kLowest, hi_key = top_key;  // hi_key is kept, lo_key not (or below all)
         const float least_w = fminf(m, 1.f);
         while (m > 0.f && hi_key - lo_key > 1) {
@@ -902,8 +920,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         }
         if (lane == 0) sh.least = m > 0.f ? logit_of(hi_key) : -INFINITY;
     }
-    __syncthreads();
-    const float least_x = sh.least;
 
     Picker<Elem> pick{sh, row, cluster, rank, ctas, wlo, whi, low};
     Cut cut{0u, 0x7fffffff};
@@ -919,28 +935,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         float hi = -INFINITY, lo_x = -INFINITY;
         bool border = p < 1.f;  // top-p's has to be found
         if (border) {
-            for (int i = tid; i < kOrders; i += kThreads) sh.orders[i] = 0;
+            for (int i = tid; i < kFine; i += kThreads) sh.orders[i] = 0;
             __syncthreads();
-            // bins of a 128th of a factor of two, as far as 2^-32 (or the smallest logit)
+            // bins of a 64th of a factor of two, as far as 2^-32 (or the smallest logit)
             const float span = fminf(32.f * 16.f / s.c, s.top - logit_of(low));
-            const float per = span > 0.f && s.top < INFINITY ? fminf((kOrders - 2) / span, 1e30f) : 1.f;
+            const float per = span > 0.f && s.top < INFINITY ? fminf((kFine - 2) / span, 1e30f) : 1.f;
             unsigned int behind = 0;
             row.vectors_of(wlo, whi, [&](int, const float (&x)[VEC]) {
 #pragma unroll
                 for (int z = 0; z < VEC; ++z) {
-                    const float d = fminf((s.top - x[z]) * per, (float)(kOrders - 1));  // NaN: the last
-                    const int b = __float_as_int(d + kMagic) & (kOrders - 1);
-                    if (b < kOrders - 1)
+                    const float d = fminf((s.top - x[z]) * per, (float)(kFine - 1));  // NaN: the last
+                    const int b = __float_as_int(d + kMagic) & (kFine - 1);
+                    if (b < kFine - 1)
                         atomicAdd(&sh.orders[b], 1u);
                     else
                         ++behind;
                 }
             });
             behind = __reduce_add_sync(0xffffffffu, behind);
-            if (lane == 0 && behind) atomicAdd(&sh.orders[kOrders - 1], behind);
+            if (lane == 0 && behind) atomicAdd(&sh.orders[kFine - 1], behind);
             cluster_sync();
             // approximate weights in whole units of 2^-32: every CTA gets the same bracket
-            constexpr int kPer = kOrders / kThreads;
+            constexpr int kPer = kFine / kThreads;
+            const float least_x = sh.least;
             unsigned int n[kPer] = {};
             for (int c = 0; c < ctas; ++c) {
                 const uint4* h = reinterpret_cast<const uint4*>(cluster.map_shared_rank(&sh.orders[0], c)) +
@@ -962,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                 mine += w[z];
             }
             if (tid == 0) {
-                sh.bin = sh.base = kOrders - 1;
+                sh.bin = sh.base = kFine - 1;
                 sh.good = 0;
             }
             unsigned long long at = block_sums(sh, mine, total) - mine;
@@ -971,12 +988,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                              off = 1e-3 * fmin((double)p, 1.0 - (double)p) * (double)total;
                 sh.want[0] = (unsigned long long)fmax(want - off, 0.0);
                 sh.want[1] = (unsigned long long)fmax(want + off, 0.0);
-                sh.want[2] = (unsigned long long)fmax(want * 0.99, 0.0);
+                sh.want[2] = (unsigned long long)fmax(want * 0.98, 0.0);
             }
             __syncthreads();
             const unsigned long long from_w = sh.want[0], to_w = sh.want[1], surely = sh.want[2];
-            // where min-p cuts: a bin's weights are within 0.3 % of its middle's
-            const int bin_m = (int)fminf((s.top - least_x) * per + 0.5f, (float)(kOrders - 1));
+            // where min-p cuts: a bin's weights are within 0.6 % of its middle's
+            const int bin_m = (int)fminf((s.top - least_x) * per + 0.5f, (float)(kFine - 1));
 #pragma unroll
             for (int z = 0; z < kPer; ++z) {
                 const int b = tid * kPer + z;
@@ -990,10 +1007,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             // a bin's border lies half a bin before it; one bin more on either side
             const int b0 = (int)sh.bin - 1, b1 = (int)sh.base + 1;
             hi = b0 > 0 ? s.top - ((float)b0 - 0.5f) / per : INFINITY;
-            lo_x = b1 < kOrders - 1 ? s.top - ((float)b1 + 0.5f) / per : -INFINITY;
+            lo_x = b1 < kFine - 1 ? s.top - ((float)b1 + 0.5f) / per : -INFINITY;
             if (sh.good) border = false;
             __syncthreads();
         }
+        if (!(p < 1.f)) __syncthreads();
+        const float least_x = sh.least;
         summed = true;
         unsigned long long all = 0, above = 0, kept = 0;
         if (!border && least_x > -INFINITY) {
@@ -1011,19 +1030,30 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         } else {
             // exact sums: of the row, above the bracket (without one: all), and of what is
             // kept there
-            row.vectors_of(wlo, whi, [&](int v, const float (&x)[VEC]) {
+            // (above its own: least_x only matters where it lies above the bracket)
+            const bool few = least_x > hi;
+            auto add = [&](auto weight) {
+                row.vectors_of(wlo, whi, [&](int v, const float (&x)[VEC]) {
 #pragma unroll
-                for (int z = 0; z < VEC; ++z) {
-                    const unsigned long long q = fixed_of(sh.table, s, x[z]);
-                    all += q;
-                    if (x[z] > hi) {
-                        above += q;
-                        kept += x[z] >= least_x ? q : 0;
-                    } else if (border && x[z] >= lo_x && row.has(v * VEC - row.shift + z)) {
-                        pick.note(v * VEC - row.shift + z, x[z]);
+                    for (int z = 0; z < VEC; ++z) {
+                        const unsigned long long q = weight(x[z]);
+                        if (x[z] > hi)
+                            above += q;
+                        else
+                            all += q;
+                        if (few && x[z] >= least_x) kept += q;
+                        if (border && x[z] <= hi && x[z] >= lo_x &&
+                            row.has(v * VEC - row.shift + z))
+                            pick.note(v * VEC - row.shift + z, x[z]);
                     }
-                }
-            });
+                });
+            };
+            if (s.fast)
+                add([&](float x) { return fixed_fast(sh.table, s, x); });
+            else
+                add([&](float x) { return fixed_slow(sh.table, s, x); });
+            all += above;
+            if (!few) kept = above;
         }
         kept = warp_total(kept);
         all = warp_total(all);
@@ -1090,6 +1120,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         cluster_sync();
         pick.find(0u, p, set, false, cut);
     }
+    const float least_x = sh.least;
     if (whole && rank == 0) {
         // the first CTA draws, or adds up, in index order
         const int n = sh.found;
