@@ -819,7 +819,7 @@ kvd_status kvd_verify_drafts(const void* target_probs, const void* draft_probs,
  * token whose page is negative or whose slot is past 2^31 - 1
  * (KVD_DEV_BLOCK_RANGE), or whose position is
  * outside 32 bits (KVD_DEV_POS_RANGE), has no place.  One launch; runs that
- * change the same tables must be ordered.  Q at most 2^20.
+ * change the same tables must be ordered.  Q at most 2^20, N at most 2^30.
  */
 kvd_status kvd_plan_pages(int32_t* block_tables, int32_t* pages_held, int32_t* free_pages,
                           int32_t* free_count, const int32_t* kept_lens, const int32_t* new_lens,

@@ -108,6 +108,25 @@ def test_one_long_sequence(kvd):
     same(kvd, st, st.device(), [0, 0], [0, 39999, 40001], 40001)
 
 
+@pytest.mark.parametrize("Q", [3, 700])
+def test_many_tokens(kvd, Q):
+    """More tokens than the planning kernel looks up itself: a pool that runs out, bad
+    pages, padding, and what refuses every sequence."""
+    n = 30000 // Q
+    for kind in range(4):
+        st = State(Q, -(-n // 16) + 3, Q * (-(-n // 16)) * 3 // 4 + Q, 16, [1] * Q, seed=kind)
+        kept, new = [5] * Q, cum([n - q % 7 for q in range(Q)])
+        N, base = new[-1] + 100, [q for q in range(Q)]
+        if kind == 1:
+            st.table[1][0] = -4
+            base[0] = -7
+        elif kind == 2:
+            new[Q // 2] = new[Q // 2 + 1] + 1
+        elif kind == 3:
+            st.count = [-1]
+        same(kvd, st, st.device(), kept, new, N, base)
+
+
 def test_padding_and_no_tokens(kvd):
     st = State(3, 4, 10, 8, [1, 0, 2], seed=3)
     dev = st.device()

@@ -28,7 +28,7 @@ def test_plan_pages_validates(lib):
     for bad in (dict(bt=None), dict(held=None), dict(free=None), dict(lens=None), dict(slots=None),
                 dict(Q=-1), dict(N=-1), dict(BS=0), dict(cols=0), dict(F=0), dict(bt=ODD)):
         assert call(**bad) == 1, bad
-    assert call(Q=(1 << 20) + 1) == 2
+    assert call(Q=(1 << 20) + 1) == 2 and call(N=(1 << 30) + 1) == 2
 
 
 def test_rotate_validates(lib):
