@@ -114,7 +114,9 @@ struct AttendParams {
     // The launch runs beside the kernel before it on the stream, which leaves SMs free and
     // whose results it does not read: that kernel waits for all before it and only then
     // lets this one start, so this one waits at its end, for the kernels behind it.  CTAs
-    // may start late, so every unit comes from the work counter.
+    // may start late, so every unit comes from the work counter; with a CTA a unit there is
+    // nothing to share out (4 sequences of 8 heads: from the counter, a CTA that starts first
+    // takes several and the call is 25 us long; a unit each, 16).
     int beside;
     int small_push;              // one-launch kernel: the splits push partials into split 0
     int small_nwg;               // one-launch kernel: consumer warp groups per CTA (1 or 2)
@@ -698,7 +700,8 @@ attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap kmap,
         // share their mask row or sequence, so that the metadata reads after
         // the first hit L1 -- else the first units are spread over all CTAs.
         const int n_sched = kSchedN * (int)gridDim.x;
-        const int first_units = p.beside ? 0 : n_sched;
+        const bool counted = p.beside && p.units > (int)gridDim.x;
+        const int first_units = counted ? 0 : n_sched;
         int u = p.units >= n_sched ? (int)blockIdx.x * kSchedN + sw
                                    : sw * (int)gridDim.x + (int)blockIdx.x;
         auto publish = [&](int slot) {
@@ -726,7 +729,7 @@ attend_kernel(const AttendParams p, const __grid_constant__ CUtensorMap kmap,
             }
             return __shfl_sync(0xffffffffu, ok, 0) != 0;
         };
-        bool first = !p.beside;
+        bool first = !counted;
         // Scheduler 0 of the static buffer publishes its first slot without
         // the lookahead gate: the loader waits for that slot first (its
         // unit's first tiles were loaded speculatively) and takes no other

@@ -16,7 +16,8 @@
 // above 128 rows) in a ring of eight blocks of 128 tokens x 64 elements.
 //
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, a row a thread; they also lay out the
-// queries.  Warp 8 issues the MMAs.  Warp 9 looks up pages and issues the copies.
+// queries.  Warp 8 issues the MMAs.  Warp 9 looks up pages and issues the copies.  Warp 10
+// writes what the merge has to know.
 #include "../kvd_internal.h"
 #include "../latent/latent_common.cuh"  // encode_rows, FastDiv, kTinyScale
 #include "../latent/tcgen05_ptx.cuh"
@@ -33,7 +34,8 @@ constexpr int kSteps = 4;            // steps with barriers of their own (the ri
 // i - 4 at the latest are complete, so that step i - 5 has been through the softmax.
 constexpr int kValid = 8;
 constexpr int kMmaWarp = 8, kCopyWarp = 9;
-constexpr int kThreads = 384;  // warps 10 and 11 complete the third warpgroup
+constexpr int kMetaWarp = 10;
+constexpr int kThreads = 384;  // warp 11 completes the third warpgroup
 // Registers a thread: the softmax holds a row of 128 scores.  2 x 208 + 80 is
 // within the 3 x 168 that three warpgroups start with.
 constexpr int kSoftmaxRegs = 208, kIssueRegs = 80;
@@ -198,6 +200,8 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
             while (global_timer_ns() - since < 1000000ull) {
             }
         }
+    } else if (warp == kMetaWarp) {
+        prefix_meta(a, sh.groups, runs, lane, 32);
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issue
         // One warp in a fixed order, S0(0) S1(0) PV0(0) S0(1) PV1(0) S1(1) PV0(1) ..: a warp

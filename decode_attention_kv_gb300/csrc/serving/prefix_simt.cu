@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(kThreads) prefix_simt_kernel(const PrefixArgs 
     pdl_wait();
     const int tid = threadIdx.x, row = tid >> 4, sub = tid & 15;
     const PrefixRuns runs = prefix_setup<kThreads>(a, groups);
+    prefix_meta(a, groups, runs, tid, kThreads);
     const int w = blockIdx.x;
     if (runs.tot == 0 || w >= runs.W) return;
     const int lo = runs.start(w), hi = runs.start(w + 1);
@@ -170,7 +171,7 @@ cudaError_t go_simt(const PrefixArgs& a, cudaStream_t stream) {
 // One warp an output row: the pieces of its prefix and the splits of its own keys, by
 // log-sum-exp; 32 partial rows at a time against a running maximum, a lane each for the
 // weights, then D / 32 dims a lane.
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 4, kMergeRows = 4;
 
 template <typename Out, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) prefix_combine_kernel(const PrefixArgs a) {
@@ -226,22 +227,30 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_combine_kernel(const 
         l *= corr;
 #pragma unroll
         for (int e = 0; e < kDims; ++e) acc[e] *= corr;
-        for (int j = 0; j < min(32, n - i0); ++j) {
-            const float f = __shfl_sync(0xffffffffu, wt, j);
-            const float* o = reinterpret_cast<const float*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j));
-            if (f == 0.f) continue;  // an empty range's row was not written
-            l += f;
-            if constexpr (kDims == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(o + 4 * lane);
-                acc[0] = fmaf(f, x.x, acc[0]);
-                acc[1] = fmaf(f, x.y, acc[1]);
-                acc[2] = fmaf(f, x.z, acc[2]);
-                acc[3] = fmaf(f, x.w, acc[3]);
-            } else {
-                const float2 x = *reinterpret_cast<const float2*>(o + 2 * lane);
-                acc[0] = fmaf(f, x.x, acc[0]);
-                acc[1] = fmaf(f, x.y, acc[1]);
+        const int many = min(32, n - i0);
+        for (int j0 = 0; j0 < many; j0 += kMergeRows) {
+            float f[kMergeRows], x[kMergeRows][kDims];
+#pragma unroll
+            for (int j = 0; j < kMergeRows; ++j) {
+                f[j] = __shfl_sync(0xffffffffu, wt, min(j0 + j, 31));
+                const float* o = reinterpret_cast<const float*>(__shfl_sync(
+                    0xffffffffu, reinterpret_cast<unsigned long long>(src), min(j0 + j, 31)));
+                if (j0 + j >= many) f[j] = 0.f;
+                // an empty range's row was not written
+#pragma unroll
+                for (int e = 0; e < kDims; ++e) x[j][e] = 0.f;
+                if (f[j] != 0.f) {
+                    if constexpr (kDims == 4)
+                        *reinterpret_cast<float4*>(x[j]) = *reinterpret_cast<const float4*>(o + 4 * lane);
+                    else
+                        *reinterpret_cast<float2*>(x[j]) = *reinterpret_cast<const float2*>(o + 2 * lane);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kMergeRows; ++j) {
+                l += f[j];
+#pragma unroll
+                for (int e = 0; e < kDims; ++e) acc[e] = fmaf(f[j], x[j][e], acc[e]);
             }
         }
     }

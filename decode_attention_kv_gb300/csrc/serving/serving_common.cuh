@@ -75,21 +75,27 @@ __device__ __forceinline__ int last_not_above(const int* x, int n, int v) {
     return lo;
 }
 
-// One worker's run [first, first + n) of the line: worker w takes
-// [floor(w tot / W), floor((w + 1) tot / W)).
+// The line over W workers: worker w takes [start(w), start(w + 1)), start(w) = floor(w tot / W),
+// in 32 bits (W is a few hundred, tot below 2^30).
 struct PrefixRuns {
-    int tot, W;
-    __device__ __forceinline__ PrefixRuns(int tot_, int W_) : tot(tot_), W(W_) {}
-    __device__ __forceinline__ int start(int w) const { return (int)((long long)w * tot / W); }
+    int tot, W, per, rest;
+    __device__ __forceinline__ PrefixRuns(int tot_, int W_) : tot(tot_), W(W_) {
+        per = tot / W;
+        rest = tot - per * W;
+    }
+    __device__ __forceinline__ int start(int w) const { return w * per + w * rest / W; }
     __device__ __forceinline__ int worker_of(int place) const {
-        return (int)((((long long)place + 1) * W - 1) / tot);
+        int w = min(W - 1, (int)((float)place * (float)W / (float)tot));  // or one beside it
+        while (w > 0 && start(w) > place) --w;
+        while (w + 1 < W && start(w + 1) <= place) ++w;
+        return w;
     }
 };
 
-// By all threads of a CTA: reads and checks the groups, lays out the line, writes this
-// CTA's share of the meta rows; returns the line's division.  The attention over the
-// sequences' own keys, which is launched behind, runs beside this kernel: it may start
-// from here on, when everything before both is complete and its counters are zero.
+// By all threads of a CTA: reads and checks the groups, lays out the line; returns its
+// division.  The attention over the sequences' own keys, which is launched behind, runs
+// beside this kernel: it may start from here on, when everything before both is complete
+// and its counters are zero.
 template <int THREADS>
 __device__ __forceinline__ PrefixRuns prefix_setup(const PrefixArgs& a, PrefixGroups& t) {
     const int tid = threadIdx.x;
@@ -151,19 +157,25 @@ __device__ __forceinline__ PrefixRuns prefix_setup(const PrefixArgs& a, PrefixGr
         const float mine = a.place_cost * (float)tot, theirs = a.token_cost * (float)own;
         W = max(1, min(W, (int)(a.workers * mine / (mine + theirs) + 0.5f)));
     }
-    for (int q = blockIdx.x * THREADS + tid; q <= a.Q; q += gridDim.x * THREADS) {
+    return PrefixRuns(tot, W);
+}
+
+// The CTA's share of the meta rows, by `threads` of its threads (without groups t.base[G] is
+// 0, and a bad group_lens leaves no places).
+__device__ __forceinline__ void prefix_meta(const PrefixArgs& a, const PrefixGroups& t,
+                                            const PrefixRuns& runs, int thread, int threads) {
+    for (int q = blockIdx.x * threads + thread; q <= a.Q; q += gridDim.x * threads) {
         int4 m = make_int4(0, 0, 0, 0);
         if (q == a.Q) {
-            m.x = tot;
-            m.y = W;
-        } else if (!bad && a.G > 0 && q < t.start[a.G]) {
+            m.x = runs.tot;
+            m.y = runs.W;
+        } else if (runs.tot > 0 && q < t.start[a.G]) {
             const int i = last_not_above(t.start, a.G, q);
             m = make_int4(t.base[i], ceil_div(t.sequences(i) * a.g, a.rows),
                           ceil_div(t.keys[i], a.keys), q - t.start[i]);
         }
         a.meta[q] = m;
     }
-    return PrefixRuns(tot, W);
 }
 
 // The piece of a segment that a run holds.
