@@ -17,6 +17,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <array>
 #include <initializer_list>
 #include <string>
 
@@ -111,6 +112,25 @@ struct Call {
         }
         return at::empty(at::IntArrayRef(shape.begin(), shape.size()),
                          at::TensorOptions().dtype(dtype).device(at::kCUDA, (c10::DeviceIndex)dev));
+    }
+    // New int32 outputs in one allocation, each from a 256-byte boundary of it (an allocation
+    // takes the host a microsecond, such a view a tenth of one).
+    template <size_t K>
+    std::array<at::Tensor, K> outputs(const int64_t (&lengths)[K]) const {
+        int64_t total = 0;
+        for (int64_t n : lengths) total += (n + 63) / 64 * 64;
+        const at::Tensor all = at::empty(
+            {total}, at::TensorOptions().dtype(at::kInt).device(at::kCUDA, (c10::DeviceIndex)dev));
+        std::array<at::Tensor, K> out;
+        int64_t at = 0;
+        for (size_t i = 0; i < K; ++i) {
+            out[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()),
+                                                              all.key_set(), all.dtype());
+            out[i].unsafeGetTensorImpl()->set_storage_offset(at);
+            out[i].unsafeGetTensorImpl()->set_sizes_contiguous(lengths[i]);
+            at += (lengths[i] + 63) / 64 * 64;
+        }
+        return out;
     }
     int32_t* status(int i) const {
         if (!given(i)) return nullptr;
@@ -380,8 +400,15 @@ PyObject* plan_pages(Call& c) {
     int32_t* status = c.status(12);
     const int q = c.small(Q, "block_tables"), co = c.small(cols, "block_tables"),
               f = c.small(F, "free_pages");
-    at::Tensor sl = c.output(9, "seq_lens", kI32, {Q + 1}), st = c.output(10, "slots", kI32, {n}),
-               ps = c.output(11, "positions", kI32, {n});
+    at::Tensor sl, st, ps;
+    if (!c.given(9) && !c.given(10) && !c.given(11)) {
+        auto o = c.outputs<3>({Q + 1, n, n});
+        sl = o[0], st = o[1], ps = o[2];
+    } else {
+        sl = c.output(9, "seq_lens", kI32, {Q + 1});
+        st = c.output(10, "slots", kI32, {n});
+        ps = c.output(11, "positions", kI32, {n});
+    }
     c.run("kvd_plan_pages", [&](kvd_stream_t s) {
         return g_plan_pages(tables, held, pages, count, kept, lens, base, ints(sl.data_ptr()),
                             ints(st.data_ptr()), ints(ps.data_ptr()), q, n, bs, co, f, status, s);
