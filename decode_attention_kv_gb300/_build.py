@@ -2,11 +2,11 @@
 
 Each translation unit compiles in parallel into ``_build/`` and is linked
 into ``decode_attention_kv_gb300/libkvd.so`` (CUDA runtime linked
-statically).  The host binding of the latent calls (csrc/binding) compiles
-beside them against the installed torch, into a file named for that torch and
-this Python.  libkvd.so needs nvcc only: where the binding does not compile, the
-build goes on without it and the latent calls raise what stopped it.  Rebuilds
-only when a source or header is newer than the libraries.
+statically).  The host binding of the latent and the serving-step calls
+(csrc/binding) compiles beside them against the installed torch, into a file named
+for that torch and this Python.  libkvd.so needs nvcc only: where the binding does
+not compile, the build goes on without it and those calls raise what stopped it.
+Rebuilds only when a source or header is newer than the libraries.
 """
 from __future__ import annotations
 
@@ -72,7 +72,7 @@ def binding_up_to_date() -> bool:
 
 
 def build_binding() -> str:
-    """Compile the host binding of the latent calls; returns its path."""
+    """Compile the host binding of the latent and serving-step calls; returns its path."""
     import torch
     base = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(nvcc()))
@@ -95,7 +95,7 @@ def build_binding() -> str:
 
 
 def _try_binding(force: bool) -> None:
-    """The binding, if it compiles here; what stops it is kept for the latent calls."""
+    """The binding, if it compiles here; what stops it is kept for its calls."""
     try:
         if force or not binding_up_to_date():
             build_binding()

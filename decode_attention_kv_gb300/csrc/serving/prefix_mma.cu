@@ -18,6 +18,15 @@
 // Warps 0-3 and 4-7: softmax of tile 0 and 1, a row a thread; they also lay out the
 // queries.  Warp 8 issues the MMAs.  Warp 9 looks up pages and issues the copies.  Warp 10
 // writes what the merge has to know.
+//
+// Measured, 64 sequences x 32 / 8 heads of 128 behind 16384 tokens: a step of 256 rows x 128
+// keys takes 1.7 us, 1.17 of them the tensor cores' at the rate of a large matrix product;
+// the kernel alone 25 us, of which 4 go before the first copy (lengths, division, table),
+// 5 on the first copy and the first softmax, 12 on seven steps and 3 on the rows.  With
+// the attention over own tokens (154 MB) and the merge the call takes 65 us; HBM needs 33.
+// Not kept: an idle warp that asks L2 for the tiles two to eight steps ahead (+1 to +5 us: the
+// ring's two steps are not what waits), scores taken 32 or 64 at a time in a loop
+// (63.0 and 64.3 us there, but 4 sequences behind 1000 tokens 18.5 and 16.6 instead of 16.2).
 #include "../kvd_internal.h"
 #include "../latent/latent_common.cuh"  // encode_rows, FastDiv, kTinyScale
 #include "../latent/tcgen05_ptx.cuh"

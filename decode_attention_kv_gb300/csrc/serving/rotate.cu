@@ -13,6 +13,13 @@
 // A head is held by 16 lanes (8 of D = 64 in bf16, 32 of D = 128 in fp32), two pieces of 8
 // bytes each: in the half layout a piece of the lower half and the one that it is paired
 // with, so that no lane needs another's elements but for the norm's sum.
+//
+// Measured, 8192 tokens x 48 heads of 128 with norms: 40.9 us, 201 MB, 4.9 TB/s of the
+// copy's 6.8.  Issue slots (70 to 78 % taken) bound it: without the norm 36 us, without
+// the rotation 39, without both and the angles 34.4.  A step of 64 tokens takes 3.1 us,
+// a launch and one chain of latencies.  Not kept: arithmetic on pairs of fp32 (45 us, spills or
+// moves), loads into a head's registers as soon as it is through (55), 5 to 14 tokens a
+// CTA (41.0 to 42.4).
 #include "../kvd_internal.h"
 #include "serving_common.cuh"
 

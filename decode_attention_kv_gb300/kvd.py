@@ -2,7 +2,7 @@
 
 Every function passes torch tensors' device pointers and sizes straight to the
 C entry point of the same name (``kvd_<name>``) on the current CUDA stream (the
-latent calls through the _latent_binding extension).
+latent and serving-step calls through the _latent_binding extension).
 All computation happens in libkvd's kernels; there is no other code path: if
 the library is not built, or a call fails, an exception is raised.
 """
@@ -1160,6 +1160,8 @@ def verify_drafts(target_probs, draft_probs, draft_tokens, u_accept, u_sample, n
 
 
 # ------------------------------------------------------------------ the serving step
+
+# (Through the _latent_binding extension, as the latent calls.)
 
 def plan_pages(block_tables, pages_held, free_pages, free_count, kept_lens, new_lens, block_size,
                num_tokens, pos_base=None, seq_lens=None, slots=None, positions=None,
