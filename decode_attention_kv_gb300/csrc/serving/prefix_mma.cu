@@ -23,10 +23,10 @@
 // keys takes 1.7 us, 1.17 of them the tensor cores' at the rate of a large matrix product;
 // the kernel alone 25 us, of which 4 go before the first copy (lengths, division, table),
 // 5 on the first copy and the first softmax, 12 on seven steps and 3 on the rows.  With
-// the attention over own tokens (154 MB) and the merge the call takes 65 us; HBM needs 33.
+// the attention over own tokens (154 MB) and the merge the call takes 58 us; HBM needs 33.
 // Not kept: an idle warp that asks L2 for the tiles two to eight steps ahead (+1 to +5 us: the
 // ring's two steps are not what waits), scores taken 32 or 64 at a time in a loop
-// (63.0 and 64.3 us there, but 4 sequences behind 1000 tokens 18.5 and 16.6 instead of 16.2).
+// (2 us less there, but 2 more for 4 sequences behind 1000 tokens).
 #include "../kvd_internal.h"
 #include "../latent/latent_common.cuh"  // encode_rows, FastDiv, kTinyScale
 #include "../latent/tcgen05_ptx.cuh"
@@ -506,8 +506,26 @@ cudaError_t go_mma(const PrefixArgs& a, cudaStream_t stream) {
     e = cudaFuncSetAttribute(prefix_mma_kernel<KC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              bytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(prefix_mma_kernel<KC>, dim3(a.workers), dim3(kThreads), bytes, stream, a,
-                      piece, FastDiv(a.BS), FastDiv(a.g), kmap, vmap);
+    // In clusters of two, for their place alone: the two SMs of a cluster share their way to
+    // memory, and a CTA beside one of the attention over own tokens took half as long again.
+    // So pairs go to the one or the other as a whole (64 sequences behind 16384 tokens: 63.2
+    // -> 59.8 us).
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.workers);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, prefix_mma_kernel<KC>, a, piece, FastDiv(a.BS), FastDiv(a.g),
+                              kmap, vmap);
 }
 
 }  // namespace

@@ -76,7 +76,7 @@ kvd_status prefix_plan(const char* fn, int Q, int G, int Hq, int Hkv, int BS, in
     // bf16: two tiles of 128 rows a CTA, one where all sequences together have no more
     pl->rows = mma ? ((long long)n * g > 128 ? 256 : 128) : 16;
     pl->keys = mma ? 128 / piece * piece : 32;
-    pl->lead = mma ? 1 : 2;
+    pl->lead = mma ? 4 : 2;  // (one place: 256 sequences behind 8192 tokens 76 us, four: 73)
     pl->workers = mma ? kServingSMs : 2 * kServingSMs;
     // the longest line that the groups can make
     const long long tiles = (long long)n * g / pl->rows + G + 1,
@@ -286,8 +286,15 @@ kvd_status kvd_attend_paged_prefix(const void* q, const void* key_cache, const v
     a.lead = pl.lead;
     a.workers = pl.workers;
     if (dtype == KVD_BF16) {
-        a.place_cost = 4.f;
+        // A place costs 2.5 (1.75 alone, up to 4 while the sequences' own keys fill the queues
+        // to memory): 64 sequences behind 16384 tokens with 64 to 1024 own ones 61, 58.4,
+        // 57.7 and 59.8 us with 2, 2.5, 3 and 4; 256 behind 8192 with 16 to 256 70, 73, 77 and
+        // 77.  An SM's share of the memory's rate is 45000 bytes a microsecond.
+        a.place_cost = 2.5f;
         a.token_cost = (float)Hkv * D * 4 / 45000.f;
+        // few own units: an SM for two of them, so that none starts behind the prefixes (8
+        // sequences of 8 kv heads behind 4096 tokens 28.9 -> 24.6 us, behind 16384 40.1 -> 38.7)
+        a.spare = pl.own.units <= kServingSMs / 2 ? (int)(pl.own.units + 1) / 2 : 0;
     }
     a.seq_lens = seq_lens;
     a.meta = reinterpret_cast<int4*>(ws + pl.off_meta);

@@ -34,8 +34,9 @@ struct PrefixArgs {
     int lead, workers;
     // SM microseconds that a place of the line costs, and a token of a sequence's own: how
     // many SMs the prefixes take while the sequences' own keys go through the others (0:
-    // as many as there are)
+    // as many as there are); and SMs that are left to those in any case
     float place_cost, token_cost;
+    int spare;
     const int32_t* seq_lens;
     int4* meta;           // [Q + 1] first place, row tiles, key tiles, place in the group;
                           // last the line's length and the workers that share it
@@ -155,7 +156,8 @@ __device__ __forceinline__ PrefixRuns prefix_setup(const PrefixArgs& a, PrefixGr
     int W = min(a.workers, max(tot, 1));
     if (own > 0) {
         const float mine = a.place_cost * (float)tot, theirs = a.token_cost * (float)own;
-        W = max(1, min(W, (int)(a.workers * mine / (mine + theirs) + 0.5f)));
+        W = max(1, min(min(W, a.workers - a.spare), (int)(a.workers * mine / (mine + theirs) + 0.5f)));
+        if (W > 1 && W < tot) W &= ~1;
     }
     return PrefixRuns(tot, W);
 }
