@@ -292,9 +292,7 @@ kvd_status kvd_attend_paged_prefix(const void* q, const void* key_cache, const v
         // 77.  An SM's share of the memory's rate is 45000 bytes a microsecond.
         a.place_cost = 2.5f;
         a.token_cost = (float)Hkv * D * 4 / 45000.f;
-        // few own units: an SM for two of them, so that none starts behind the prefixes (8
-        // sequences of 8 kv heads behind 4096 tokens 28.9 -> 24.6 us, behind 16384 40.1 -> 38.7)
-        a.spare = pl.own.units <= kServingSMs / 2 ? (int)(pl.own.units + 1) / 2 : 0;
+        a.own_units = (int)pl.own.units;
     }
     a.seq_lens = seq_lens;
     a.meta = reinterpret_cast<int4*>(ws + pl.off_meta);

@@ -32,11 +32,11 @@ struct PrefixArgs {
     float qscale;         // scale * log2(e)
     int rows, keys;       // of a tile
     int lead, workers;
-    // SM microseconds that a place of the line costs, and a token of a sequence's own: how
-    // many SMs the prefixes take while the sequences' own keys go through the others (0:
-    // as many as there are); and SMs that are left to those in any case
+    // SM microseconds that a place of the line costs, and a token of a sequence's own, and
+    // the units of the attention over those: how many SMs the prefixes take while the
+    // sequences' own keys go through the others (0: as many as there are)
     float place_cost, token_cost;
-    int spare;
+    int own_units;
     const int32_t* seq_lens;
     int4* meta;           // [Q + 1] first place, row tiles, key tiles, place in the group;
                           // last the line's length and the workers that share it
@@ -92,6 +92,38 @@ struct PrefixRuns {
         return w;
     }
 };
+
+// The SMs that the prefixes take of a call's workers; every warp of every CTA gets the same.
+// Two ways, by their estimated ends:
+//  - Such a share that the other SMs are through the own tokens by the time the prefixes
+//    end, so that nothing starts late.  A CTA's start and end take 8 us, a place 1.75, up to
+//    place_cost as own tokens fill the memory's queues; an own unit's chain takes 9, each
+//    further one of a CTA 1.5.
+//  - Where own tokens are most of the work: SMs by the shares of the work, and the own units
+//    that are left when the prefixes end over all SMs, a chain later.
+// (The second way and an SM for two own units at most 76: 64 sequences behind 16384 tokens
+// with up to 16 own ones 48.3 us, now 39.7; 64 in 4 groups behind 1024 to 4096 34.7, 31.0; 8
+// behind 4096 22.0, 20.5; one behind 8192 24.3, 21.7; 64 to 1024 own ones 58.4, 58.7.)
+__device__ __forceinline__ int prefix_workers(const PrefixArgs& a, int tot, int own) {
+    constexpr float kStart = 8.f, kChain = 9.f, kUnit = 1.5f, kPlace = 1.75f;
+    const int lane = threadIdx.x & 31, most = min(a.workers, max(tot, 1));
+    const float theirs = a.token_cost * (float)own, places = (float)max(tot, 1);
+    const float place =
+        kPlace + (a.place_cost - kPlace) * fminf(__fdividef(theirs, kPlace * places), 1.f);
+    const int w = max(1, min(most, a.workers - 4 * lane));
+    const float others = __fdividef(1.f, fmaxf((float)(a.workers - w), 0.5f));  // one over them
+    const float prefix_end = kStart + place * ceilf(__fdividef(places, (float)w) - 0.01f);
+    const float own_end =
+        kChain + kUnit * fmaxf(0.5f * (float)a.own_units * others - 1.f, 0.f) + theirs * others;
+    // the earliest end, in 2^-6 us, and of equal ones the smallest share
+    const uint32_t end = (uint32_t)(fminf(fmaxf(prefix_end, own_end), 1e6f) * 64.f);
+    const uint32_t best = __reduce_min_sync(0xffffffffu, end << 5 | (31 - lane));
+    const float mine = a.place_cost * places, all = __fdividef(mine + theirs, (float)a.workers);
+    if ((float)(best >> 5) <= 64.f * (kStart + all + kChain))
+        return max(1, min(most, a.workers - 4 * (31 - (int)(best & 31u))));
+    const int share = max(1, min(most, (int)(__fdividef(mine, all) + 0.5f)));
+    return share > 1 && share < most ? share & ~1 : share;
+}
 
 // By all threads of a CTA: reads and checks the groups, lays out the line; returns its
 // division.  The attention over the sequences' own keys, which is launched behind, runs
@@ -153,13 +185,7 @@ __device__ __forceinline__ PrefixRuns prefix_setup(const PrefixArgs& a, PrefixGr
     }
     __syncthreads();
     const int tot = t.base[a.G];
-    int W = min(a.workers, max(tot, 1));
-    if (own > 0) {
-        const float mine = a.place_cost * (float)tot, theirs = a.token_cost * (float)own;
-        W = max(1, min(min(W, a.workers - a.spare), (int)(a.workers * mine / (mine + theirs) + 0.5f)));
-        if (W > 1 && W < tot) W &= ~1;
-    }
-    return PrefixRuns(tot, W);
+    return PrefixRuns(tot, own > 0 ? prefix_workers(a, tot, own) : min(a.workers, max(tot, 1)));
 }
 
 // The CTA's share of the meta rows, by `threads` of its threads (without groups t.base[G] is
