@@ -7,9 +7,9 @@
 // a thread owns four dims (D = 64) or eight of one row.
 //
 // What bounds it at the sizes it is for (checks of small models): latency.  9 sequences behind
-// two prompts of 515 tokens, 8 / 2 heads of 64: 14.7 us a call, 6 of them this kernel's
+// two prompts of 515 tokens, 8 / 2 heads of 64: 12.9 us a call, 6 of them this kernel's
 // chain lengths -> page -> tile -> softmax -> rows, the rest the attention over own tokens
-// beside it and the merge (4 us: meta row, log-sum-exps, up to four rows at a time).
+// beside it and the merge (3 us: meta row, log-sum-exps, up to eight rows at a time).
 #include "../kvd_internal.h"
 #include "serving_common.cuh"
 

@@ -103,7 +103,7 @@ struct PrefixRuns {
 //    that are left when the prefixes end over all SMs, a chain later.
 // (The second way and an SM for two own units at most 76: 64 sequences behind 16384 tokens
 // with up to 16 own ones 48.3 us, now 39.7; 64 in 4 groups behind 1024 to 4096 34.7, 31.0; 8
-// behind 4096 22.0, 20.5; one behind 8192 24.3, 21.7; 64 to 1024 own ones 58.4, 58.7.)
+// behind 4096 22.0, 20.5; one behind 8192 24.3, 21.8; 64 to 1024 own ones the same.)
 __device__ __forceinline__ int prefix_workers(const PrefixArgs& a, int tot, int own) {
     constexpr float kStart = 8.f, kChain = 9.f, kUnit = 1.5f, kPlace = 1.75f;
     const int lane = threadIdx.x & 31, most = min(a.workers, max(tot, 1));
@@ -113,8 +113,9 @@ __device__ __forceinline__ int prefix_workers(const PrefixArgs& a, int tot, int 
     const int w = max(1, min(most, a.workers - 4 * lane));
     const float others = __fdividef(1.f, fmaxf((float)(a.workers - w), 0.5f));  // one over them
     const float prefix_end = kStart + place * ceilf(__fdividef(places, (float)w) - 0.01f);
-    const float own_end =
-        kChain + kUnit * fmaxf(0.5f * (float)a.own_units * others - 1.f, 0.f) + theirs * others;
+    const float rounds = 0.5f * (float)a.own_units * others;  // two CTAs an SM
+    const bool late = a.own_units <= 2 * kServingSMs && rounds > 1.f;  // a CTA a unit, not dealt
+    const float own_end = kChain + (late ? prefix_end : kUnit * fmaxf(rounds - 1.f, 0.f)) + theirs * others;
     // the earliest end, in 2^-6 us, and of equal ones the smallest share
     const uint32_t end = (uint32_t)(fminf(fmaxf(prefix_end, own_end), 1e6f) * 64.f);
     const uint32_t best = __reduce_min_sync(0xffffffffu, end << 5 | (31 - lane));
