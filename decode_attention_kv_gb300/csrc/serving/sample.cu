@@ -24,7 +24,7 @@
 // in 64 bits: a weight is a table's sixteenth of a factor of two times a polynomial, right
 // to about 2^-28 of itself without a trend, and is counted in whole multiples of 2^-42.
 //
-// Measured: a row of 32000 with all filters 10.8 us, 64 rows of 128000 46.5 (their bytes 4.8).
+// Measured: a row of 32000 with all filters 10.3 us, 64 rows of 128000 46.2 (their bytes 4.8).
 // In cycles of a row there, four CTAs to a row and two an SM: first pass 10000 (the bytes), with
 // top-k's counts 16000; top-k then 5000 to 8000 for the list, 7000 for its way and sort,
 // 10000 for both cuts and the draw: 48000 to 55000 in all.  Without top-k a count pass of 15000,
@@ -199,7 +199,7 @@ struct Shared {
     unsigned long long warp_sum[kWarps], part_sum[kWarps];
     unsigned long long cta_sum[kMaxCtas], cta_above[kMaxCtas];
     unsigned long long kept;      // the sum of what is kept, from the first CTA
-    float least;                  // the smallest logit that min-p keeps; one over the sum
+    float least;                  // the smallest logit that min-p keeps
     int good;                     // the bracket of the top-p border held it; min-p decides alone
     unsigned long long cta_top[kMaxCtas];
     uint32_t cta_low[kMaxCtas];
@@ -773,11 +773,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
 
     constexpr int VEC = Row<Elem>::VEC;
     const bool first_k = k > 0 && k < V;
-    if (tid == kThreads - 1) {
-        const double c = 23.083120654223414 / (double)T;  // 16 log2(e)
-        sh.scale.c = (float)c;
-        sh.scale.c_low = (float)(c - (double)(float)c);
-    }
     if (first_k) {
         for (int i = tid; i < kOrders; i += kThreads) sh.orders[i] = 0;
         __syncthreads();
@@ -906,13 +901,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         }
         return;
     }
+    // In pairs of fp32 words (about 2^-47 of themselves): in 64 bits one thread's division and
+    // what follows it took 1500 cycles (a row of 32000 10.9 us, now 10.3; 4 rows with top-p
+    // 17.9, 16.6).
     if (tid == 0) {
-        const float x = logit_of(top_key);
-        const double y = (double)x * ((double)sh.scale.c + (double)sh.scale.c_low);
-        sh.scale.top = x;
-        sh.scale.fast = fabs(y) < 65536.0;
-        sh.scale.whole = rintf((float)y * 64.f) * 0.015625f;
-        sh.scale.rest = (float)(y - (double)sh.scale.whole);
+        constexpr double kPer = 23.083120654223414;  // 16 log2(e)
+        constexpr float kHigh = (float)kPer, kLow = (float)(kPer - (double)kHigh);
+        const float q = __fdiv_rn(kHigh, T);
+        const float more =
+            q < INFINITY ? __fdividef(__fadd_rn(__fmaf_rn(-q, T, kHigh), kLow), T) : 0.f;
+        const float x = logit_of(top_key), c = __fadd_rn(q, more), c_low = __fsub_rn(more, __fsub_rn(c, q));
+        const float y = __fmul_rn(x, c), whole = rintf(y * 64.f) * 0.015625f;
+        sh.scale = Scale{x, c, c_low, whole,
+                         __fadd_rn(__fsub_rn(y, whole), __fmaf_rn(x, c_low, __fmaf_rn(x, c, -y))),
+                         fabsf(y) < 65536.f};
     }
     __syncthreads();
     const Scale s = sh.scale;
@@ -995,11 +997,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             }
             unsigned long long at = block_sums(sh, mine, total) - mine;
             if (tid == 0) {
-                const double want = (double)p * (double)total,
-                             off = 1e-3 * fmin((double)p, 1.0 - (double)p) * (double)total;
-                sh.want[0] = (unsigned long long)fmax(want - off, 0.0);
-                sh.want[1] = (unsigned long long)fmax(want + off, 0.0);
-                sh.want[2] = (unsigned long long)fmax(want * 0.98, 0.0);
+                // (the second term: what fp32 rounds)
+                const float sum = (float)total, want = p * sum,
+                            off = (1e-3f * fminf(p, 1.f - p) + 2.4e-7f) * sum;
+                sh.want[0] = (unsigned long long)fmaxf(want - off, 0.f);
+                sh.want[1] = (unsigned long long)fmaxf(want + off, 0.f);
+                sh.want[2] = (unsigned long long)fmaxf(want * 0.98f, 0.f);
             }
             __syncthreads();
             const unsigned long long from_w = sh.want[0], to_w = sh.want[1], surely = sh.want[2];
@@ -1202,9 +1205,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         total = sh.kept;
     }
     if constexpr (kProbs) {
-        if (tid == 0) sh.least = (float)((double)kOne / (double)total);
-        __syncthreads();
-        const float inv = sh.least;
+        // one over the sum, corrected by what the quotient and fp32 of the sum leave
+        const float sum = (float)total, left = (float)(long long)(total - (unsigned long long)sum);
+        const float near = __fdiv_rn((float)kOne, sum);
+        const float inv = __fmaf_rn(
+            __fmaf_rn(-near, left, __fmaf_rn(-near, sum, (float)kOne)), __fdividef(1.f, sum), near);
         const float from_x = fmaxf(least_x, logit_of(max(cut.key, kLowest)));
         row.vectors_of(wlo, whi, [&](int v, const float (&x)[VEC]) {
             float y[VEC];
