@@ -246,3 +246,31 @@ def test_padded_batch(kvd):
     assert (b[3][ends[live]:] == 9.0).all()
     assert (b[4][live:] == 0).all() and (b[5][live:] == -math.inf).all()
     assert torch.equal(a[6], b[6]) and torch.equal(a[7], b[7])
+
+
+@pytest.mark.parametrize("V", [37, 5000])
+@pytest.mark.parametrize("T", [1e-45, 1e-38, 3e-20, 1e20, 1e30])
+def test_far_temperatures(kvd, T, V):
+    """A division that overflows keeps the largest logits alone; one that vanishes all finite
+    ones alike."""
+    g = torch.Generator().manual_seed(V)
+    logits = torch.randn(6, V, generator=g) * 5
+    logits[1, 3] = logits[1, 20] = 40.0
+    logits[2, ::2] = -math.inf
+    logits[3] = 0.0
+    logits[4] *= 1e-30
+    logits = logits.cuda()
+    t = torch.full((6,), T, device="cuda")
+    k, p = i32([0, 0, 0, 0, 0, 9]), torch.tensor([1.0, 1.0, 0.7, 1.0, 0.6, 0.8], device="cuda")
+    u = torch.rand(6, generator=g).cuda()
+    status = kvd.status_tensor()
+    tokens = kvd.sample(logits, u, temperature=t, top_k=k, top_p=p, dev_status=status)
+    probs = kvd.filter_probs(logits, temperature=t, top_k=k, top_p=p, dev_status=status)
+    assert int(status.item()) == 0
+    for r in range(6):
+        w = ref.kept_weights(logits[r].double(), float(t[r]), int(k[r]), float(p[r]), 0.0)
+        assert int(tokens[r]) == ref.draw(w, float(u[r]))
+        q = w / w.sum()
+        got = probs[r].double()
+        tol = q * (ref.U[F32] + 3 * 2.0 ** -24) + 2.0 ** -126  # as for other rows
+        assert float(((got - q).abs() / tol).max()) <= 1.0
