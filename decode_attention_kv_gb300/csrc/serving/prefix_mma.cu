@@ -447,11 +447,16 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
             if (a.qscale != a.qscale && l != 0.f) l = a.qscale;
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t row = pc.slot < 0 ? at : (size_t)pc.slot * a.rows + in_tile;
-            // through shared memory (the queries' place: their products are complete), so that
-            // a store covers whole rows; kDims dims of the warp's 32 rows at a time
+            // through shared memory, so that a store covers whole rows; kDims dims of the warp's
+            // 32 rows at a time, in the place of the queries of the same rows: their products
+            // are complete, and no other warp puts its next queries there
             constexpr int kDims = 32 * KC, kVecs = kDims / 4;
             float* out = pc.slot < 0 ? a.whole_o : a.part_o;
-            uint4* stage = reinterpret_cast<uint4*>(sm + s * KC * kBlock) + (warp & 3) * 32 * kVecs;
+            unsigned char* stage = sm + s * KC * kBlock + (warp & 3) * 32 * 128;
+            auto staged = [&](int r, int j) {  // 16-byte piece j of the warp's row r
+                return reinterpret_cast<uint4*>(stage + (j >> 3) * kBlock + r * 128 +
+                                                (((j ^ r) & 7) << 4));
+            };
             const uint32_t rows_live = __ballot_sync(0xffffffffu, live);
 #pragma unroll 1
             for (int c = 0; c < D; c += kDims) {
@@ -461,8 +466,7 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
-                        const int j = 8 * half + e / 4;
-                        stage[lane * kVecs + (j ^ (lane & (kVecs - 1)))] =
+                        *staged(lane, 8 * half + e / 4) =
                             make_uint4(__float_as_uint(o[e] * inv), __float_as_uint(o[e + 1] * inv),
                                        __float_as_uint(o[e + 2] * inv), __float_as_uint(o[e + 3] * inv));
                     }
@@ -477,7 +481,7 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
                         __shfl_sync(0xffffffffu, (unsigned long long)row, r);
                     if ((rows_live >> r) & 1u)
                         *reinterpret_cast<uint4*>(out + to_row * D + c + 4 * j) =
-                            stage[r * kVecs + (j ^ (r & (kVecs - 1)))];
+                            *staged(r, j);
                 }
                 __syncwarp();
             }

@@ -274,3 +274,19 @@ def test_far_temperatures(kvd, T, V):
         got = probs[r].double()
         tol = q * (ref.U[F32] + 3 * 2.0 ** -24) + 2.0 ** -126  # as for other rows
         assert float(((got - q).abs() / tol).max()) <= 1.0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_short_pieces_give_the_same_each_time(kvd, D):
+    """Workers that go from piece to piece: groups of a few sequences behind prefixes of
+    one to a few hundred tokens, again and again, the same to the bit and as in 64 bits."""
+    import latent_ref as lref
+    from test_gpu_prefix import Case
+    sizes = [8, 8, 8, 7, 7, 7, 60, 1, 1, 33]
+    pre = [700, 500, 390, 1, 1, 20, 260, 17, 1, 129]
+    c = Case(sizes, pre, [3 + i % 20 for i in range(sum(sizes))], 16, 4, D, 16, BF, seed=5)
+    lse = torch.empty(c.q.shape[:2], device="cuda")
+    want = kvd.attend_paged_prefix(*c.args(), lse=lse)
+    lref.check("first", want, lse, *c.reference(), max(pre) + 23, BF)
+    outs = [kvd.attend_paged_prefix(*c.args()) for _ in range(300)]
+    assert all(torch.equal(want, x) for x in outs)
