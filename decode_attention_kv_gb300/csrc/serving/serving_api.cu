@@ -106,12 +106,12 @@ kvd_status kvd_plan_pages(int32_t* block_tables, int32_t* pages_held, int32_t* f
                           int32_t* positions, int Q, int N, int BS, int cols, int F,
                           int32_t* dev_status, kvd_stream_t stream) {
     const char* fn = "kvd_plan_pages";
-    if (Q < 0 || N < 0 || BS < 1 || cols < 1 || F < 1)
-        return fail(KVD_ERR_INVALID_ARG, "%s: Q, N >= 0 and BS, cols, F >= 1 required", fn);
+    if (Q < 0 || N < 0 || F < 0 || BS < 1 || cols < 1)
+        return fail(KVD_ERR_INVALID_ARG, "%s: Q, N, F >= 0 and BS, cols >= 1 required", fn);
     if (Q > (1 << 20) || N > (1 << 30))
         return fail(KVD_ERR_UNSUPPORTED, "%s: Q > 2^20 or N > 2^30", fn);
     if (!new_lens || !seq_lens || (Q > 0 && (!block_tables || !pages_held || !kept_lens)) ||
-        !free_pages || !free_count || (N > 0 && (!slots || !positions)))
+        (F > 0 && !free_pages) || !free_count || (N > 0 && (!slots || !positions)))
         return fail(KVD_ERR_INVALID_ARG, "%s: null pointer", fn);
     if (!aligned(4, block_tables, pages_held, free_pages, free_count, kept_lens, new_lens, pos_base,
                  seq_lens, slots, positions, dev_status))

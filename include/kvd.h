@@ -797,7 +797,8 @@ kvd_status kvd_verify_drafts(const void* target_probs, const void* draft_probs,
  *   block_tables [Q, cols] int32   columns [0, pages_held[q]) are q's (in/out)
  *   pages_held   [Q] int32         (in/out)
  *   free_pages   [F] int32, free_count [1] int32: the first free_count entries
- *                are free pages (in/out); F: at least all pages of the cache
+ *                are free pages (in/out); F: at least all pages of the cache (NULL
+ *                with F = 0)
  *   kept_lens    [Q] int32;  new_lens [Q + 1] int32, cumsum starting at 0
  *   pos_base     [Q] int32 or NULL (zeros): the position of q's first token (the
  *                length of a shared prefix before it)

@@ -217,3 +217,22 @@ def test_graph_and_streams(kvd):
         have = [y - x for x, y in zip(a, a[1:])]
         assert (lens.tolist(), slots.tolist(), pos.tolist(), bits) == (a, b, c, 0)
         assert dev[0].tolist() == st.table and dev[3].tolist() == st.count
+
+
+@pytest.mark.parametrize("Q", [2, 1030])
+def test_a_list_without_entries(kvd, Q):
+    """No page to take: sequences that need one are refused, the others go on."""
+    table = torch.arange(Q, dtype=torch.int32, device="cuda")[:, None].repeat(1, 3)
+    held = torch.ones(Q, dtype=torch.int32, device="cuda")
+    held[0] = 0
+    kept = torch.full((Q,), 2, dtype=torch.int32, device="cuda")
+    kept[0] = 0
+    new = torch.arange(Q + 1, dtype=torch.int32, device="cuda")
+    empty, count = torch.empty(0, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    status = kvd.status_tensor()
+    lens, slots, pos = kvd.plan_pages(table, held, empty, count, kept, new, 4, Q, dev_status=status)
+    assert int(status.item()) == kvd.DEV_NO_PAGES
+    assert lens.tolist() == [0] + [3 * i for i in range(Q)]
+    assert slots.tolist() == [-1] + [4 * i + 2 for i in range(1, Q)]
+    assert pos.tolist() == [-1] + [2] * (Q - 1) and held.tolist() == [0] + [1] * (Q - 1)
+    assert int(count) == 0

@@ -26,7 +26,7 @@ def test_plan_pages_validates(lib):
         return lib.kvd_plan_pages(bt, held, free, P(1), P(1), lens, None, P(1), slots, P(1), Q, N,
                                   BS, cols, F, None, None)
     for bad in (dict(bt=None), dict(held=None), dict(free=None), dict(lens=None), dict(slots=None),
-                dict(Q=-1), dict(N=-1), dict(BS=0), dict(cols=0), dict(F=0), dict(bt=ODD)):
+                dict(Q=-1), dict(N=-1), dict(BS=0), dict(cols=0), dict(F=-1), dict(bt=ODD)):
         assert call(**bad) == 1, bad
     assert call(Q=(1 << 20) + 1) == 2 and call(N=(1 << 30) + 1) == 2
 
