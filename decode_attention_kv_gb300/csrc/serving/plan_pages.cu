@@ -209,8 +209,10 @@ __global__ void __launch_bounds__(kThreads) plan_pages_kernel(const PlanArgs a) 
         uint32_t none = 0;
         const PlanSeq s = plan_seq(a, q, true, none);
         const int len = a.seq_lens[q + 1] - a.seq_lens[q];
-        if (!s.good || len != s.kept + s.n) continue;
-        if (s.need > s.held || (s.need < s.held && give_back)) a.pages_held[q] = s.need;
+        if (!s.good) continue;
+        // what went onto the list is no longer held, whether or not the tokens have a place
+        if (s.need < s.held ? give_back : s.need > s.held && len == s.kept + s.n)
+            a.pages_held[q] = s.need;
     }
     for (int i = me; i < a.N; i += all) {
         int lo = usable ? 0 : a.Q, hi = a.Q;  // the first sequence that ends behind i
@@ -426,7 +428,8 @@ __global__ void __launch_bounds__(THREADS, 1) plan_one_kernel(const PlanArgs a, 
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (lead && usable) {
         if (tid == 0) a.free_count[0] = (int)(avail - taken);
-        if (tid < a.Q && served && (s.need > s.held || (s.need < s.held && give_back)))
+        // what went onto the list is no longer held, whether or not the tokens have a place
+        if (tid < a.Q && s.good && (s.need < s.held ? give_back : s.need > s.held && served))
             a.pages_held[tid] = s.need;
     }
     if (bits) report(a.dev_status, bits);

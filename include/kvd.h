@@ -809,18 +809,19 @@ kvd_status kvd_verify_drafts(const void* target_probs, const void* draft_probs,
  *                slot = block_tables[q, t / BS] * BS + t % BS, position =
  *                pos_base[q] + t; both -1 for tokens without a place: those of a
  *                refused sequence, and padding behind new_lens[Q]
- * A refused sequence keeps its pages and counts kept_lens[q] tokens: too few
- * pages left, or need above cols (KVD_DEV_TABLE_COLS).  A bad one is left alone
- * and counts none: kept_lens negative or more than its pages hold, pages_held
- * outside [0, cols], or kept + new past 2^31 - 1 (KVD_DEV_POS_RANGE), or an end of
- * seq_lens past 2^31 - 1, its and those before it counted (KVD_DEV_SEQLENS).  All
- * sequences are refused, and none gives pages back, by a new_lens that does not
- * start at 0, decreases or passes N (KVD_DEV_SEQLENS) and by a free_count outside
- * [0, F] (KVD_DEV_POS_RANGE).  Where the list has no room for all pages given back,
- * none is (KVD_DEV_NO_PAGES).  A token whose page is negative or whose slot is past
- * 2^31 - 1 (KVD_DEV_BLOCK_RANGE), or whose position is outside 32 bits
- * (KVD_DEV_POS_RANGE), has no place.  One launch, two for many tokens; runs that
- * change the same tables must be ordered.  Q at most 2^20, N at most 2^30.
+ * A refused sequence keeps its pages and counts kept_lens[q] tokens: too few pages
+ * left, or need above cols (KVD_DEV_TABLE_COLS).  A bad one is left alone and counts
+ * none: kept_lens negative or more than its pages hold, pages_held outside [0,
+ * cols], or kept + new past 2^31 - 1 (KVD_DEV_POS_RANGE).  One whose end in seq_lens
+ * would pass 2^31 - 1, it and those before it counted, takes no pages and counts
+ * none (KVD_DEV_SEQLENS); pages above its need[q] are given back all the same and no
+ * longer held.  All sequences are refused, and none gives pages back, by a new_lens
+ * that does not start at 0, decreases or passes N (KVD_DEV_SEQLENS) and by a
+ * free_count outside [0, F] (KVD_DEV_POS_RANGE).  Where the list has no room for all
+ * pages given back, none is (KVD_DEV_NO_PAGES).  A token whose page is negative or
+ * whose slot is past 2^31 - 1 (KVD_DEV_BLOCK_RANGE), or whose position is outside 32
+ * bits (KVD_DEV_POS_RANGE), has no place.  One launch, two for many tokens; runs
+ * that change the same tables must be ordered.  Q at most 2^20, N at most 2^30.
  */
 kvd_status kvd_plan_pages(int32_t* block_tables, int32_t* pages_held, int32_t* free_pages,
                           int32_t* free_count, const int32_t* kept_lens, const int32_t* new_lens,
