@@ -987,7 +987,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             unsigned long long w[kPer], mine = 0, total;
 #pragma unroll
             for (int z = 0; z < kPer; ++z) {
-                const float e = 32.f - (float)(tid * kPer + z) * (s.c * 0.0625f) / per;
+                // (the last bin weighs nothing: far elements, and, whatever the bins' width,
+                // -inf and NaN)
+                const int b = tid * kPer + z;
+                const float e = b < kFine - 1 ? 32.f - (float)b * (s.c * 0.0625f) / per : -1.f;
                 w[z] = (unsigned long long)n[z] * (unsigned long long)exp2f(fmaxf(e, -1.f));
                 mine += w[z];
             }
