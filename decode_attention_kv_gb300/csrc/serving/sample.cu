@@ -388,7 +388,7 @@ struct Picker {
     const Row<Elem>& row;
     cg::cluster_group& cluster;
     int rank, ctas, wlo, whi;  // of this warp's vectors
-    uint32_t low;              // the smallest order above kLowest, or the largest
+    uint32_t low;              // the smallest order above kLowest (inf's where there is none)
 
     // Elements on their way to the first CTA: into this CTA's list, then all at once.
     __device__ __forceinline__ void note(int i, float x) {
@@ -777,16 +777,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
         for (int i = tid; i < kOrders; i += kThreads) sh.orders[i] = 0;
         __syncthreads();
     }
-    // the largest logit and the first vector that holds it; the smallest
+    // the largest logit and the first vector that holds it; the smallest above -inf (which the
+    // bins of the passes below span; what lies beside the row is -inf too)
     float best = -INFINITY, least = INFINITY;
     int where = 0;
     row.vectors_of(wlo, whi, [&](int v, const float (&x)[VEC]) {
-        float most = x[0];
+        float most = x[0], fewest = x[0];
 #pragma unroll
-        for (int z = 0; z < VEC; ++z) {
+        for (int z = 1; z < VEC; ++z) {
             most = fmaxf(most, x[z]);
-            least = fminf(least, x[z]);
+            fewest = fminf(fewest, x[z]);
         }
+        if (fewest == -INFINITY) {
+            fewest = INFINITY;
+#pragma unroll
+            for (int z = 0; z < VEC; ++z)
+                if (x[z] > -INFINITY) fewest = fminf(fewest, x[z]);
+        }
+        least = fminf(least, fewest);
         if (most > best) {
             best = most;
             where = v;
@@ -1024,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             // a bin's border lies half a bin before it; one bin more on either side
             const int b0 = (int)sh.bin - 1, b1 = (int)sh.base + 1;
             hi = b0 > 0 ? s.top - ((float)b0 - 0.5f) / per : INFINITY;
-            lo_x = b1 < kFine - 1 ? s.top - ((float)b1 + 0.5f) / per : -INFINITY;
+            lo_x = b1 < kFine - 1 ? s.top - ((float)b1 + 0.5f) / per : logit_of(low);
             if (sh.good) border = false;
             __syncthreads();
         }

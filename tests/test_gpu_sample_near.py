@@ -37,3 +37,20 @@ def test_near_logits_beside_hidden_ones(kvd, V, hidden, dtype):
     same(kvd, logits, u, T=T, p=p, m=m)
     same(kvd, logits, u, T=T, p=p)
     same(kvd, logits, u, T=T, m=m)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V", [50256, 50257, 50260])
+def test_flat_rows(kvd, V, dtype):
+    """Logits that hardly differ, in rows that start at and beside whole vectors, with and without
+    one at -inf or most of them: the bins follow the finite ones."""
+    R = 8
+    g = torch.Generator().manual_seed(V)
+    logits = (torch.rand(R, V, generator=g) * 0.05).to(dtype)
+    logits[R // 2:, 1234] = -math.inf
+    logits[:2, 5000:] = -math.inf
+    logits = logits.cuda()
+    u = torch.rand(R, generator=g).cuda()
+    p = torch.tensor([0.3, 0.9, 0.5, 0.99] * 2, device="cuda")
+    same(kvd, logits, u, p=p)
+    same(kvd, logits, u, T=p, p=p, m=torch.full((R,), 0.97, device="cuda"))
