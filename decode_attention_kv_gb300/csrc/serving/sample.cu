@@ -22,7 +22,9 @@
 //
 // Whole numbers decide, so sums must not depend on an order and have to agree with sums
 // in 64 bits: a weight is a table's sixteenth of a factor of two times a polynomial, right
-// to about 2^-28 of itself without a trend, and is counted in whole multiples of 2^-42.
+// to about 2^-28 of itself without a trend, and is counted in whole multiples of 2^-42 (sums of
+// 2^20 of them fit 64 bits).  A flat tail is off by up to half a multiple a token, all to one
+// side: 2^-23 of the largest weight for 2^20 tokens; below half a multiple nothing of it counts.
 //
 // Measured: a row of 32000 with all filters 10.3 us, 64 rows of 128000 46.2 (their bytes 4.8).
 // In cycles of a row there, four CTAs to a row and two an SM: first pass 10000 (the bytes), with

@@ -937,8 +937,11 @@ kvd_status kvd_attend_paged_prefix(const void* q, const void* key_cache, const v
  *   tokens [R] int32
  * NaN logits count as -inf; among infinite ones the weight is shared alike.
  * Weights are right to about 2^-28 of themselves, without a trend, and are summed as
- * whole multiples of 2^-42 of the largest, in any order to the same sum: a draw or a
- * top-p border that differs from one in 64 bits lies within 2^-28 of a token's border.
+ * whole multiples of 2^-42 of the largest, in any order to the same sum.  A multiple
+ * is half of one off at most, but equal weights to the same side: a draw or a top-p
+ * border that differs from one in 64 bits lies within 2^-28 + V 2^-43 of the sum (2^-23
+ * for V = 2^20) of a token's border, and weights below 2^-43 of the largest count as
+ * zero: such a token is not drawn.
  * A row without a logit above -inf gives -1 (KVD_DEV_PROBS); a NaN, a temperature
  * below 0 or above 1e30, or u outside [0, 1) gives -1 (KVD_DEV_PARAM).
  * V at most 2^20.
@@ -951,7 +954,8 @@ kvd_status kvd_sample(const void* logits, const float* temperature, const int32_
  * kvd_filter_probs -- the distributions that kvd_sample draws from: probs[r, v] =
  * w_v over the sum of the weights that stay, 0 for the others, as kvd_verify_drafts
  * takes them.  probs [R, V] of probs_dtype, not overlapping the logits; rows that
- * kvd_sample refuses are zero.  Otherwise as kvd_sample.
+ * kvd_sample refuses are zero.  Weights that stay but are too small to be drawn keep
+ * their probability (down to 2^-125 of the largest).  Otherwise as kvd_sample.
  */
 kvd_status kvd_filter_probs(const void* logits, const float* temperature, const int32_t* top_k,
                             const float* top_p, const float* min_p, void* probs, int R, int V,
