@@ -793,7 +793,9 @@ kvd_status kvd_verify_drafts(const void* target_probs, const void* draft_probs,
  *  - then pages are taken from the list's end, the first sequence's first column
  *    first (so that taking and giving back the same pages leaves the list as it
  *    was), while they last: a sequence whose pages and those of all sequences
- *    before it are more than there are gets none (KVD_DEV_NO_PAGES).
+ *    before it are more than there are gets none (KVD_DEV_NO_PAGES).  One that
+ *    needs more than cols pages asks for none; what was refused to one for want of
+ *    pages does count against those behind it.
  *   block_tables [Q, cols] int32   columns [0, pages_held[q]) are q's (in/out)
  *   pages_held   [Q] int32         (in/out)
  *   free_pages   [F] int32, free_count [1] int32: the first free_count entries

@@ -76,3 +76,37 @@ def test_lengths_past_32_bits_with_pages_too_many(kvd, Q, new):
                                 sum(counts), dev_status=status)
     assert int(status.item()) == 0
     once(table, held, free, count, range(2, Q), pages + extra)
+
+
+@pytest.mark.parametrize("Q", [4, 1030])
+def test_a_sequence_past_the_columns_asks_for_nothing(kvd, Q):
+    """The first sequence needs more columns than there are; the list holds three pages.  The
+    second and third get one and two, the fourth is refused for want of pages, and all that
+    need some behind it."""
+    BS, cols = 4, 3
+    table = torch.full((Q, cols), -1, dtype=torch.int32, device="cuda")
+    held, kept = i32([0] * Q), i32([0] * Q)
+    free, count = i32([7, 8, 9]), i32([3])
+    counts = [BS * cols + 1, 1, BS + 1, 1] + [1] * (Q - 4)
+    status = kvd.status_tensor()
+    lens, slots, pos = kvd.plan_pages(table, held, free, count, kept, i32(cum(counts)), BS,
+                                      sum(counts), dev_status=status)
+    assert int(status.item()) == kvd.DEV_TABLE_COLS | kvd.DEV_NO_PAGES
+    assert lens.tolist() == [0, 0, 1] + [2 + BS] * (Q - 2)
+    assert held.tolist() == [0, 1, 2] + [0] * (Q - 3) and int(count) == 0
+    assert table[1, 0].item() == 9 and table[2, :2].tolist() == [8, 7]
+    first = BS * cols + 1
+    assert slots.tolist() == [-1] * first + [36, 32, 33, 34, 35, 28] + [-1] * (Q - 3)
+    assert pos.tolist() == [-1] * first + [0, 0, 1, 2, 3, 4] + [-1] * (Q - 3)
+
+
+def test_what_was_refused_counts_against_those_behind(kvd):
+    """Two pages for sequences that need one, two and one: the second is refused, and the third,
+    though a page is left."""
+    status = kvd.status_tensor()
+    table = torch.full((3, 3), -1, dtype=torch.int32, device="cuda")
+    held, free, count = i32([0] * 3), i32([5, 6]), i32([2])
+    lens, _, _ = kvd.plan_pages(table, held, free, count, i32([0] * 3), i32([0, 1, 6, 7]), 4, 7,
+                                dev_status=status)
+    assert int(status.item()) == kvd.DEV_NO_PAGES
+    assert lens.tolist() == [0, 1, 1, 1] and held.tolist() == [1, 0, 0] and int(count) == 1
