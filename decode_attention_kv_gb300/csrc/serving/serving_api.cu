@@ -67,8 +67,11 @@ kvd_status prefix_plan(const char* fn, int Q, int G, int Hq, int Hkv, int BS, in
     if (D != 64 && D != 128)
         return fail(KVD_ERR_UNSUPPORTED, "%s: head_dim %d (supported: 64, 128)", fn, D);
     if (G > kMaxGroups) return fail(KVD_ERR_UNSUPPORTED, "%s: G > %d", fn, kMaxGroups);
-    if ((long long)cols * BS >= (1ll << 31) || (long long)pcols * BS >= (1ll << 31))
-        return fail(KVD_ERR_UNSUPPORTED, "%s: cols*BS or pcols*BS >= 2^31", fn);
+    if ((long long)cols * BS >= (1ll << 31))
+        return fail(KVD_ERR_UNSUPPORTED, "%s: cols*BS >= 2^31", fn);
+    // (a prefix's length is rounded up to whole tiles of at most 128 keys in 32 bits)
+    if ((long long)pcols * BS > (1ll << 31) - 128)
+        return fail(KVD_ERR_UNSUPPORTED, "%s: pcols*BS > 2^31 - 128", fn);
     if ((long long)Q * Hq > (1ll << 28)) return fail(KVD_ERR_UNSUPPORTED, "%s: Q*Hq > 2^28", fn);
     const int g = Hq / Hkv, n = Q < 1 ? 1 : Q;
     const bool mma = dt == KVD_BF16;

@@ -909,7 +909,7 @@ kvd_status kvd_rotate_append_paged(const void* qkv, const void* q_weight, const 
  * Workspace: at least kvd_attend_paged_prefix_workspace_bytes(...) bytes, 256-byte
  * aligned; its contents do not matter before a call, and calls that may overlap
  * on the GPU must not share one.  D in {64, 128}; any Hq multiple of Hkv;
- * G at most 1024.
+ * G at most 1024; pcols * BS at most 2^31 - 128.
  */
 size_t kvd_attend_paged_prefix_workspace_bytes(int Q, int G, int Hq, int Hkv, int BS, int pcols,
                                                int cols, int D, kvd_dtype dtype);
