@@ -402,7 +402,10 @@ prefix_mma_kernel(const PrefixArgs a, const int piece, const FastDiv by_page, co
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     // over scores that have been read: 16 columns hold 32 weights, rounded to
-                    // bf16 as the matrix unit takes them (2^-8 of each); their sum keeps fp32
+                    // bf16 as the matrix unit takes them beside bf16 values (2^-8 of each); their
+                    // sum keeps fp32.  (Two bf16 words a weight, the second one's product added:
+                    // bf16 outputs 1.7e-3 from 64 bits instead of 2.3e-3, but 64 sequences behind
+                    // 16384 tokens 65 us instead of 55.5, 8 37.1 instead of 30.3.)
                     float pk[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {

@@ -292,7 +292,10 @@ kvd_status kvd_attend_paged_prefix(const void* q, const void* key_cache, const v
         // A place costs 2.5 (1.75 alone, up to 4 while the sequences' own keys fill the queues
         // to memory): 64 sequences behind 16384 tokens with 64 to 1024 own ones 61, 58.4,
         // 57.7 and 59.8 us with 2, 2.5, 3 and 4; 256 behind 8192 with 16 to 256 70, 73, 77 and
-        // 77.  An SM's share of the memory's rate is 45000 bytes a microsecond.
+        // 77.  An SM's share of the memory's rate is 45000 bytes a microsecond.  (All at D = 128
+        // with two row tiles; D = 64 and one tile go by the same numbers.  own_units counts
+        // splits of the tables' width, empty ones among them: the first case with tables
+        // four times as wide as needed 69 us instead of 61.)
         a.place_cost = 2.5f;
         a.token_cost = (float)Hkv * D * 4 / 45000.f;
         a.own_units = (int)pl.own.units;

@@ -906,6 +906,12 @@ kvd_status kvd_rotate_append_paged(const void* qkv, const void* q_weight, const 
  * decreases or passes Q leaves every sequence without a prefix (KVD_DEV_SEQLENS).
  * A query without any key gives out = 0, lse = -inf.  Slots behind a prefix's or
  * a sequence's end may hold anything (inf, NaN).
+ * bf16: the weights of a prefix's keys are rounded to bf16 before they multiply the
+ * values (their sum keeps fp32), whatever Hq / Hkv; those of own keys as in
+ * kvd_attend_paged, which rounds them from three query heads a kv head on.
+ * Pays where a group's sequences times its prefix's tokens are above some 8000 (16000
+ * where the caches do not come from L2); below, kvd_attend_paged over tables that
+ * list the prefix's pages in front is up to 6 us faster.
  * Workspace: at least kvd_attend_paged_prefix_workspace_bytes(...) bytes, 256-byte
  * aligned; its contents do not matter before a call, and calls that may overlap
  * on the GPU must not share one.  D in {64, 128}; any Hq multiple of Hkv;
